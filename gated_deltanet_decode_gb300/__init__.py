@@ -10,6 +10,8 @@ decode path runs in the library's CUDA kernels.  The names follow the C ABI
   gdn_decode_step                gated delta rule per row and value head
   gdn_layer_decode               both in one kernel
   gdn_commit                     twin-slot commit (swap read/write slots)
+  attn_prologue, paged_attention, kv_pages_*   the attention layers beside the
+                                 GDN layers, over a paged cache (KVPagePool)
 
 The operation is the decode step of "mstar PR #1139" ("Why": the GDN rule is
 the recurrent state update of one token a row; "What changed": twin slots,
@@ -18,12 +20,13 @@ the decode-only conv), with padding on the null slot of "mstar PR #1127".
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional
 
 import torch
 
 from . import _lib
-from ._lib import (GDN_BF16, GDN_DEVERR_BAD_SLOT, GDN_DEVERR_NONE, GDN_DEVERR_TIMEOUT, GDN_F32,
+from ._lib import (GDN_BF16, GDN_DEVERR_BAD_PAGE, GDN_DEVERR_BAD_SLOT, GDN_DEVERR_NO_PAGES, GDN_DEVERR_NONE, GDN_DEVERR_TIMEOUT, GDN_F32,
                    GDN_NOALLOC_SCRATCH_SLOTS,
                    GDN_PROBE_INPLACE, GDN_PROBE_READ, GDN_PROBE_TWIN, GDN_PROBE_WRITE, gdn_dims)
 
@@ -604,3 +607,271 @@ def prepare_commit(read_slot: torch.Tensor, write_slot: torch.Tensor,
 
 
 __all__ += ["PreparedCall", "prepare_layer_decode", "prepare_commit"]
+
+
+# ---- attention layers over a paged cache ------------------------------------
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, scaling: Optional[dict] = None):
+    """(inverse frequencies [rot/2] as float64 on the CPU, mscale) of rotary positions.
+
+    scaling, for contexts longer than the model was trained on, is None or one of
+      {"type": "linear", "factor": f}    position interpolation: every frequency over f
+      {"type": "ntk", "factor": f}       base * f^(rot / (rot - 2)): the lowest frequency over f, the highest kept
+      {"type": "yarn", "factor": f, "original": n, "fast": 32, "slow": 1, "mscale": m}
+                                         frequencies that turn more than `fast` times in the n positions of training are
+                                         kept, those that turn less than `slow` times are taken over f, with a linear
+                                         ramp over the dimensions between; mscale (default 0.1 ln f + 1) scales the table
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and positive, got {rot}")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    kind = scaling.get("type") if scaling else None
+    f = float(scaling["factor"]) if scaling else 1.0
+    if f <= 0:
+        raise ValueError("the scaling factor must be positive")
+    if kind == "ntk" and rot > 2:
+        base = base * f ** (rot / (rot - 2))
+    freq = float(base) ** (-2.0 * i / rot)
+    if kind in (None, "ntk"):
+        return freq, 1.0
+    if kind == "linear":
+        return freq / f, 1.0
+    if kind != "yarn":
+        raise ValueError(f"unknown rotary scaling {kind!r}")
+    n = float(scaling["original"])
+
+    def dim(turns):  # the (real) index of the frequency that turns so often in n positions
+        return rot * math.log(n / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    lo = max(math.floor(dim(scaling.get("fast", 32))), 0)
+    hi = min(math.ceil(dim(scaling.get("slow", 1))), rot - 1)
+    ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    mscale = scaling.get("mscale")
+    if mscale is None:
+        mscale = 0.1 * math.log(f) + 1.0 if f > 1 else 1.0
+    return freq / f * ramp + freq * (1 - ramp), float(mscale)
+
+
+def rope_table(rot: int, positions: int, base: float = 10000.0, scaling: Optional[dict] = None, device=None) -> torch.Tensor:
+    """The rotation table [positions][rot] fp32 (cosines, then sines) that attn_prologue reads; made once for a model."""
+    device = torch.device(device if device is not None else "cuda")
+    freq, mscale = rope_inv_freq(rot, base, scaling)
+    freq = freq.to(device)
+    table = torch.empty((positions, rot), dtype=torch.float32, device=device)
+    with torch.cuda.device(device):
+        _check(_lib.load().rope_table(_ptr(freq, "inv_freq"), rot, positions, mscale, _ptr(table, "table"),
+                                      _stream(device)))
+    return table
+
+
+class KVPagePool:
+    """K and V of attention layers, each [layers][num_pages][hkv][page_size][d], in torch-owned memory (`k`, `v`).
+
+    Page 0 is the null page.  The library wraps the tensors (it never frees them)."""
+
+    def __init__(self, num_pages: int, page_size: int, hkv: int, d: int, layers: int = 1, dtype=torch.bfloat16,
+                 device=None, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
+        L = _lib.load()
+        shape = (layers, num_pages, hkv, page_size, d)
+        if (k is None) != (v is None):
+            raise ValueError("give both k and v, or neither")
+        if k is None:
+            device = torch.device(device if device is not None else "cuda")
+            k = torch.zeros(shape, dtype=dtype, device=device)
+            v = torch.zeros(shape, dtype=dtype, device=device)
+        if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != dtype or v.dtype != dtype:
+            raise ValueError("k and v must be [layers][num_pages][hkv][page_size][d] of the given dtype")
+        self.k, self.v, self.device = k, v, k.device
+        self.num_pages, self.page_size, self.hkv, self.d = num_pages, page_size, hkv, d
+        self.layers, self.dtype, self._code = layers, dtype, _dtype_code(dtype)
+        h = ctypes.c_void_p()
+        _check(L.kv_page_pool_wrap(_ptr(k, "k"), _ptr(v, "v", None, k.device), num_pages, page_size, layers, hkv, d,
+                                   self._code, ctypes.byref(h)))
+        self._h = h
+
+    @property
+    def handle(self):
+        return self._h
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            try:
+                _lib.load().kv_page_pool_destroy(h)
+            except Exception:
+                pass
+            self._h = None
+
+
+class KVPageMoves:
+    """Pages to copy, as kv_pages_fork and kv_pages_compact list them on the device: src[j] -> dst[j] for j < count[0]
+    (zeros past it).  `n` is the capacity: the forks, or the pool's pages.  `status` is 0 for every fork that was done."""
+
+    def __init__(self, n: int, device=None):
+        device = torch.device(device if device is not None else "cuda")
+        self.src = torch.zeros(n, dtype=torch.int32, device=device)
+        self.dst = torch.zeros(n, dtype=torch.int32, device=device)
+        self.count = torch.zeros(1, dtype=torch.int32, device=device)
+        self.status = torch.zeros(n, dtype=torch.int32, device=device)
+
+
+def _token_rows(x: torch.Tensor, heads: int, pool: KVPagePool, what: str) -> int:
+    """Token stride of x [T][heads][d], whose tokens may be apart but whose heads are dense."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != pool.d:
+        raise ValueError(f"{what} must be [tokens][{heads}][{pool.d}], got {tuple(x.shape)}")
+    st = x.stride()
+    if st[2] != 1 or (st[1] != pool.d and heads > 1):
+        raise ValueError(f"{what}: the heads of a token must be dense")
+    return st[0] if x.shape[0] > 1 else heads * pool.d
+
+
+def _table(table: torch.Tensor, what: str = "table"):
+    if table.dim() != 2:
+        raise ValueError(f"{what} must be [rows][max_pages]")
+    return table.shape
+
+
+def attn_prologue(q, k, v, pool: KVPagePool, rope: Optional[torch.Tensor], table, seq_len, cu_seqlens, layer: int = 0,
+                  q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  interleaved: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """RMS norm (optional) and rotary positions of q and k, and the append of k and v to the pages of each token's row.
+
+    q [T][hq][d], k, v [T][hkv][d] (views of a packed projection are fine); row r's tokens are cu_seqlens[r] ..
+    cu_seqlens[r+1], and seq_len[r] counts them already.  rope is a table of rope_table (its width says how much of a
+    head is rotated) or None.  Returns the rotated q, [T][hq][d]."""
+    dt, dev = pool.dtype, pool.device
+    T, hq = q.shape[0], q.shape[1]
+    rows, max_pages = _table(table)
+    qs, ks = _token_rows(q, hq, pool, "q"), _token_rows(k, pool.hkv, pool, "k")
+    vs = _token_rows(v, pool.hkv, pool, "v")
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must have as many tokens")
+    _numel(cu_seqlens, rows + 1, "cu_seqlens")
+    _numel(seq_len, rows, "seq_len")
+    for w, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _numel(w, pool.d, what)
+    if rope is not None and rope.dim() != 2:
+        raise ValueError("rope must be [positions][rot]")
+    if out is None:
+        out = torch.empty((T, hq, pool.d), dtype=dt, device=dev)
+    _numel(out, T * hq * pool.d, "out")
+    i32, f32 = torch.int32, torch.float32
+    _check(_lib.load().attn_prologue(
+        _ptr(q, "q", dt, dev, False), qs, _ptr(k, "k", dt, dev, False), ks, _ptr(v, "v", dt, dev, False), vs, pool._h,
+        layer, _ptr(rope, "rope", f32, dev), rope.shape[0] if rope is not None else 0,
+        rope.shape[1] if rope is not None else 0, int(bool(interleaved)), _ptr(q_norm, "q_norm", f32, dev),
+        _ptr(k_norm, "k_norm", f32, dev), eps, _ptr(table, "table", i32, dev), max_pages,
+        _ptr(seq_len, "seq_len", i32, dev), _ptr(cu_seqlens, "cu_seqlens", i32, dev), _ptr(out, "out", dt, dev), hq,
+        rows, T, pool._code, _stream(dev)))
+    return out
+
+
+def paged_attention_workspace_bytes(pool: KVPagePool, hq: int, rows: int, total_tokens: int) -> int:
+    """Bytes of the device workspace of paged_attention."""
+    return int(_lib.load().paged_attention_workspace_bytes(pool._h, int(hq), int(rows), int(total_tokens)))
+
+
+def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int = 0, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of new tokens (q [T][hq][d], rotated) over their rows' pages, the tokens' own keys included.
+
+    scale defaults to d^-1/2.  workspace is a uint8 tensor of paged_attention_workspace_bytes (allocated here when none
+    is given).  Returns [T][hq][d]."""
+    dt, dev = pool.dtype, pool.device
+    T, hq = q.shape[0], q.shape[1]
+    rows, max_pages = _table(table)
+    qs = _token_rows(q, hq, pool, "q")
+    _numel(cu_seqlens, rows + 1, "cu_seqlens")
+    _numel(seq_len, rows, "seq_len")
+    if out is None:
+        out = torch.empty((T, hq, pool.d), dtype=dt, device=dev)
+    _numel(out, T * hq * pool.d, "out")
+    L = _lib.load()
+    if workspace is None:
+        need = L.paged_attention_workspace_bytes(pool._h, hq, rows, T)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    i32 = torch.int32
+    _check(L.paged_attention(
+        _ptr(q, "q", dt, dev, False), qs, pool._h, layer, _ptr(table, "table", i32, dev), max_pages,
+        _ptr(seq_len, "seq_len", i32, dev), _ptr(cu_seqlens, "cu_seqlens", i32, dev),
+        pool.d ** -0.5 if scale is None else scale, _ptr(out, "out", dt, dev), hq, rows, T,
+        _ptr(workspace, "workspace", None, dev), nbytes, pool._code, _stream(dev)))
+    return out
+
+
+def kv_pages_reserve(table, refs, rows, tokens, page_size: int, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Give row rows[i] of the table the pages for tokens[i] tokens in all.  Returns status (0 where done)."""
+    trows, max_pages = _table(table)
+    dev, n, i32 = table.device, rows.numel(), torch.int32
+    _numel(tokens, n, "tokens")
+    if status is None:
+        status = torch.empty(n, dtype=i32, device=dev)
+    _numel(status, n, "status")
+    _check(_lib.load().kv_pages_reserve(
+        _ptr(table, "table", i32), trows, max_pages, _ptr(refs, "refs", i32, dev), refs.numel(), page_size,
+        _ptr(rows, "rows", i32, dev), _ptr(tokens, "tokens", i32, dev), n, _ptr(status, "status", i32, dev),
+        _stream(dev)))
+    return status
+
+
+def kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size: int, moves: KVPageMoves) -> KVPageMoves:
+    """Make the empty rows dst_rows copies of src_rows: full pages are shared, partial last pages get a free page each,
+    whose copies are listed in `moves` (then kv_pages_copy(pool, moves))."""
+    trows, max_pages = _table(table)
+    dev, n, i32 = table.device, src_rows.numel(), torch.int32
+    _numel(dst_rows, n, "dst_rows")
+    _numel(seq_len, trows, "seq_len")
+    _numel(moves.src, n, "moves")
+    _check(_lib.load().kv_pages_fork(
+        _ptr(table, "table", i32), trows, max_pages, _ptr(seq_len, "seq_len", i32, dev), _ptr(refs, "refs", i32, dev),
+        refs.numel(), page_size, _ptr(src_rows, "src_rows", i32, dev), _ptr(dst_rows, "dst_rows", i32, dev), n,
+        _ptr(moves.src, "moves", i32, dev), _ptr(moves.dst, "moves", i32, dev), _ptr(moves.count, "moves", i32, dev),
+        _ptr(moves.status, "moves", i32, dev), _stream(dev)))
+    return moves
+
+
+def kv_pages_free(table, seq_len, refs, rows) -> None:
+    """Give up the pages of the listed rows and set their lengths to 0."""
+    trows, max_pages = _table(table)
+    dev, i32 = table.device, torch.int32
+    _numel(seq_len, trows, "seq_len")
+    _check(_lib.load().kv_pages_free(
+        _ptr(table, "table", i32), trows, max_pages, _ptr(seq_len, "seq_len", i32, dev), _ptr(refs, "refs", i32, dev),
+        refs.numel(), _ptr(rows, "rows", i32, dev), rows.numel(), _stream(dev)))
+
+
+def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.Tensor] = None,
+                     refs_out: Optional[torch.Tensor] = None, remap: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Renumber the pages in use to the lowest numbers, in place or into table_out and refs_out; the copies are listed
+    in `moves` (of as many entries as the pool has pages), then kv_pages_copy(pool, moves).  Returns remap: each page's
+    new number, 0 for a free page."""
+    trows, max_pages = _table(table)
+    dev, i32, n = table.device, torch.int32, refs.numel()
+    table_out = table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    remap = torch.empty(n, dtype=i32, device=dev) if remap is None else remap
+    _numel(table_out, table.numel(), "table_out")
+    for x, what in ((refs_out, "refs_out"), (remap, "remap"), (moves.src, "moves")):
+        _numel(x, n, what)
+    _check(_lib.load().kv_pages_compact(
+        _ptr(table, "table", i32), trows, max_pages, _ptr(refs, "refs", i32, dev), n,
+        _ptr(table_out, "table_out", i32, dev), _ptr(refs_out, "refs_out", i32, dev), _ptr(remap, "remap", i32, dev),
+        _ptr(moves.src, "moves", i32, dev), _ptr(moves.dst, "moves", i32, dev), _ptr(moves.count, "moves", i32, dev),
+        _ptr(moves.status, "moves", i32, dev), _stream(dev)))
+    return remap
+
+
+def kv_pages_copy(pool: KVPagePool, moves: KVPageMoves) -> None:
+    """Copy the listed pages, K and V of all layers."""
+    dev, i32 = pool.device, torch.int32
+    _check(_lib.load().kv_pages_copy(
+        pool._h, _ptr(moves.src, "moves", i32, dev), _ptr(moves.dst, "moves", i32, dev), moves.src.numel(),
+        _ptr(moves.count, "moves", i32, dev), _stream(dev)))
+
+
+__all__ += ["rope_inv_freq", "rope_table", "KVPagePool", "KVPageMoves", "attn_prologue",
+            "paged_attention", "paged_attention_workspace_bytes", "kv_pages_reserve", "kv_pages_fork", "kv_pages_free",
+            "kv_pages_compact", "kv_pages_copy", "GDN_DEVERR_BAD_PAGE", "GDN_DEVERR_NO_PAGES"]

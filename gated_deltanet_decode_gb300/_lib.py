@@ -21,6 +21,8 @@ GDN_ESLOTS = 5
 GDN_DEVERR_NONE = 0
 GDN_DEVERR_BAD_SLOT = 1
 GDN_DEVERR_TIMEOUT = 2
+GDN_DEVERR_BAD_PAGE = 3
+GDN_DEVERR_NO_PAGES = 4
 
 GDN_F32 = 0
 GDN_BF16 = 1
@@ -32,6 +34,7 @@ GDN_PROBE_WRITE = 3
 
 GDN_MAX_POOLS = 4096
 GDN_NOALLOC_SCRATCH_SLOTS = 64
+GDN_MAX_PAGE_ROWS = 4096
 
 # Every symbol the header declares (the export test checks this list against
 # include/gdn_decode.h).
@@ -46,6 +49,9 @@ EXPORTS = [
     "gdn_layer_decode_noalloc", "gdn_layer_decode_bucket", "gdn_prefill", "gdn_prefill_chunked", "gdn_prefill_chunked_workspace_bytes", "gdn_verify", "causal_conv1d_prefill",
     "gdn_commit", "gdn_validate_slots", "gdn_get_device_error", "gdn_selftest_wait_timeout",
     "gdn_probe_traffic",
+    "kv_page_pool_create", "kv_page_pool_wrap", "kv_page_pool_destroy", "kv_page_pool_k", "kv_page_pool_v",
+    "kv_page_pool_num_pages", "rope_table", "attn_prologue", "paged_attention_workspace_bytes", "paged_attention",
+    "kv_pages_reserve", "kv_pages_fork", "kv_pages_free", "kv_pages_compact", "kv_pages_copy",
 ]
 
 
@@ -55,6 +61,7 @@ class gdn_dims(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
 _SIGS = {
@@ -96,6 +103,23 @@ _SIGS = {
     "gdn_get_device_error": (_I, [ctypes.POINTER(ctypes.c_int), _P]),
     "gdn_probe_traffic": (_I, [_P, _P, _P, _I, _I, _P, _P]),
     "gdn_selftest_wait_timeout": (_I, [_I, _P]),
+    "kv_page_pool_create": (_I, [_I, _I, _I, _I, _I, _I, _P, _PP]),
+    "kv_page_pool_wrap": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _PP]),
+    "kv_page_pool_destroy": (_I, [_P]),
+    "kv_page_pool_k": (_P, [_P]),
+    "kv_page_pool_v": (_P, [_P]),
+    "kv_page_pool_num_pages": (_I, [_P]),
+    "rope_table": (_I, [_P, _I, _I, ctypes.c_double, _P, _P]),
+    "attn_prologue": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _P, _I, _I, _I, _P, _P, ctypes.c_float, _P, _I, _P, _P, _P,
+                           _I, _I, _I, _I, _P]),
+    "paged_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
+    "paged_attention": (_I, [_P, _L, _P, _I, _P, _I, _P, _P, ctypes.c_float, _P, _I, _I, _I, _P, ctypes.c_size_t, _I,
+                             _P]),
+    "kv_pages_reserve": (_I, [_P, _I, _I, _P, _I, _I, _P, _P, _I, _P, _P]),
+    "kv_pages_fork": (_I, [_P, _I, _I, _P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "kv_pages_free": (_I, [_P, _I, _I, _P, _P, _I, _P, _I, _P]),
+    "kv_pages_compact": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "kv_pages_copy": (_I, [_P, _P, _P, _I, _P, _P]),
 }
 
 _lock = threading.Lock()

@@ -87,6 +87,22 @@ int device_error_ptr(int **out)
 
 } // namespace
 
+namespace gdn {
+
+int api_fail(int code, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_msg, sizeof t_msg, fmt, ap);
+    va_end(ap);
+    return code;
+}
+int api_ok() { return ok(); }
+int api_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+int api_error_word(int **out) { return device_error_ptr(out); }
+
+} // namespace gdn
+
 // ---------------------------------------------------------------------------
 // Work counters of the state kernels.  Each state pool handle holds one pair
 // (the next unit to claim, producers done) in this table, handed out on the

@@ -27,7 +27,21 @@ struct conv_pool {
     bool owned;
 };
 
+struct kv_page_pool {
+    void *k, *v; // each [layers][num_pages][hkv][page_size][d]
+    int num_pages, page_size, layers, hkv, d, dtype;
+    bool owned;
+};
+
 namespace gdn {
+
+// The C ABI's error state, for its other translation units: set the calling
+// thread's message and return the code; clear it (GDN_OK); report a failed
+// runtime call; find the current device's error word.
+int api_fail(int code, const char *fmt, ...);
+int api_ok();
+int api_cuda_fail(cudaError_t e, const char *what);
+int api_error_word(int **out);
 
 // Everything one launch of the state kernels needs.  Pointers are device
 // pointers; layouts as in gdn_decode.h.
@@ -100,6 +114,53 @@ struct ConvPrefillArgs {
     int *err;
 };
 
+// One layer of a page pool, for a kernel.
+struct PageView {
+    void *k, *v; // the layer's [num_pages][hkv][page_size][d]
+    int num_pages, page_size, page_shift, hkv, d;
+};
+
+// New tokens of cache rows: row r's are [cu_seqlens[r], cu_seqlens[r+1]).
+struct CacheRows {
+    const int32_t *table;
+    const int32_t *seq_len, *cu_seqlens;
+    int max_pages, rows, total_tokens;
+};
+
+struct PrologueArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride; // elements a token
+    PageView pages;
+    CacheRows c;
+    const float *rope;
+    int rope_positions, rot, interleaved;
+    const float *q_norm, *k_norm;
+    float eps;
+    void *q_out;
+    int hq;
+    int *err;
+};
+
+struct AttentionArgs {
+    const void *q;
+    long long q_stride;
+    PageView pages;
+    CacheRows c;
+    float scale;
+    void *out;
+    int hq;
+    void *work;
+    int *err;
+};
+
+struct PageTables {
+    int32_t *table;
+    int table_rows, max_pages;
+    int32_t *seq_len, *refs;
+    int num_pages, page_size;
+    int *err;
+};
+
 // Launchers return cudaSuccess or the launch error.  Shapes were validated by
 // the caller.
 cudaError_t launch_gdn_step(const StepArgs &a, int dtype, cudaStream_t s);
@@ -113,6 +174,24 @@ cudaError_t launch_gdn_prefill_chunked(const PrefillArgs &a, int dtype, cudaStre
 cudaError_t launch_gdn_prefill_chunked_tc(const PrefillArgs &a, cudaStream_t s);
 // Bytes of the workspace the bf16 chunked prefill needs (0 for no sequence).
 size_t prefill_chunked_workspace_bytes(int nseq, int total_tokens, int hv);
+
+// Attention layers over a page pool.
+cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table,
+                              cudaStream_t s);
+cudaError_t launch_attn_prologue(const PrologueArgs &a, int dtype, cudaStream_t s);
+size_t attention_workspace_bytes(int d, int dtype, int hq, int hkv, int rows, int total_tokens);
+cudaError_t launch_paged_attention(const AttentionArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_pages_reserve(const PageTables &t, const int32_t *list_rows, const int32_t *tokens, int n,
+                                 int32_t *status, cudaStream_t s);
+cudaError_t launch_pages_fork(const PageTables &t, const int32_t *src_rows, const int32_t *dst_rows, int n,
+                              int32_t *move_src, int32_t *move_dst, int32_t *move_count, int32_t *status,
+                              cudaStream_t s);
+cudaError_t launch_pages_free(const PageTables &t, const int32_t *list_rows, int n, cudaStream_t s);
+cudaError_t launch_pages_compact(const PageTables &t, int32_t *table_out, int32_t *refs_out, int32_t *remap,
+                                 int32_t *move_src, int32_t *move_dst, int32_t *move_count, int32_t *scratch,
+                                 cudaStream_t s);
+cudaError_t launch_pages_copy(const kv_page_pool &pool, const int32_t *src, const int32_t *dst, int n,
+                              const int32_t *count, int *err, cudaStream_t s);
 
 // True when the state kernels are built for (dk, dv).
 bool step_shape_supported(int dk, int dv);

@@ -89,9 +89,12 @@ extern "C" {
 #define GDN_DEVERR_NONE 0
 #define GDN_DEVERR_BAD_SLOT 1 /* some row named a slot outside the pool */
 #define GDN_DEVERR_TIMEOUT 2  /* a bounded wait inside a kernel ran out; its CTA stopped */
+#define GDN_DEVERR_BAD_PAGE 3 /* a cache row's length, position, page or reference count is out of range */
+#define GDN_DEVERR_NO_PAGES 4 /* a page pool had too few free pages for a fork or a reservation */
 
 /* ---- limits ------------------------------------------------------------ */
 #define GDN_MAX_POOLS 4096 /* state pool handles alive at once, per process */
+#define GDN_MAX_PAGE_ROWS 4096 /* rows in one fork or reservation */
 
 /* ---- activation dtypes ------------------------------------------------ */
 #define GDN_F32 0
@@ -380,6 +383,130 @@ int gdn_layer_decode_noalloc(const void *x, conv_pool *cp, const void *w, const 
  * Twin-slot commit: swap read_slot[r] and write_slot[r] for every row, on the
  * device ("mstar PR #1139", "What changed": commit swaps them). */
 int gdn_commit(int32_t *read_slot, int32_t *write_slot, int rows, void *stream);
+
+/* ---- attention layers over a paged cache -------------------------------- *
+ * The layers of a hybrid decoder that are not GDN layers attend over a cache
+ * of keys and values.  The pages name their work ("mstar PR #1139", "What
+ * changed": the packed attention prologue, q/k norm, rotary positions and the
+ * cache write in one kernel; "mstar PR #1127", "What changed": block tables
+ * and lengths that stay on the device); the layout and the kernels here are
+ * the library's own.
+ *
+ * A page pool holds K and V, each [layers][num_pages][hkv][page_size][d] in
+ * the activation dtype, d contiguous.  page_size is 16, 32, 64 or 128; d is
+ * 64, 128 or 256.  Page 0 is the null page: never written, never read as a
+ * key.  The tables are shared by all layers:
+ *   table    [rows][max_pages] int32: row r's pages in order, then zeros
+ *   seq_len  [rows] int32: tokens a row holds; 0 is a padding row
+ *   refs     [num_pages] int32: how many table entries name a page; 0 is free
+ *            (refs[0] is not used)
+ * A row that has more pages than its tokens need has them in reserve. */
+typedef struct kv_page_pool kv_page_pool;
+
+/* Create allocates and zero-fills (GDN_ENOMEM when the device is full); wrap
+ * adopts caller memory, 16-byte aligned, and makes no CUDA call; destroy
+ * frees what create allocated, after the pool's last launch has finished. */
+int kv_page_pool_create(int num_pages, int page_size, int layers, int hkv, int d, int dtype, void *stream,
+                        kv_page_pool **out);
+int kv_page_pool_wrap(void *k, void *v, int num_pages, int page_size, int layers, int hkv, int d, int dtype,
+                      kv_page_pool **out);
+int kv_page_pool_destroy(kv_page_pool *pool);
+void *kv_page_pool_k(const kv_page_pool *pool);
+void *kv_page_pool_v(const kv_page_pool *pool);
+int kv_page_pool_num_pages(const kv_page_pool *pool);
+
+/* rope_table: rotation table [positions][rot] fp32, a row being rot/2 cosines
+ * then rot/2 sines: cos(p inv_freq[i]) mscale, sin(p inv_freq[i]) mscale, with
+ * the angle and the functions in 64 bits.  inv_freq [rot/2] is device memory,
+ * fp64; scaling for long contexts is in inv_freq and mscale (rope_inv_freq of
+ * the Python package).  rot is a multiple of 16. */
+int rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table, void *stream);
+
+/* attn_prologue: for every new token, q and k normalised (optional), rotated,
+ * and k and v appended to the row's pages.  New tokens are packed: row r's
+ * are cu_seqlens[r] .. cu_seqlens[r+1] (cu_seqlens [rows+1] int32, from 0,
+ * non-decreasing, ending at total_tokens), and seq_len[r] counts them
+ * already: token i of n sits at position p = seq_len[r] - n + i.  Per head x:
+ *   y  = w * x / sqrt(mean(x^2) + eps)      (w = q_norm or k_norm; NULL: y = x)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)   with row p of `rope`
+ *        and the pairs (i, i + rot/2), or (2i, 2i+1) when interleaved != 0;
+ *        dimensions from rot on are left alone; rot 0 rotates nothing
+ * in fp32, rounded once.  q_out[t] receives q's; page table[r][p/page_size],
+ * slot p % page_size receives k's and v.
+ *   q [T][hq][d], k, v [T][hkv][d]: token strides in elements (at least
+ *   heads*d; a token's heads are dense), base and strides 16-byte multiples
+ *   q_out [T][hq][d], dense    rope [rope_positions][rot] fp32
+ *   q_norm, k_norm [d] fp32 or NULL
+ * Padding rows' tokens get zero q_out and write nothing.  So do, with
+ * GDN_DEVERR_BAD_PAGE, tokens outside every row, of a row shorter than its
+ * new tokens, past the rotation table, or on a page outside [1, num_pages). */
+int attn_prologue(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                  kv_page_pool *pool, int layer, const float *rope, int rope_positions, int rot, int interleaved,
+                  const float *q_norm, const float *k_norm, float eps, const int32_t *table, int max_pages,
+                  const int32_t *seq_len, const int32_t *cu_seqlens, void *q_out, int hq, int rows,
+                  int total_tokens, int dtype, void *stream);
+
+/* paged_attention: causal attention of every new token over its row's cache.
+ * Token i of row r's n sees the seq_len[r] - n + i + 1 keys up to its own:
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . K[j][h / (hq/hkv)]) V[j][h / (hq/hkv)]
+ * Softmax statistics and sums are fp32; in bf16 the weights are rounded to
+ * bf16 for the product with V.  One new token a row is decode; more are a
+ * prefill chunk or a verification; rows may differ.
+ *   q [T][hq][d]: token stride q_stride as in attn_prologue; out [T][hq][d],
+ *   dense, 16-byte aligned; scale finite and positive
+ *   workspace: device memory, 16-byte aligned, at least
+ *   paged_attention_workspace_bytes(...) bytes, its contents without meaning
+ *   before and after; calls that overlap on the GPU need their own
+ * Keys past seq_len are never used, whatever their bits.  Padding rows give
+ * zeros.  With GDN_DEVERR_BAD_PAGE, zeros are given by the tokens of a row
+ * that is shorter than its new tokens or longer than max_pages pages, and by
+ * tokens that would see a key on a page outside [1, num_pages). */
+size_t paged_attention_workspace_bytes(const kv_page_pool *pool, int hq, int rows, int total_tokens);
+int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int layer, const int32_t *table,
+                    int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens, float scale, void *out, int hq,
+                    int rows, int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream);
+
+/* Pages of rows, on the device.  Free pages are taken lowest first, for the
+ * listed rows in order.  `list_rows` (n of them) are distinct row numbers
+ * below table_rows; n is at most GDN_MAX_PAGE_ROWS.  status[i] is 0 where
+ * entry i was done, else the device error that it raised, and the row is as
+ * it was.  A launch of these must not overlap another that uses the same
+ * tables.
+ *
+ * kv_pages_reserve: gives row list_rows[i] the pages for tokens[i] tokens in
+ * all; a row that has them keeps what it has.
+ * kv_pages_fork: makes row dst_rows[i], which must hold no page, a copy of
+ * row src_rows[i] (sources may repeat; none is a destination): full pages are
+ * shared, and a partial last page is replaced by a free one.  The pages to
+ * copy, (move_src[j], move_dst[j]) for j < *move_count, are then for
+ * kv_pages_copy; the lists hold n entries, zero past the count.  A row is not
+ * to be cut back below the length at which it was forked.
+ * kv_pages_free: gives up all pages of the listed rows and sets their lengths
+ * to 0.
+ * kv_pages_compact: renumbers the L pages in use (the null page among them)
+ * to 0 .. L-1: those below L stay, and the others, in order, go to the free
+ * numbers below L, in order.  remap[p] is page p's new number (0 for a free
+ * page); the moves are listed as by kv_pages_fork, in lists of num_pages
+ * entries, and have to be copied (kv_pages_copy) before a page is next read
+ * or written.  table_out and refs_out may be table and refs themselves.
+ * scratch holds num_pages int32.  Table entries outside [0, num_pages) become
+ * 0, with GDN_DEVERR_BAD_PAGE.
+ * kv_pages_copy: for all layers, K and V, page dst[j] receives page src[j],
+ * for j < n, and j < *count where count is given.  Pairs (0, 0) are skipped;
+ * destinations are distinct and no sources.  A page outside [1, num_pages)
+ * skips the pair, with GDN_DEVERR_BAD_PAGE. */
+int kv_pages_reserve(int32_t *table, int table_rows, int max_pages, int32_t *refs, int num_pages, int page_size,
+                     const int32_t *list_rows, const int32_t *tokens, int n, int32_t *status, void *stream);
+int kv_pages_fork(int32_t *table, int table_rows, int max_pages, int32_t *seq_len, int32_t *refs, int num_pages,
+                  int page_size, const int32_t *src_rows, const int32_t *dst_rows, int n, int32_t *move_src,
+                  int32_t *move_dst, int32_t *move_count, int32_t *status, void *stream);
+int kv_pages_free(int32_t *table, int table_rows, int max_pages, int32_t *seq_len, int32_t *refs, int num_pages,
+                  const int32_t *list_rows, int n, void *stream);
+int kv_pages_compact(const int32_t *table, int table_rows, int max_pages, const int32_t *refs, int num_pages,
+                     int32_t *table_out, int32_t *refs_out, int32_t *remap, int32_t *move_src, int32_t *move_dst,
+                     int32_t *move_count, int32_t *scratch, void *stream);
+int kv_pages_copy(kv_page_pool *pool, const int32_t *src, const int32_t *dst, int n, const int32_t *count,
+                  void *stream);
 
 /* ---- debugging --------------------------------------------------------- *
  * gdn_validate_slots copies the tables to the host (synchronising `stream`)
