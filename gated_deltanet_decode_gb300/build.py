@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgdn_decode.so")
 SOURCES = ["gdn_api.cu", "gdn_stream.cu", "gdn_conv.cu", "gdn_prefill.cu", "gdn_chunked.cu", "gdn_chunked_tc.cu",
-           "kv_api.cu", "kv_pages.cu", "attn_prologue.cu", "attn_paged.cu"]
+           "kv_api.cu", "kv_pages.cu", "attn_prologue.cu", "attn_paged.cu", "attn_tc.cu"]
 HEADERS = [os.path.join(CSRC, "gdn_device.cuh"), os.path.join(CSRC, "gdn_ptx.cuh"),
            os.path.join(CSRC, "gdn_chunk_common.cuh"),
            os.path.join(CSRC, "gdn_internal.h"),

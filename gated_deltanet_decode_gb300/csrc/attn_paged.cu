@@ -109,10 +109,15 @@ template <typename T> cudaError_t by_d(const AttentionArgs &a, cudaStream_t s)
 
 } // namespace
 
-size_t attention_workspace_bytes(int, int, int, int, int, int) { return 0; }
+size_t attention_workspace_bytes(int d, int dtype, int hq, int hkv, int, int total_tokens)
+{
+    return dtype == GDN_BF16 && attention_tc_supported(hq, hkv) ? attention_tc_workspace_bytes(d, hq, hkv, total_tokens) : 0;
+}
 
 cudaError_t launch_paged_attention(const AttentionArgs &a, int dtype, cudaStream_t s)
 {
+    if (dtype == GDN_BF16 && attention_tc_supported(a.hq, a.pages.hkv))
+        return launch_paged_attention_tc(a, s);
     return dtype == GDN_BF16 ? by_d<__nv_bfloat16>(a, s) : by_d<float>(a, s);
 }
 
