@@ -715,21 +715,48 @@ class KVPageMoves:
         self.count = torch.zeros(1, dtype=torch.int32, device=device)
         self.status = torch.zeros(n, dtype=torch.int32, device=device)
 
+    def _pointers(self, n: int, dev: torch.device):
+        i32 = torch.int32
+        return (_arg(self.src, n, i32, dev, "moves"), _arg(self.dst, n, i32, dev, "moves"),
+                _arg(self.count, 1, i32, dev, "moves"))
 
-def _token_rows(x: torch.Tensor, heads: int, pool: KVPagePool, what: str) -> int:
-    """Token stride of x [T][heads][d], whose tokens may be apart but whose heads are dense."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != pool.d:
-        raise ValueError(f"{what} must be [tokens][{heads}][{pool.d}], got {tuple(x.shape)}")
-    st = x.stride()
+
+# A decode step makes a few of these calls a layer, each of some microseconds on the GPU: the helpers below look at a
+# tensor once, and only then at what is wrong with it.
+
+
+def _raw_stream(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _arg(t: Optional[torch.Tensor], n: int, dtype, dev: torch.device, what: str):
+    """Device pointer of a contiguous tensor of n elements (or None)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.device == dev and t.is_contiguous() and t.numel() == n:
+        return t.data_ptr()
+    _numel(t, n, what)
+    return _ptr(t, what, dtype, dev)
+
+
+def _token_rows(x: torch.Tensor, tokens: int, heads: int, pool: KVPagePool, what: str):
+    """Device pointer and token stride of x [tokens][heads][d], whose tokens may be apart but whose heads are dense."""
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or shape[2] != pool.d:
+        raise ValueError(f"{what} must be [{tokens}][{heads}][{pool.d}], got {tuple(shape)}")
     if st[2] != 1 or (st[1] != pool.d and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be dense")
-    return st[0] if x.shape[0] > 1 else heads * pool.d
+    if x.dtype is not pool.dtype or x.device != pool.device:
+        _ptr(x, what, pool.dtype, pool.device, False)
+    return x.data_ptr(), st[0] if tokens > 1 else heads * pool.d
 
 
-def _table(table: torch.Tensor, what: str = "table"):
-    if table.dim() != 2:
+def _table(table: torch.Tensor, dev: torch.device, what: str = "table"):
+    """Device pointer, rows and width of a page table."""
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be [rows][max_pages]")
-    return table.shape
+    return _arg(table, shape[0] * shape[1], torch.int32, dev, what), shape[0], shape[1]
 
 
 def attn_prologue(q, k, v, pool: KVPagePool, rope: Optional[torch.Tensor], table, seq_len, cu_seqlens, layer: int = 0,
@@ -740,31 +767,24 @@ def attn_prologue(q, k, v, pool: KVPagePool, rope: Optional[torch.Tensor], table
     q [T][hq][d], k, v [T][hkv][d] (views of a packed projection are fine); row r's tokens are cu_seqlens[r] ..
     cu_seqlens[r+1], and seq_len[r] counts them already.  rope is a table of rope_table (its width says how much of a
     head is rotated) or None.  Returns the rotated q, [T][hq][d]."""
-    dt, dev = pool.dtype, pool.device
-    T, hq = q.shape[0], q.shape[1]
-    rows, max_pages = _table(table)
-    qs, ks = _token_rows(q, hq, pool, "q"), _token_rows(k, pool.hkv, pool, "k")
-    vs = _token_rows(v, pool.hkv, pool, "v")
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v must have as many tokens")
-    _numel(cu_seqlens, rows + 1, "cu_seqlens")
-    _numel(seq_len, rows, "seq_len")
-    for w, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _numel(w, pool.d, what)
-    if rope is not None and rope.dim() != 2:
-        raise ValueError("rope must be [positions][rot]")
+    dev, d, hkv, i32, f32 = pool.device, pool.d, pool.hkv, torch.int32, torch.float32
+    T, hq = q.shape[:2]
+    tab, rows, max_pages = _table(table, dev)
+    qp, qs = _token_rows(q, T, hq, pool, "q")
+    kp, ks = _token_rows(k, T, hkv, pool, "k")
+    vp, vs = _token_rows(v, T, hkv, pool, "v")
+    positions = rot = 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope must be [positions][rot]")
+        positions, rot = rope.shape
     if out is None:
-        out = torch.empty((T, hq, pool.d), dtype=dt, device=dev)
-    _numel(out, T * hq * pool.d, "out")
-    i32, f32 = torch.int32, torch.float32
+        out = torch.empty((T, hq, d), dtype=pool.dtype, device=dev)
     _check(_lib.load().attn_prologue(
-        _ptr(q, "q", dt, dev, False), qs, _ptr(k, "k", dt, dev, False), ks, _ptr(v, "v", dt, dev, False), vs, pool._h,
-        layer, _ptr(rope, "rope", f32, dev), rope.shape[0] if rope is not None else 0,
-        rope.shape[1] if rope is not None else 0, int(bool(interleaved)), _ptr(q_norm, "q_norm", f32, dev),
-        _ptr(k_norm, "k_norm", f32, dev), eps, _ptr(table, "table", i32, dev), max_pages,
-        _ptr(seq_len, "seq_len", i32, dev), _ptr(cu_seqlens, "cu_seqlens", i32, dev), _ptr(out, "out", dt, dev), hq,
-        rows, T, pool._code, _stream(dev)))
+        qp, qs, kp, ks, vp, vs, pool._h, layer, _arg(rope, positions * rot, f32, dev, "rope"), positions, rot,
+        1 if interleaved else 0, _arg(q_norm, d, f32, dev, "q_norm"), _arg(k_norm, d, f32, dev, "k_norm"), eps, tab,
+        max_pages, _arg(seq_len, rows, i32, dev, "seq_len"), _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"),
+        _arg(out, T * hq * d, pool.dtype, dev, "out"), hq, rows, T, pool._code, _raw_stream(dev)))
     return out
 
 
@@ -779,68 +799,59 @@ def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int 
 
     scale defaults to d^-1/2.  workspace is a uint8 tensor of paged_attention_workspace_bytes (allocated here when none
     is given).  Returns [T][hq][d]."""
-    dt, dev = pool.dtype, pool.device
-    T, hq = q.shape[0], q.shape[1]
-    rows, max_pages = _table(table)
-    qs = _token_rows(q, hq, pool, "q")
-    _numel(cu_seqlens, rows + 1, "cu_seqlens")
-    _numel(seq_len, rows, "seq_len")
+    dev, d, i32 = pool.device, pool.d, torch.int32
+    T, hq = q.shape[:2]
+    tab, rows, max_pages = _table(table, dev)
+    qp, qs = _token_rows(q, T, hq, pool, "q")
     if out is None:
-        out = torch.empty((T, hq, pool.d), dtype=dt, device=dev)
-    _numel(out, T * hq * pool.d, "out")
+        out = torch.empty((T, hq, d), dtype=pool.dtype, device=dev)
     L = _lib.load()
     if workspace is None:
         need = L.paged_attention_workspace_bytes(pool._h, hq, rows, T)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    i32 = torch.int32
     _check(L.paged_attention(
-        _ptr(q, "q", dt, dev, False), qs, pool._h, layer, _ptr(table, "table", i32, dev), max_pages,
-        _ptr(seq_len, "seq_len", i32, dev), _ptr(cu_seqlens, "cu_seqlens", i32, dev),
-        pool.d ** -0.5 if scale is None else scale, _ptr(out, "out", dt, dev), hq, rows, T,
-        _ptr(workspace, "workspace", None, dev), nbytes, pool._code, _stream(dev)))
+        qp, qs, pool._h, layer, tab, max_pages, _arg(seq_len, rows, i32, dev, "seq_len"),
+        _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"), d ** -0.5 if scale is None else scale,
+        _arg(out, T * hq * d, pool.dtype, dev, "out"), hq, rows, T, _ptr(workspace, "workspace", None, dev), nbytes,
+        pool._code, _raw_stream(dev)))
     return out
 
 
 def kv_pages_reserve(table, refs, rows, tokens, page_size: int, status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Give row rows[i] of the table the pages for tokens[i] tokens in all.  Returns status (0 where done)."""
-    trows, max_pages = _table(table)
     dev, n, i32 = table.device, rows.numel(), torch.int32
-    _numel(tokens, n, "tokens")
+    tab, trows, max_pages = _table(table, dev)
     if status is None:
         status = torch.empty(n, dtype=i32, device=dev)
-    _numel(status, n, "status")
+    pages = refs.numel()
     _check(_lib.load().kv_pages_reserve(
-        _ptr(table, "table", i32), trows, max_pages, _ptr(refs, "refs", i32, dev), refs.numel(), page_size,
-        _ptr(rows, "rows", i32, dev), _ptr(tokens, "tokens", i32, dev), n, _ptr(status, "status", i32, dev),
-        _stream(dev)))
+        tab, trows, max_pages, _arg(refs, pages, i32, dev, "refs"), pages, page_size, _arg(rows, n, i32, dev, "rows"),
+        _arg(tokens, n, i32, dev, "tokens"), n, _arg(status, n, i32, dev, "status"), _raw_stream(dev)))
     return status
 
 
 def kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size: int, moves: KVPageMoves) -> KVPageMoves:
     """Make the empty rows dst_rows copies of src_rows: full pages are shared, partial last pages get a free page each,
     whose copies are listed in `moves` (then kv_pages_copy(pool, moves))."""
-    trows, max_pages = _table(table)
     dev, n, i32 = table.device, src_rows.numel(), torch.int32
-    _numel(dst_rows, n, "dst_rows")
-    _numel(seq_len, trows, "seq_len")
-    _numel(moves.src, n, "moves")
+    tab, trows, max_pages = _table(table, dev)
+    pages = refs.numel()
     _check(_lib.load().kv_pages_fork(
-        _ptr(table, "table", i32), trows, max_pages, _ptr(seq_len, "seq_len", i32, dev), _ptr(refs, "refs", i32, dev),
-        refs.numel(), page_size, _ptr(src_rows, "src_rows", i32, dev), _ptr(dst_rows, "dst_rows", i32, dev), n,
-        _ptr(moves.src, "moves", i32, dev), _ptr(moves.dst, "moves", i32, dev), _ptr(moves.count, "moves", i32, dev),
-        _ptr(moves.status, "moves", i32, dev), _stream(dev)))
+        tab, trows, max_pages, _arg(seq_len, trows, i32, dev, "seq_len"), _arg(refs, pages, i32, dev, "refs"), pages,
+        page_size, _arg(src_rows, n, i32, dev, "src_rows"), _arg(dst_rows, n, i32, dev, "dst_rows"), n,
+        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"), _raw_stream(dev)))
     return moves
 
 
 def kv_pages_free(table, seq_len, refs, rows) -> None:
     """Give up the pages of the listed rows and set their lengths to 0."""
-    trows, max_pages = _table(table)
-    dev, i32 = table.device, torch.int32
-    _numel(seq_len, trows, "seq_len")
+    dev, n, i32 = table.device, rows.numel(), torch.int32
+    tab, trows, max_pages = _table(table, dev)
+    pages = refs.numel()
     _check(_lib.load().kv_pages_free(
-        _ptr(table, "table", i32), trows, max_pages, _ptr(seq_len, "seq_len", i32, dev), _ptr(refs, "refs", i32, dev),
-        refs.numel(), _ptr(rows, "rows", i32, dev), rows.numel(), _stream(dev)))
+        tab, trows, max_pages, _arg(seq_len, trows, i32, dev, "seq_len"), _arg(refs, pages, i32, dev, "refs"), pages,
+        _arg(rows, n, i32, dev, "rows"), n, _raw_stream(dev)))
 
 
 def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.Tensor] = None,
@@ -848,28 +859,23 @@ def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.
     """Renumber the pages in use to the lowest numbers, in place or into table_out and refs_out; the copies are listed
     in `moves` (of as many entries as the pool has pages), then kv_pages_copy(pool, moves).  Returns remap: each page's
     new number, 0 for a free page."""
-    trows, max_pages = _table(table)
     dev, i32, n = table.device, torch.int32, refs.numel()
-    table_out = table if table_out is None else table_out
-    refs_out = refs if refs_out is None else refs_out
+    tab, trows, max_pages = _table(table, dev)
     remap = torch.empty(n, dtype=i32, device=dev) if remap is None else remap
-    _numel(table_out, table.numel(), "table_out")
-    for x, what in ((refs_out, "refs_out"), (remap, "remap"), (moves.src, "moves")):
-        _numel(x, n, what)
+    refp = _arg(refs, n, i32, dev, "refs")
     _check(_lib.load().kv_pages_compact(
-        _ptr(table, "table", i32), trows, max_pages, _ptr(refs, "refs", i32, dev), n,
-        _ptr(table_out, "table_out", i32, dev), _ptr(refs_out, "refs_out", i32, dev), _ptr(remap, "remap", i32, dev),
-        _ptr(moves.src, "moves", i32, dev), _ptr(moves.dst, "moves", i32, dev), _ptr(moves.count, "moves", i32, dev),
-        _ptr(moves.status, "moves", i32, dev), _stream(dev)))
+        tab, trows, max_pages, refp, n,
+        tab if table_out is None else _arg(table_out, trows * max_pages, i32, dev, "table_out"),
+        refp if refs_out is None else _arg(refs_out, n, i32, dev, "refs_out"), _arg(remap, n, i32, dev, "remap"),
+        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"), _raw_stream(dev)))
     return remap
 
 
 def kv_pages_copy(pool: KVPagePool, moves: KVPageMoves) -> None:
     """Copy the listed pages, K and V of all layers."""
-    dev, i32 = pool.device, torch.int32
-    _check(_lib.load().kv_pages_copy(
-        pool._h, _ptr(moves.src, "moves", i32, dev), _ptr(moves.dst, "moves", i32, dev), moves.src.numel(),
-        _ptr(moves.count, "moves", i32, dev), _stream(dev)))
+    dev, n = pool.device, moves.src.numel()
+    src, dst, count = moves._pointers(n, dev)
+    _check(_lib.load().kv_pages_copy(pool._h, src, dst, n, count, _raw_stream(dev)))
 
 
 __all__ += ["rope_inv_freq", "rope_table", "KVPagePool", "KVPageMoves", "attn_prologue",

@@ -114,10 +114,10 @@ size_t attention_workspace_bytes(int d, int dtype, int hq, int hkv, int, int tot
     return dtype == GDN_BF16 && attention_tc_supported(hq, hkv) ? attention_tc_workspace_bytes(d, hq, hkv, total_tokens) : 0;
 }
 
-cudaError_t launch_paged_attention(const AttentionArgs &a, int dtype, cudaStream_t s)
+cudaError_t launch_paged_attention(const AttentionArgs &a, kv_page_pool &pool, int dtype, cudaStream_t s)
 {
     if (dtype == GDN_BF16 && attention_tc_supported(a.hq, a.pages.hkv))
-        return launch_paged_attention_tc(a, s);
+        return launch_paged_attention_tc(a, pool, s);
     return dtype == GDN_BF16 ? by_d<__nv_bfloat16>(a, s) : by_d<float>(a, s);
 }
 

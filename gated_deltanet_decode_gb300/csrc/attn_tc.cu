@@ -539,7 +539,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                         const uint32_t dst = stage_addr(st) + i * box * 128;
 #pragma unroll
                         for (int c = 0; c < G::CH; ++c)
-                            tma3(dst + c * KT * 128, is_v ? &vmap : &kmap, 64 * c, key & (ps - 1), page * hkv + it.head, b);
+                            tma3(dst + c * KT * 128, is_v ? &vmap : &kmap, 64 * c, key & (ps - 1),
+                                 (a.pages.layer * a.pages.num_pages + page) * hkv + it.head, b);
                     }
                     __syncwarp();
                     ++issued;
@@ -988,17 +989,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled()
     return fn;
 }
 
-// one layer's K or V as [pages x heads][page_size][d], boxes of 64 d x `box` keys
-bool encode_pages(CUtensorMap *m, const void *base, const PageView &v, int box)
+// a pool's K or V as [layers x pages x heads][page_size][d], boxes of 64 d x `box` keys
+bool encode_pages(CUtensorMap *m, void *base, const kv_page_pool &v, int box)
 {
     const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
     if (!fn)
         return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)v.d, (cuuint64_t)v.page_size, (cuuint64_t)v.num_pages * v.hkv};
+    const cuuint64_t dims[3] = {(cuuint64_t)v.d, (cuuint64_t)v.page_size, (cuuint64_t)v.layers * v.num_pages * v.hkv};
     const cuuint64_t strides[2] = {(cuuint64_t)v.d * 2, (cuuint64_t)v.page_size * v.d * 2};
     const cuuint32_t boxes[3] = {64u, (cuuint32_t)box, 1u};
     const cuuint32_t step[3] = {1u, 1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxes, step,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, boxes, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1011,7 +1012,7 @@ int slot_rows(int d, int g, int total_tokens)
     return 128 + one; // a pair of tiles, the second's rows from 128 on
 }
 
-template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
+template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s)
 {
     typedef Geo<D> G;
     static_assert(G::TOTAL <= 232448, "shared memory");
@@ -1035,13 +1036,16 @@ template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
     p.cuts = static_cast<Cut *>(a.work);
     p.part_ml = reinterpret_cast<float2 *>(p.cuts + kCtas);
     p.part_o = reinterpret_cast<float *>(p.part_ml + 2 * (size_t)kCtas * p.rows_max);
-    CUtensorMap kmap, vmap;
-    memset(&kmap, 0, sizeof kmap);
-    memset(&vmap, 0, sizeof vmap);
-    const int box = a.pages.page_size < G::KT ? a.pages.page_size : G::KT;
-    if (!encode_pages(&kmap, a.pages.k, a.pages, box) || !encode_pages(&vmap, a.pages.v, a.pages, box))
-        return cudaErrorInvalidValue;
-    e = launch_pdl(attn_tc_kernel<D>, dim3(kCtas), dim3(G::THREADS), (size_t)G::TOTAL, s, p, kmap, vmap);
+    {
+        const std::lock_guard<std::mutex> lk(pool.map_mutex);
+        const int box = pool.page_size < G::KT ? pool.page_size : G::KT;
+        if (!pool.mapped) {
+            if (!encode_pages(&pool.kmap, pool.k, pool, box) || !encode_pages(&pool.vmap, pool.v, pool, box))
+                return cudaErrorInvalidValue;
+            pool.mapped = true;
+        }
+    }
+    e = launch_pdl(attn_tc_kernel<D>, dim3(kCtas), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(attn_combine_kernel<D>, dim3(kCtas, p.rows_max > 32 ? 8 : 1), dim3(128), 0, s, p);
@@ -1057,15 +1061,15 @@ size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens)
     return sizeof(Cut) * kCtas + 2 * (size_t)kCtas * rows * (sizeof(float2) + sizeof(float) * d);
 }
 
-cudaError_t launch_paged_attention_tc(const AttentionArgs &a, cudaStream_t s)
+cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s)
 {
     switch (a.pages.d) {
     case 64:
-        return go<64>(a, s);
+        return go<64>(a, pool, s);
     case 128:
-        return go<128>(a, s);
+        return go<128>(a, pool, s);
     default:
-        return go<256>(a, s);
+        return go<256>(a, pool, s);
     }
 }
 

@@ -2,8 +2,11 @@
 // translation units.  Not part of the public ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "../../include/gdn_decode.h"
 
@@ -31,6 +34,15 @@ struct kv_page_pool {
     void *k, *v; // each [layers][num_pages][hkv][page_size][d]
     int num_pages, page_size, layers, hkv, d, dtype;
     bool owned;
+    // tensor maps of k and v for paged_attention, made by its first call
+    std::mutex map_mutex;
+    bool mapped;
+    CUtensorMap kmap, vmap;
+    kv_page_pool(void *k_, void *v_, int pages, int size, int layers_, int hkv_, int d_, int dtype_, bool owned_)
+        : k(k_), v(v_), num_pages(pages), page_size(size), layers(layers_), hkv(hkv_), d(d_), dtype(dtype_),
+          owned(owned_), mapped(false)
+    {
+    }
 };
 
 namespace gdn {
@@ -117,7 +129,7 @@ struct ConvPrefillArgs {
 // One layer of a page pool, for a kernel.
 struct PageView {
     void *k, *v; // the layer's [num_pages][hkv][page_size][d]
-    int num_pages, page_size, page_shift, hkv, d;
+    int num_pages, page_size, page_shift, hkv, d, layer;
 };
 
 // New tokens of cache rows: row r's are [cu_seqlens[r], cu_seqlens[r+1]).
@@ -180,11 +192,11 @@ cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, do
                               cudaStream_t s);
 cudaError_t launch_attn_prologue(const PrologueArgs &a, int dtype, cudaStream_t s);
 size_t attention_workspace_bytes(int d, int dtype, int hq, int hkv, int rows, int total_tokens);
-cudaError_t launch_paged_attention(const AttentionArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_paged_attention(const AttentionArgs &a, kv_page_pool &pool, int dtype, cudaStream_t s);
 // bf16 on the tensor cores: up to 128 query heads a key head
 bool attention_tc_supported(int hq, int hkv);
 size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens);
-cudaError_t launch_paged_attention_tc(const AttentionArgs &a, cudaStream_t s);
+cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s);
 cudaError_t launch_pages_reserve(const PageTables &t, const int32_t *list_rows, const int32_t *tokens, int n,
                                  int32_t *status, cudaStream_t s);
 cudaError_t launch_pages_fork(const PageTables &t, const int32_t *src_rows, const int32_t *dst_rows, int n,

@@ -28,8 +28,8 @@ int check_pool_geometry(int num_pages, int page_size, int layers, int hkv, int d
         return api_fail(GDN_EUNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", page_size);
     if (d != 64 && d != 128 && d != 256)
         return api_fail(GDN_EUNSUPPORTED, "d=%d (64, 128 or 256)", d);
-    if ((long long)num_pages * hkv > 0x7fffffffll)
-        return api_fail(GDN_EUNSUPPORTED, "num_pages * hkv = %lld is over 2^31 - 1", (long long)num_pages * hkv);
+    if ((double)num_pages * hkv * layers > 2147483647.0)
+        return api_fail(GDN_EUNSUPPORTED, "layers * num_pages * hkv is over 2^31 - 1");
     return GDN_OK;
 }
 
@@ -50,6 +50,7 @@ gdn::PageView view(const kv_page_pool *p, int layer)
         ++v.page_shift;
     v.hkv = p->hkv;
     v.d = p->d;
+    v.layer = layer;
     return v;
 }
 
@@ -117,7 +118,7 @@ int kv_page_pool_wrap(void *k, void *v, int num_pages, int page_size, int layers
     int rc = check_pool_geometry(num_pages, page_size, layers, hkv, d, dtype);
     if (rc)
         return rc;
-    *out = new (std::nothrow) kv_page_pool{k, v, num_pages, page_size, layers, hkv, d, dtype, false};
+    *out = new (std::nothrow) kv_page_pool(k, v, num_pages, page_size, layers, hkv, d, dtype, false);
     return *out ? api_ok() : api_fail(GDN_ENOMEM, "no host memory for a page pool handle");
 }
 
@@ -130,7 +131,7 @@ int kv_page_pool_create(int num_pages, int page_size, int layers, int hkv, int d
     int rc = check_pool_geometry(num_pages, page_size, layers, hkv, d, dtype);
     if (rc)
         return rc;
-    kv_page_pool *p = new (std::nothrow) kv_page_pool{nullptr, nullptr, num_pages, page_size, layers, hkv, d, dtype, true};
+    kv_page_pool *p = new (std::nothrow) kv_page_pool(nullptr, nullptr, num_pages, page_size, layers, hkv, d, dtype, true);
     if (!p)
         return api_fail(GDN_ENOMEM, "no host memory for a page pool handle");
     const size_t bytes = layer_bytes(p) * layers;
@@ -268,7 +269,7 @@ int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int lay
     a.pages = view(pool, layer);
     a.c = {table, seq_len, cu_seqlens, max_pages, rows, total_tokens};
     a.scale = scale, a.out = out, a.hq = hq, a.work = workspace;
-    return launched(gdn::launch_paged_attention(a, dtype, static_cast<cudaStream_t>(stream)),
+    return launched(gdn::launch_paged_attention(a, *pool, dtype, static_cast<cudaStream_t>(stream)),
                     "paged_attention launch");
 }
 
