@@ -1,0 +1,361 @@
+// Attention of new tokens over a paged cache in fp32 (sm_103a).
+//
+// Products run on the tensor cores in tf32 (mma.sync m16n8k8) with both
+// operands split in a head and a tail, x = hi + lo, and three products hi hi +
+// hi lo + lo hi: what is dropped is about 2^-22 of a term, as much as an fp32
+// product's own rounding.  One tf32 product (2^-11) would not do, and tcgen05
+// takes its operands from shared memory, where every head and tail would have
+// to be written first.  Sums, weights and statistics are fp32.
+//
+// Rows (token, head) are packed as in the bf16 kernel, 16 WR a tile; 8 warps
+// stand as WR row blocks of 16 x WK shares of a tile's keys.  Few rows (decode)
+// take WR small and split the keys instead.  Each warp keeps its own O, m and
+// l; the shares are joined through shared memory at the item's end.  K and V
+// tiles come by 16-byte asynchronous copies, one tile ahead.
+//
+// A weight of zero does not hide a NaN or an infinity, and infinity has no
+// tail: elements of V that are not finite are left out of the products, and
+// the item's end adds them to the rows that see them.
+#include "attn_plan.cuh"
+
+#include <atomic>
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int D> struct Geo32 {
+    static constexpr int KT = D == 256 ? 32 : 64;  // keys a tile
+    static constexpr int LD = D + 4;               // row stride: fragment reads hit 32 banks
+    static constexpr int WRB = D == 256 ? 4 : 8;   // row blocks with many rows,
+    static constexpr int WRS = D == 256 ? 2 : 1;   // and with up to 16 WRS rows
+    static constexpr int M = 16 * WRB;
+    static constexpr int TILE = KT * LD;           // floats of a K or V tile
+    static constexpr int FLOATS = M * LD + 4 * TILE;
+};
+
+struct Ctrl32 {
+    long long scan[kThreads / 32], found[2];
+    Item item;
+    int more, broken, dirty;
+    float2 ml[8 * 16]; // (m, l) by (share, row): 128 pairs in every form
+};
+
+__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
+{
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    lo = __float_as_uint(x - __uint_as_float(hi)); // the product reads its leading 11 bits
+}
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool there) // zeros where it is not there
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// One warp's keys kb .. kb + 8 NT of a tile, rows g and g + 8 of its block
+// (g = lane / 4, c = lane % 4).  Fragments: A (row g, k c), (g + 8, c), (g, c +
+// 4), (g + 8, c + 4); B (k c, n g), (c + 4, g); D (g, 2c), (g, 2c + 1), (g + 8,
+// 2c), (g + 8, 2c + 1).  P V names key 2c as its k = c and key 2c + 1 as k = c +
+// 4, so the weights are an A fragment as they stand.
+template <int D, int NT>
+__device__ __forceinline__ void tile_step(const float *q, const float *k, const float *v, int see0, int see8, float c2,
+                                          float (&o)[D / 8][4], float &m0, float &m8, float &l0, float &l8, bool &odd)
+{
+    constexpr int LD = Geo32<D>::LD;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    constexpr int CHAINS = NT == 1 ? 2 : 1; // a single column tile: two sums, for latency
+    float s[NT][CHAINS][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < CHAINS; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[n][h][e] = 0.f;
+#pragma unroll 4
+    for (int ks = 0; ks < D / 8; ++ks) {
+        const float *qp = q + g * LD + 8 * ks + c;
+        uint32_t ah[4], al[4];
+        split(qp[0], ah[0], al[0]);
+        split(qp[8 * LD], ah[1], al[1]);
+        split(qp[4], ah[2], al[2]);
+        split(qp[8 * LD + 4], ah[3], al[3]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float *kp = k + (8 * n + g) * LD + 8 * ks + c;
+            uint32_t h0, h1, t0, t1;
+            split(kp[0], h0, t0);
+            split(kp[4], h1, t1);
+            float(&d)[4] = s[n][CHAINS == 2 ? ks & 1 : 0];
+            mma8(d, al, h0, h1);
+            mma8(d, ah, t0, t1);
+            mma8(d, ah, h0, h1);
+        }
+    }
+    // weights 2^(c2 (s - m))
+    float top0 = m0, top8 = m8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (CHAINS == 2) {
+                s[n][0][e] += s[n][CHAINS - 1][e];
+                s[n][0][e + 2] += s[n][CHAINS - 1][e + 2];
+            }
+            const int at = 8 * n + 2 * c + e;
+            s[n][0][e] = at < see0 ? s[n][0][e] : -INFINITY;
+            s[n][0][e + 2] = at < see8 ? s[n][0][e + 2] : -INFINITY;
+            top0 = fmaxf(top0, s[n][0][e]);
+            top8 = fmaxf(top8, s[n][0][e + 2]);
+        }
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, x));
+        top8 = fmaxf(top8, __shfl_xor_sync(0xffffffffu, top8, x));
+    }
+    const float z0 = top0 == -INFINITY ? 0.f : -top0 * c2, z8 = top8 == -INFINITY ? 0.f : -top8 * c2;
+    const float f0 = m0 == -INFINITY ? 0.f : ex2(fmaf(m0, c2, z0)), f8 = m8 == -INFINITY ? 0.f : ex2(fmaf(m8, c2, z8));
+    m0 = top0, m8 = top8;
+    l0 *= f0, l8 *= f8;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+        o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f8, o[n][3] *= f8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float p0 = ex2(fmaf(s[n][0][0], c2, z0)), p1 = ex2(fmaf(s[n][0][1], c2, z0));
+        const float p2 = ex2(fmaf(s[n][0][2], c2, z8)), p3 = ex2(fmaf(s[n][0][3], c2, z8));
+        l0 += p0 + p1, l8 += p2 + p3;
+        uint32_t ah[4], al[4];
+        split(p0, ah[0], al[0]);
+        split(p2, ah[1], al[1]);
+        split(p1, ah[2], al[2]);
+        split(p3, ah[3], al[3]);
+        const float *vp = v + (8 * n + 2 * c) * LD + g;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+            float x = vp[8 * e], y = vp[8 * e + LD];
+            const bool fx = fabsf(x) < INFINITY, fy = fabsf(y) < INFINITY;
+            odd |= !fx | !fy;
+            x = fx ? x : 0.f, y = fy ? y : 0.f;
+            uint32_t h0, h1, t0, t1;
+            split(x, h0, t0);
+            split(y, h1, t1);
+            mma8(o[e], al, h0, h1);
+            mma8(o[e], ah, t0, t1);
+            mma8(o[e], ah, h0, h1);
+        }
+    }
+}
+
+template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const WorkArgs p)
+{
+    typedef Geo32<D> G;
+    constexpr int KT = G::KT, LD = G::LD;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ Ctrl32 ctl;
+    float *const Q = sm, *const ring = sm + G::M * LD;
+    const AttentionArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int ps = a.pages.page_size, hkv = a.pages.hkv;
+    const float c2 = a.scale * 1.44269504088896341f;
+    wait_prior_grid();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Run run = plan_run<kThreads, KT>(p, p.tq, ctl.scan, ctl.found);
+    zero_dead<float, D, kThreads>(p);
+    Walk walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
+    for (;;) {
+        __syncthreads();
+        if (warp == 0) {
+            Item next;
+            const bool more = walk.next(next);
+            if (lane == 0) {
+                ctl.item = next;
+                ctl.more = more, ctl.broken = 0x7fffffff, ctl.dirty = 0;
+            }
+        }
+        __syncthreads();
+        if (!ctl.more)
+            break;
+        const Item it = ctl.item;
+        const int32_t *const table = a.c.table + (size_t)it.row * a.c.max_pages;
+        const int kvh = it.head / p.groups, rows = it.ntok * p.g, end = it.see + it.ntok - 1;
+        const bool few = rows <= 16 * G::WRS;
+        const int wr_n = few ? G::WRS : G::WRB, wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n;
+        // Q: token rows of this head group
+        {
+            const float *const src = static_cast<const float *>(a.q) + (size_t)it.tok * a.q_stride + (size_t)it.head * p.g * D;
+            for (int x = tid; x < 16 * wr_n * (D / 4); x += kThreads) {
+                const int row = x / (D / 4), vec = x - row * (D / 4), t = row / p.g;
+                const bool there = row < rows;
+                copy16(Q + row * LD + 4 * vec, there ? src + (size_t)t * a.q_stride + (row - t * p.g) * D + 4 * vec : src, there);
+            }
+        }
+        auto load = [&](int j) {
+            float *const K = ring + (j & 1) * 2 * G::TILE, *const V = K + G::TILE;
+            for (int x = tid; x < KT * (D / 4); x += kThreads) {
+                const int row = x / (D / 4), vec = x - row * (D / 4), key = (it.ja + j) * KT + row;
+                int page = 0;
+                if (key < end) {
+                    page = table[key >> a.pages.page_shift];
+                    if (page <= 0 || page >= a.pages.num_pages) {
+                        page = 0;
+                        atomicMin(&ctl.broken, key);
+                        report(a.err, GDN_DEVERR_BAD_PAGE);
+                    }
+                }
+                const size_t at = (((size_t)page * hkv + kvh) * ps + (key & (ps - 1))) * D + 4 * vec;
+                copy16(K + row * LD + 4 * vec, static_cast<const float *>(a.pages.k) + at, page > 0);
+                copy16(V + row * LD + 4 * vec, static_cast<const float *>(a.pages.v) + at, page > 0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        const int r0 = 16 * wr + g, r8 = r0 + 8;
+        const int s0 = r0 < rows ? it.see + r0 / p.g : 0, s8 = r8 < rows ? it.see + r8 / p.g : 0; // keys the rows see
+        float o[D / 8][4], m0 = -INFINITY, m8 = -INFINITY, l0 = 0.f, l8 = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        const int n = it.jb - it.ja;
+        load(0);
+        for (int j = 0; j < n; ++j) {
+            if (j + 1 < n) {
+                load(j + 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncthreads();
+            if (16 * wr < rows) {
+                const int kb = wk * (KT / wk_n), key = (it.ja + j) * KT + kb;
+                const float *const K = ring + (j & 1) * 2 * G::TILE + kb * LD, *const V = K + G::TILE;
+                if (few)
+                    tile_step<D, KT * G::WRS / 64>(Q + 16 * wr * LD, K, V, s0 - key, s8 - key, c2, o, m0, m8, l0, l8, odd);
+                else
+                    tile_step<D, KT * G::WRB / 64>(Q + 16 * wr * LD, K, V, s0 - key, s8 - key, c2, o, m0, m8, l0, l8, odd);
+            }
+            __syncthreads();
+        }
+        // the shares' sums to shared memory, in place of the tiles
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+            l8 += __shfl_xor_sync(0xffffffffu, l8, x);
+        }
+        float *const mine = ring + (size_t)(wk * 16 * wr_n + r0) * LD;
+        if (16 * wr < rows) {
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) {
+                *reinterpret_cast<float2 *>(mine + 8 * e + 2 * c) = make_float2(o[e][0], o[e][1]);
+                *reinterpret_cast<float2 *>(mine + 8 * LD + 8 * e + 2 * c) = make_float2(o[e][2], o[e][3]);
+            }
+            if (c == 0)
+                ctl.ml[wk * 16 * wr_n + r0] = make_float2(m0, l0), ctl.ml[wk * 16 * wr_n + r8] = make_float2(m8, l8);
+            if (odd)
+                ctl.dirty = 1;
+        }
+        __syncthreads();
+        const float NaN = __int_as_float(0x7fc00000);
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), col = 4 * (x - row * (D / 4)), t = row / p.g, see = it.see + t;
+            const bool bad = see > ctl.broken;
+            float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int w = 0; w < wk_n; ++w)
+                m = fmaxf(m, ctl.ml[w * 16 * wr_n + row].x);
+            for (int w = 0; w < wk_n; ++w) {
+                const float2 s = ctl.ml[w * 16 * wr_n + row];
+                const float f = s.x == -INFINITY ? 0.f : ex2((s.x - m) * c2);
+                const float4 z = *reinterpret_cast<const float4 *>(ring + (size_t)(w * 16 * wr_n + row) * LD + col);
+                l = fmaf(s.y, f, l);
+                y[0] = fmaf(z.x, f, y[0]), y[1] = fmaf(z.y, f, y[1]), y[2] = fmaf(z.z, f, y[2]), y[3] = fmaf(z.w, f, y[3]);
+            }
+            if (ctl.dirty && !bad) {
+                for (int key = it.ja * KT; key < min(see, it.jb * KT); ++key) {
+                    const float *const v = static_cast<const float *>(a.pages.v) +
+                                           (((size_t)table[key >> a.pages.page_shift] * hkv + kvh) * ps + (key & (ps - 1))) * D + col;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!isfinite(v[e]))
+                            y[e] += v[e];
+                }
+            }
+            if (it.part >= 0) {
+                *reinterpret_cast<float4 *>(p.part_o + ((size_t)it.part * p.rows_max + row) * D + col) =
+                    make_float4(y[0], y[1], y[2], y[3]);
+                if (col == 0)
+                    p.part_ml[(size_t)it.part * p.rows_max + row] = make_float2(bad ? NaN : m, l);
+            } else {
+                const float i = 1.f / l;
+                float *const out = static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + it.head * p.g + (row - t * p.g)) * D + col;
+                *reinterpret_cast<float4 *>(out) =
+                    bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[0] * i, y[1] * i, y[2] * i, y[3] * i);
+            }
+        }
+    }
+}
+
+int slot_rows32(int m, int g, int total_tokens)
+{
+    const int tq = m / g;
+    return (total_tokens < tq ? total_tokens : tq) * g;
+}
+
+template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
+{
+    typedef Geo32<D> G;
+    static_assert(G::FLOATS * 4 + sizeof(Ctrl32) <= 232448, "shared memory");
+    static std::atomic<unsigned long long> configured{0}; // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::FLOATS * 4);
+        if (e != cudaSuccess)
+            return e;
+        configured.fetch_or(bit, std::memory_order_release);
+    }
+    WorkArgs p;
+    p.a = a;
+    p.g = group_heads(a.hq, a.pages.hkv, G::M);
+    p.groups = a.hq / a.pages.hkv / p.g;
+    p.tq = G::M / p.g;
+    p.rows_max = slot_rows32(G::M, p.g, a.c.total_tokens);
+    p.second = 0;
+    work_layout(p);
+    e = launch_pdl(attn_f32_kernel<D>, dim3(kCtas), dim3(kThreads), (size_t)G::FLOATS * 4, s, p);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(attn_combine_kernel<float, D>, dim3(kCtas, p.rows_max > 32 ? 8 : 1), dim3(128), 0, s, p);
+}
+
+} // namespace
+
+size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens)
+{
+    const int m = d == 256 ? Geo32<256>::M : Geo32<128>::M;
+    return work_bytes(d, slot_rows32(m, group_heads(hq, hkv, m), total_tokens));
+}
+
+cudaError_t launch_paged_attention_f32(const AttentionArgs &a, cudaStream_t s)
+{
+    switch (a.pages.d) {
+    case 64:
+        return go<64>(a, s);
+    case 128:
+        return go<128>(a, s);
+    default:
+        return go<256>(a, s);
+    }
+}
+
+} // namespace gdn

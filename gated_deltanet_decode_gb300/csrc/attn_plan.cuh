@@ -1,0 +1,334 @@
+// How the attention kernels over a paged cache divide their work (sm_103a),
+// and how the parts of a divided item are joined.
+//
+// An item is one key head (or a share of its query heads, where it has more
+// than a tile holds) and up to `mt` consecutive new tokens of a cache row; its
+// keys come in tiles of KT.  All items' key tiles, in order, are cut into equal
+// runs, one a CTA: every CTA finds its run from the lengths on the device.
+// Included by one translation unit a kernel; everything here has internal
+// linkage.
+#pragma once
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kCtas = 152; // runs: one CTA an SM
+
+struct Item {
+    int tok, ntok, head, row; // first token, tokens, head group, cache row
+    int see;                  // keys the first token sees; one more each token on
+    int ja, jb;               // key tiles of this run
+    int part;                 // workspace slot of a cut item, or -1
+};
+
+// One cut item, for the combining kernel: written by the run that holds the
+// item's second part.
+struct Cut {
+    int parts, tok, ntok, head;
+};
+
+// A call's arguments with its division.  Query heads are taken g at a time
+// (head groups of one key head); a tile holds tq tokens of a group.
+struct WorkArgs {
+    AttentionArgs a;
+    int g, groups, tq; // heads a group, groups a key head, tokens a tile
+    int rows_max;      // rows of a workspace slot
+    int second;        // rows before an item's second tile (0: items have one tile)
+    float *part_o;     // [2 kCtas][rows_max][D]
+    float2 *part_ml;
+    Cut *cuts;         // [kCtas]
+};
+
+// The workspace: cuts, then (m, l) and O of the cut items' parts.
+inline size_t work_bytes(int d, int rows_max)
+{
+    return sizeof(Cut) * kCtas + 2 * (size_t)kCtas * rows_max * (sizeof(float2) + sizeof(float) * d);
+}
+inline void work_layout(WorkArgs &p)
+{
+    p.cuts = static_cast<Cut *>(p.a.work);
+    p.part_ml = reinterpret_cast<float2 *>(p.cuts + kCtas);
+    p.part_o = reinterpret_cast<float *>(p.part_ml + 2 * (size_t)kCtas * p.rows_max);
+}
+// Heads a group: the largest divisor of hq / hkv that a tile of `rows` rows holds.
+inline int group_heads(int hq, int hkv, int rows)
+{
+    const int all = hq / hkv;
+    int g = all < rows ? all : rows;
+    while (all % g)
+        --g;
+    return g;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A cache row's work: its tokens [b, b + n) and length, live when it is a real
+// row whose table can hold it.
+struct Row {
+    int b, n, len;
+    bool live, bad;
+};
+__device__ __forceinline__ Row row_of(const CacheRows &c, int page_size, int r)
+{
+    Row x;
+    x.b = c.cu_seqlens[r];
+    const int e = c.cu_seqlens[r + 1];
+    x.len = c.seq_len[r];
+    x.n = 0;
+    x.live = x.bad = false;
+    if (x.b < 0 || e < x.b || e > c.total_tokens) {
+        x.bad = true;
+    } else {
+        x.n = e - x.b;
+        x.bad = x.n > 0 && (x.len < 0 || (x.len > 0 && (x.len < x.n || x.len > c.max_pages * page_size)));
+        x.live = x.n > 0 && x.len > 0 && !x.bad;
+    }
+    return x;
+}
+// Key tiles of the row's item t (mt tokens an item).
+__device__ __forceinline__ int item_tiles(const Row &x, int t, int mt, int kt)
+{
+    const int last = min(x.n, (t + 1) * mt);
+    return (x.len - x.n + last + kt - 1) / kt;
+}
+__device__ __forceinline__ int items_of(const Row &x, int mt) { return (x.n + mt - 1) / mt; }
+__device__ long long head_tiles(const Row &x, int mt, int kt) // of one key head
+{
+    long long s = 0;
+    const int n = items_of(x, mt);
+    for (int t = 0; t < n; ++t)
+        s += item_tiles(x, t, mt, kt);
+    return s;
+}
+
+// Exclusive sum over the CTA's threads; `part` is one long long a warp, and one.
+__device__ __forceinline__ long long scan64(long long v, long long *part, int warps, long long &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o)
+            s += x;
+    }
+    if (lane == 31)
+        part[warp] = s;
+    __syncthreads();
+    long long before = s - v;
+    total = 0;
+    for (int w = 0; w < warps; ++w) {
+        const long long x = part[w];
+        if (w < warp)
+            before += x;
+        total += x;
+    }
+    __syncthreads();
+    return before;
+}
+
+// This CTA's run of the units (key tiles) 0 .. total: [u0, u1), beginning in
+// `row`, whose units begin at `base`.  Called by the whole CTA; `part` is a
+// long long a warp, and `found` the place where one thread leaves the row.
+struct Run {
+    long long share, u0, u1, base;
+    int row;
+};
+template <int THREADS, int KT>
+__device__ Run plan_run(const WorkArgs &p, int mt, long long *part, volatile long long *found)
+{
+    const CacheRows &c = p.a.c;
+    const int ps = p.a.pages.page_size, heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
+    auto cost_of = [&](int r, bool first) -> long long {
+        if (r >= c.rows)
+            return 0;
+        const Row x = row_of(c, ps, r);
+        if (first && x.bad && blockIdx.x == 0)
+            report(p.a.err, GDN_DEVERR_BAD_PAGE);
+        return x.live ? head_tiles(x, mt, KT) * heads : 0;
+    };
+    Run run;
+    long long total = 0;
+    for (int b = 0; b < c.rows; b += THREADS) {
+        long long sum;
+        scan64(cost_of(b + tid, true), part, THREADS / 32, sum);
+        total += sum;
+    }
+    run.share = (total + gridDim.x - 1) / gridDim.x;
+    if (run.share < 1)
+        run.share = 1;
+    run.u0 = run.share * blockIdx.x;
+    run.u1 = min(total, run.u0 + run.share);
+    long long seen = 0;
+    for (int b = 0; b < c.rows && seen <= run.u0 && run.u0 < total; b += THREADS) {
+        long long sum;
+        const long long cost = cost_of(b + tid, false);
+        const long long before = seen + scan64(cost, part, THREADS / 32, sum);
+        if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
+            found[0] = b + tid, found[1] = before;
+        seen += sum;
+    }
+    __syncthreads();
+    run.row = (int)found[0];
+    run.base = found[1];
+    return run;
+}
+
+// Zeros for the outputs of tokens that no live row has, by all CTAs together.
+template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkArgs &p)
+{
+    const CacheRows &c = p.a.c;
+    const size_t vecs = (size_t)p.a.hq * D * sizeof(T) / 16; // a token's
+    uint4 *const out = static_cast<uint4 *>(p.a.out);
+    auto zero = [&](int t0, int t1) {
+        for (size_t i = (size_t)t0 * vecs + threadIdx.x; i < (size_t)t1 * vecs; i += THREADS)
+            out[i] = make_uint4(0, 0, 0, 0);
+    };
+    for (int r = blockIdx.x; r < c.rows; r += gridDim.x) {
+        const Row x = row_of(c, p.a.pages.page_size, r);
+        if (!x.live && x.n > 0)
+            zero(x.b, x.b + x.n);
+    }
+    if (blockIdx.x == 0) {
+        const int first = c.cu_seqlens[0], last = c.cu_seqlens[c.rows];
+        if (first > 0)
+            zero(0, min(first, c.total_tokens));
+        if (last >= 0 && last < c.total_tokens)
+            zero(last, c.total_tokens);
+        if (threadIdx.x == 0 && (first != 0 || last != c.total_tokens))
+            report(p.a.err, GDN_DEVERR_BAD_PAGE);
+    }
+}
+
+// The items of a run, in order, by one warp.
+struct Walk {
+    const WorkArgs &p;
+    const Run &run;
+    int mt, kt, heads, lane;
+    long long u;     // the next unit
+    int r, win;      // row; rows win .. win + 31 are in the lanes
+    Row mine, x;     // a lane's row; the current one
+    int items, h, t, ja;
+    bool in_row;
+
+    __device__ Walk(const WorkArgs &p_, const Run &run_, int mt_, int kt_)
+        : p(p_), run(run_), mt(mt_), kt(kt_), heads(p_.a.pages.hkv * p_.groups), lane(threadIdx.x & 31), u(run_.u0),
+          r(run_.row), win(run_.row), in_row(false)
+    {
+        if (lane == 0)
+            p.cuts[blockIdx.x].parts = 0;
+        __syncwarp();
+        fetch();
+    }
+    __device__ void fetch()
+    {
+        win = r;
+        mine = Row{0, 0, 0, false, false};
+        if (u < run.u1 && win + lane < p.a.c.rows)
+            mine = row_of(p.a.c, p.a.pages.page_size, win + lane);
+    }
+    // The next item; false at the run's end.  Lane 0 lists a cut.
+    __device__ bool next(Item &it)
+    {
+        if (u >= run.u1)
+            return false;
+        while (!in_row) {
+            if (r >= win + 32)
+                fetch();
+            x.b = __shfl_sync(0xffffffffu, mine.b, r - win);
+            x.n = __shfl_sync(0xffffffffu, mine.n, r - win);
+            x.len = __shfl_sync(0xffffffffu, mine.len, r - win);
+            if (!__shfl_sync(0xffffffffu, (int)mine.live, r - win)) {
+                if (++r >= p.a.c.rows)
+                    return false;
+                continue;
+            }
+            in_row = true;
+            items = items_of(x, mt);
+            h = t = ja = 0;
+            if (u == run.u0) { // the run begins inside this row
+                const long long per = head_tiles(x, mt, kt);
+                long long rem = u - run.base;
+                h = (int)(rem / per);
+                rem -= h * per;
+                while (rem >= item_tiles(x, t, mt, kt))
+                    rem -= item_tiles(x, t++, mt, kt);
+                ja = (int)rem;
+            }
+        }
+        const int J = item_tiles(x, t, mt, kt);
+        const int jb = (int)min((long long)J, ja + (run.u1 - u));
+        const int t0 = t * mt, ntok = min(mt, x.n - t0);
+        it = {x.b + t0, ntok, h, r, x.len - x.n + t0 + 1, ja, jb,
+              ja > 0 || jb < J ? 2 * (int)blockIdx.x + (ja > 0 ? 0 : 1) : -1};
+        // the run that holds an item's second part lists it for the combining kernel
+        if (lane == 0 && ja > 0 && u - run.share <= u - ja)
+            p.cuts[blockIdx.x] = {1 + (int)((J - ja + run.share - 1) / run.share), x.b + t0, ntok, h};
+        u += jb - ja;
+        ja = 0;
+        if (++t == items) {
+            t = 0;
+            if (++h == heads)
+                in_row = false, ++r;
+        }
+        return true;
+    }
+};
+
+// Joins the parts of cut items: block x holds the cut listed by run x, y
+// strides over its rows, a warp a row.
+template <typename T, int D> __global__ void __launch_bounds__(128) attn_combine_kernel(const WorkArgs p)
+{
+    wait_prior_grid();
+    const int w = blockIdx.x;
+    const Cut c = p.cuts[w];
+    if (c.parts == 0)
+        return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rows = c.ntok > p.tq ? p.second + (c.ntok - p.tq) * p.g : c.ntok * p.g;
+    const float k2 = p.a.scale * 1.44269504088896341f;
+    // the first part lies in run w - 1 (its last item), the others are the first items of runs w ..
+    auto slot = [&](int i) { return i == 0 ? 2 * (w - 1) + 1 : 2 * (w + i - 1); };
+    for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
+        const int tile = p.second && row >= p.second, in = row - tile * p.second, t = in / p.g, tok = t + tile * p.tq;
+        if (t >= p.tq || tok >= c.ntok)
+            continue;
+        float m = -INFINITY;
+        bool bad = false;
+        for (int i = 0; i < c.parts; ++i) {
+            const float mi = p.part_ml[(size_t)slot(i) * p.rows_max + row].x;
+            bad |= mi != mi;
+            m = fmaxf(m, mi);
+        }
+        float l = 0.f, x[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            x[e] = 0.f;
+        for (int i = 0; i < c.parts; ++i) {
+            const float2 ml = p.part_ml[(size_t)slot(i) * p.rows_max + row];
+            if (ml.x == -INFINITY)
+                continue;
+            const float f = ex2((ml.x - m) * k2);
+            l = fmaf(ml.y, f, l);
+            const float *o = p.part_o + ((size_t)slot(i) * p.rows_max + row) * D;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+                x[e] = fmaf(o[e * 32 + lane], f, x[e]);
+        }
+        T *const out = static_cast<T *>(p.a.out) + ((size_t)(c.tok + tok) * p.a.hq + c.head * p.g + (in - t * p.g)) * D;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            out[e * 32 + lane] = from_f<T>(bad ? 0.f : x[e] / l);
+    }
+}
+
+} // namespace
+} // namespace gdn

@@ -31,6 +31,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attn_plan.cuh"
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
 #include "gdn_ptx.cuh"
@@ -40,7 +41,6 @@ namespace {
 
 typedef __nv_bfloat16 bf16;
 
-constexpr int kCtas = 152;  // one CTA an SM (its tensor memory is taken whole)
 constexpr int kQueue = 4;   // items in flight between the walking warp and the others
 constexpr int kMeta = 16;   // key tiles whose valid-row count is kept; over a ring's tiles
 constexpr float kLazy = 8.f;
@@ -65,12 +65,6 @@ template <int D> struct Geo {
 };
 
 // The control block in shared memory, after Q and the ring.
-struct Item {
-    int tok, ntok, head, row; // first token, tokens, key head, cache row
-    int see;                  // keys the first token sees; one more each token on
-    int ja, jb;               // key tiles of this run
-    int part;                 // workspace slot of a cut item, or -1
-};
 struct Ctrl {
     unsigned long long full[12], empty[12];    // ring
     unsigned long long qfull[2], qempty[2];
@@ -80,20 +74,13 @@ struct Ctrl {
     Item item[kQueue];
     int valid[kMeta];       // good rows of a key tile, by the tile's count
     long long scan[13];
-    long long start, base;  // this run's first unit's row: found by the plan
-    int start_row;
+    long long found[2];     // this run's first row, by the plan
     uint32_t tmem;
     float ml[2][128][2];    // (m, l) of the two groups' rows, for the merge
     int bad[2];             // first key that could not be read, by group
     int dirty;              // 1 + the last item with a non-finite V element that only some of its tokens see
 };
 static_assert(sizeof(Ctrl) <= 3072, "control block");
-
-// One cut item, for the combining kernel: written by the run that holds the
-// item's second part.
-struct Cut {
-    int parts, tok, ntok, head;
-};
 
 // ---- tensor core and copy wrappers ----
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart
@@ -153,13 +140,6 @@ __device__ __forceinline__ uint32_t drop2(uint32_t w)
         w &= 0xffffu;
     return w;
 }
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // x[at] += y without indexing the registers
 __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
 {
@@ -202,85 +182,10 @@ __device__ __forceinline__ void tst(uint32_t a, const uint32_t (&r)[32])
 }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ---- the plan ----
-// A cache row's work: its tokens [b, b + n) and length, live when it is a real
-// row whose table can hold it.
-struct Row {
-    int b, n, len;
-    bool live, bad;
-};
-__device__ __forceinline__ Row row_of(const CacheRows &c, int page_size, int r)
-{
-    Row x;
-    x.b = c.cu_seqlens[r];
-    const int e = c.cu_seqlens[r + 1];
-    x.len = c.seq_len[r];
-    x.n = 0;
-    x.live = x.bad = false;
-    if (x.b < 0 || e < x.b || e > c.total_tokens) {
-        x.bad = true;
-    } else {
-        x.n = e - x.b;
-        x.bad = x.n > 0 && (x.len < 0 || (x.len > 0 && (x.len < x.n || x.len > c.max_pages * page_size)));
-        x.live = x.n > 0 && x.len > 0 && !x.bad;
-    }
-    return x;
-}
-// Key tiles of the row's item t (mt tokens an item).
-__device__ __forceinline__ int item_tiles(const Row &x, int t, int mt, int kt)
-{
-    const int last = min(x.n, (t + 1) * mt);
-    return (x.len - x.n + last + kt - 1) / kt;
-}
-__device__ __forceinline__ int items_of(const Row &x, int mt) { return (x.n + mt - 1) / mt; }
-__device__ long long head_tiles(const Row &x, int mt, int kt) // of one key head
-{
-    long long s = 0;
-    const int n = items_of(x, mt);
-    for (int t = 0; t < n; ++t)
-        s += item_tiles(x, t, mt, kt);
-    return s;
-}
-
-// Exclusive sum over the CTA's threads; `part` is one long long a warp, and one.
-__device__ __forceinline__ long long scan64(long long v, long long *part, int warps, long long &total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o)
-            s += x;
-    }
-    if (lane == 31)
-        part[warp] = s;
-    __syncthreads();
-    long long before = s - v;
-    total = 0;
-    for (int w = 0; w < warps; ++w) {
-        const long long x = part[w];
-        if (w < warp)
-            before += x;
-        total += x;
-    }
-    __syncthreads();
-    return before;
-}
-
-struct TcArgs {
-    AttentionArgs a;
-    int g, tq;      // query heads a key head, tokens a tile
-    int rows_max;   // rows of a workspace slot
-    float *part_o;  // [2 kCtas][rows_max][D]
-    float2 *part_ml;
-    Cut *cuts;      // [kCtas]
-};
-
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
-    attn_tc_kernel(const TcArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+    attn_tc_kernel(const WorkArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
     typedef Geo<D> G;
     constexpr int KT = G::KT;
@@ -323,63 +228,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- the plan: the whole work, then the row where this CTA's run begins
-    long long total = 0, share, u0;
-    {
-        const int warps = G::THREADS / 32;
-        for (int base = 0; base < a.c.rows; base += G::THREADS) {
-            long long cost = 0, sum;
-            if (base + tid < a.c.rows) {
-                const Row x = row_of(a.c, ps, base + tid);
-                if (x.live)
-                    cost = head_tiles(x, mt, KT) * hkv;
-                else if (x.bad && blockIdx.x == 0)
-                    report(a.err, GDN_DEVERR_BAD_PAGE);
-            }
-            scan64(cost, ctl.scan, warps, sum);
-            total += sum;
-        }
-        share = (total + gridDim.x - 1) / gridDim.x;
-        if (share < 1)
-            share = 1;
-        u0 = share * blockIdx.x;
-        long long seen = 0;
-        for (int base = 0; base < a.c.rows && seen <= u0 && u0 < total; base += G::THREADS) {
-            long long cost = 0, sum;
-            if (base + tid < a.c.rows) {
-                const Row x = row_of(a.c, ps, base + tid);
-                if (x.live)
-                    cost = head_tiles(x, mt, KT) * hkv;
-            }
-            const long long before = seen + scan64(cost, ctl.scan, warps, sum);
-            if (cost > 0 && before <= u0 && u0 < before + cost)
-                ctl.start_row = base + tid, ctl.base = before;
-            seen += sum;
-        }
-        // outputs of tokens that no live row has: zeros
-        bf16 *const out = static_cast<bf16 *>(a.out);
-        const size_t tok_vecs = (size_t)a.hq * D / 8;
-        auto zero = [&](int t0, int t1) {
-            for (size_t i = (size_t)t0 * tok_vecs + tid; i < (size_t)t1 * tok_vecs; i += G::THREADS)
-                reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
-        };
-        for (int r = blockIdx.x; r < a.c.rows; r += gridDim.x) {
-            const Row x = row_of(a.c, ps, r);
-            if (!x.live && x.n > 0)
-                zero(x.b, x.b + x.n);
-        }
-        if (blockIdx.x == 0) {
-            const int first = a.c.cu_seqlens[0], last = a.c.cu_seqlens[a.c.rows];
-            if (first > 0)
-                zero(0, min(first, a.c.total_tokens));
-            if (last >= 0 && last < a.c.total_tokens)
-                zero(last, a.c.total_tokens);
-            if (tid == 0 && (first != 0 || last != a.c.total_tokens))
-                report(a.err, GDN_DEVERR_BAD_PAGE);
-        }
-        __syncthreads();
-    }
-    const long long u1 = min(total, u0 + share);
+    const Run run = plan_run<G::THREADS, KT>(p, mt, ctl.scan, ctl.found);
+    zero_dead<bf16, D, G::THREADS>(p);
     bool alive = true; // false once a bounded wait ran out
     auto wait1 = [&](unsigned long long &b, uint32_t parity) { // by one lane
         if (alive && !mbar_wait(bar(b), parity)) {
@@ -406,80 +256,22 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 3) {
             // ---- the walk: this run's items, in order
-            if (lane == 0)
-                p.cuts[blockIdx.x].parts = 0;
-            __syncwarp();
-            if (u0 < u1) {
-                long long u = u0;
-                int r = ctl.start_row;
-                long long off = u0 - ctl.base;
-                int q = 0;
-                bool first = true;
-                int win = r; // rows win .. win + 31 are in the lanes
-                Row mine = win + lane < a.c.rows ? row_of(a.c, ps, win + lane) : Row{0, 0, 0, false, false};
-                while (u < u1 && alive) {
-                    if (r >= win + 32) {
-                        win = r;
-                        mine = win + lane < a.c.rows ? row_of(a.c, ps, win + lane) : Row{0, 0, 0, false, false};
-                    }
-                    Row x;
-                    x.b = __shfl_sync(0xffffffffu, mine.b, r - win);
-                    x.n = __shfl_sync(0xffffffffu, mine.n, r - win);
-                    x.len = __shfl_sync(0xffffffffu, mine.len, r - win);
-                    x.live = __shfl_sync(0xffffffffu, (int)mine.live, r - win);
-                    if (!x.live) {
-                        ++r;
-                        continue;
-                    }
-                    const int items = items_of(x, mt);
-                    const long long per = head_tiles(x, mt, KT);
-                    int h = (int)(off / per), t = 0;
-                    int ja = 0;
-                    {
-                        long long rem = off - h * per;
-                        while (rem >= item_tiles(x, t, mt, KT))
-                            rem -= item_tiles(x, t++, mt, KT);
-                        ja = (int)rem;
-                    }
-                    off = 0;
-                    for (; h < hkv && u < u1; ++h, t = 0)
-                        for (; t < items && u < u1; ++t) {
-                            const int J = item_tiles(x, t, mt, KT);
-                            const int jb = (int)min((long long)J, ja + (u1 - u));
-                            const bool cut = ja > 0 || jb < J;
-                            const int slot = q % kQueue;
-                            if (!wait(ctl.iempty[slot], (q / kQueue + 1) & 1))
-                                break;
-                            const int t0 = t * mt, ntok = min(mt, x.n - t0);
-                            if (lane == 0) {
-                                ctl.item[slot] = {x.b + t0, ntok, h, r, x.len - x.n + t0 + 1, ja, jb,
-                                                  cut ? 2 * (int)blockIdx.x + (ja > 0 ? 0 : 1) : -1};
-                                if (first) {
-                                    // the run that holds an item's second part lists it for the combining kernel
-                                    const long long begin = u - ja;
-                                    Cut c = {0, x.b + t0, ntok, h};
-                                    if (ja > 0 && u - share <= begin)
-                                        c.parts = 1 + (int)((begin + J - u + share - 1) / share);
-                                    p.cuts[blockIdx.x] = c;
-                                }
-                                mbar_arrive(bar(ctl.ifull[slot]));
-                            }
-                            __syncwarp();
-                            first = false;
-                            u += jb - ja;
-                            ja = 0;
-                            ++q;
-                        }
-                    ++r;
-                }
+            Walk walk(p, run, mt, KT);
+            Item it;
+            for (int q = 0; alive; ++q) {
+                const bool more = walk.next(it);
                 const int slot = q % kQueue;
-                if (wait(ctl.iempty[slot], (q / kQueue + 1) & 1) && lane == 0) {
-                    ctl.item[slot].ntok = 0;
+                if (!wait(ctl.iempty[slot], (q / kQueue + 1) & 1))
+                    break;
+                if (!more)
+                    it.ntok = 0;
+                if (lane == 0) {
+                    ctl.item[slot] = it;
                     mbar_arrive(bar(ctl.ifull[slot]));
                 }
-            } else if (lane == 0) {
-                ctl.item[0].ntok = 0;
-                mbar_arrive(bar(ctl.ifull[0]));
+                __syncwarp();
+                if (!more)
+                    break;
             }
         } else if (warp == 0) {
             // ---- K and V pages into the ring
@@ -497,6 +289,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 if (it.ntok == 0)
                     break;
                 const int32_t *const table = a.c.table + (size_t)it.row * a.c.max_pages;
+                const int kvh = it.head / p.groups;
                 const int end = it.see + it.ntok - 1;     // keys the item's last token sees
                 const int pages = (end + ps - 1) >> a.pages.page_shift;
                 const bool pair = G::NO == 2 && it.ntok > p.tq;
@@ -540,7 +333,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < G::CH; ++c)
                             tma3(dst + c * KT * 128, is_v ? &vmap : &kmap, 64 * c, key & (ps - 1),
-                                 (a.pages.layer * a.pages.num_pages + page) * hkv + it.head, b);
+                                 (a.pages.layer * a.pages.num_pages + page) * hkv + kvh, b);
                     }
                     __syncwarp();
                     ++issued;
@@ -886,7 +679,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                         for (int key = max(it.see, it.ja * KT); key < min(see, it.jb * KT); ++key) {
                             const int page = a.c.table[(size_t)it.row * a.c.max_pages + (key >> a.pages.page_shift)];
                             const bf16 *const v = static_cast<const bf16 *>(a.pages.v) +
-                                                  (((size_t)page * hkv + it.head) * ps + (key & (ps - 1))) * D + k;
+                                                  (((size_t)page * hkv + it.head / p.groups) * ps + (key & (ps - 1))) * D + k;
 #pragma unroll 1
                             for (int e = 0; e < 32; ++e) {
                                 const float y = __bfloat162float(v[e]);
@@ -925,53 +718,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     after_sync();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
-}
-
-// Joins the parts of cut items: block x holds the cut listed by run x, y
-// strides over its rows, a warp a row.
-template <int D> __global__ void __launch_bounds__(128) attn_combine_kernel(const TcArgs p)
-{
-    wait_prior_grid();
-    const int w = blockIdx.x;
-    const Cut c = p.cuts[w];
-    if (c.parts == 0)
-        return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rows = c.ntok > p.tq ? 128 + (c.ntok - p.tq) * p.g : c.ntok * p.g;
-    const float k2 = p.a.scale * 1.44269504088896341f;
-    // the first part lies in run w - 1 (its last item), the others are the first items of runs w ..
-    auto slot = [&](int i) { return i == 0 ? 2 * (w - 1) + 1 : 2 * (w + i - 1); };
-    for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
-        const int in = row & 127, t = in / p.g, tok = t + (row >> 7) * p.tq;
-        if (t >= p.tq || tok >= c.ntok)
-            continue;
-        float m = -INFINITY;
-        bool bad = false;
-        for (int i = 0; i < c.parts; ++i) {
-            const float mi = p.part_ml[(size_t)slot(i) * p.rows_max + row].x;
-            bad |= mi != mi;
-            m = fmaxf(m, mi);
-        }
-        float l = 0.f, x[D / 32];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            x[e] = 0.f;
-        for (int i = 0; i < c.parts; ++i) {
-            const float2 ml = p.part_ml[(size_t)slot(i) * p.rows_max + row];
-            if (ml.x == -INFINITY)
-                continue;
-            const float f = ex2((ml.x - m) * k2);
-            l = fmaf(ml.y, f, l);
-            const float *o = p.part_o + ((size_t)slot(i) * p.rows_max + row) * D;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                x[e] = fmaf(o[e * 32 + lane], f, x[e]);
-        }
-        bf16 *const out = static_cast<bf16 *>(p.a.out) + ((size_t)(c.tok + tok) * p.a.hq + c.head * p.g + (in - t * p.g)) * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            out[e * 32 + lane] = __float2bfloat16_rn(bad ? 0.f : x[e] / l);
-    }
 }
 
 // ---- host ----
@@ -1028,14 +774,14 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
             return e;
         configured.fetch_or(bit, std::memory_order_release);
     }
-    TcArgs p;
+    WorkArgs p;
     p.a = a;
-    p.g = a.hq / a.pages.hkv;
+    p.g = group_heads(a.hq, a.pages.hkv, 128);
+    p.groups = a.hq / a.pages.hkv / p.g;
     p.tq = 128 / p.g;
     p.rows_max = slot_rows(D, p.g, a.c.total_tokens);
-    p.cuts = static_cast<Cut *>(a.work);
-    p.part_ml = reinterpret_cast<float2 *>(p.cuts + kCtas);
-    p.part_o = reinterpret_cast<float *>(p.part_ml + 2 * (size_t)kCtas * p.rows_max);
+    p.second = G::NO == 2 ? 128 : 0;
+    work_layout(p);
     {
         const std::lock_guard<std::mutex> lk(pool.map_mutex);
         const int box = pool.page_size < G::KT ? pool.page_size : G::KT;
@@ -1048,17 +794,14 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
     e = launch_pdl(attn_tc_kernel<D>, dim3(kCtas), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<D>, dim3(kCtas, p.rows_max > 32 ? 8 : 1), dim3(128), 0, s, p);
+    return launch_pdl(attn_combine_kernel<bf16, D>, dim3(kCtas, p.rows_max > 32 ? 8 : 1), dim3(128), 0, s, p);
 }
 
 } // namespace
 
-bool attention_tc_supported(int hq, int hkv) { return hq / hkv <= 128; }
-
 size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens)
 {
-    const size_t rows = (size_t)slot_rows(d, hq / hkv, total_tokens);
-    return sizeof(Cut) * kCtas + 2 * (size_t)kCtas * rows * (sizeof(float2) + sizeof(float) * d);
+    return work_bytes(d, slot_rows(d, group_heads(hq, hkv, 128), total_tokens));
 }
 
 cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s)

@@ -191,12 +191,11 @@ size_t prefill_chunked_workspace_bytes(int nseq, int total_tokens, int hv);
 cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table,
                               cudaStream_t s);
 cudaError_t launch_attn_prologue(const PrologueArgs &a, int dtype, cudaStream_t s);
-size_t attention_workspace_bytes(int d, int dtype, int hq, int hkv, int rows, int total_tokens);
-cudaError_t launch_paged_attention(const AttentionArgs &a, kv_page_pool &pool, int dtype, cudaStream_t s);
-// bf16 on the tensor cores: up to 128 query heads a key head
-bool attention_tc_supported(int hq, int hkv);
+// paged_attention: bf16 (attn_tc.cu) and fp32 (attn_f32.cu)
 size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens);
+size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens);
 cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s);
+cudaError_t launch_paged_attention_f32(const AttentionArgs &a, cudaStream_t s);
 cudaError_t launch_pages_reserve(const PageTables &t, const int32_t *list_rows, const int32_t *tokens, int n,
                                  int32_t *status, cudaStream_t s);
 cudaError_t launch_pages_fork(const PageTables &t, const int32_t *src_rows, const int32_t *dst_rows, int n,

@@ -1,5 +1,5 @@
 // C ABI of the attention layers over a paged cache: pool handles and argument
-// checks.  The kernels are in attn_prologue.cu, attn_paged.cu and kv_pages.cu.
+// checks.  The kernels are in attn_prologue.cu, attn_tc.cu, attn_f32.cu and kv_pages.cu.
 #include <cmath>
 #include <new>
 
@@ -240,7 +240,8 @@ size_t paged_attention_workspace_bytes(const kv_page_pool *pool, int hq, int row
 {
     if (!pool || hq < 1 || hq % pool->hkv != 0 || rows < 1 || total_tokens < 1)
         return 0;
-    return gdn::attention_workspace_bytes(pool->d, pool->dtype, hq, pool->hkv, rows, total_tokens);
+    return pool->dtype == GDN_BF16 ? gdn::attention_tc_workspace_bytes(pool->d, hq, pool->hkv, total_tokens)
+                                   : gdn::attention_f32_workspace_bytes(pool->d, hq, pool->hkv, total_tokens);
 }
 
 int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int layer, const int32_t *table,
@@ -269,7 +270,8 @@ int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int lay
     a.pages = view(pool, layer);
     a.c = {table, seq_len, cu_seqlens, max_pages, rows, total_tokens};
     a.scale = scale, a.out = out, a.hq = hq, a.work = workspace;
-    return launched(gdn::launch_paged_attention(a, *pool, dtype, static_cast<cudaStream_t>(stream)),
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launched(dtype == GDN_BF16 ? gdn::launch_paged_attention_tc(a, *pool, s) : gdn::launch_paged_attention_f32(a, s),
                     "paged_attention launch");
 }
 

@@ -19,7 +19,7 @@ def run(G, c, new, hq, seed=1, scale=None, layer=0, q=None, **kw):
     return q, out
 
 
-HEADS = [(4, 4, 64), (12, 4, 64), (16, 4, 128), (7, 1, 128), (10, 2, 128), (16, 2, 256), (6, 2, 256)]
+HEADS = [(136, 1, 64), (4, 4, 64), (12, 4, 64), (16, 4, 128), (7, 1, 128), (10, 2, 128), (16, 2, 256), (6, 2, 256)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
