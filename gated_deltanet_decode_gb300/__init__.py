@@ -780,11 +780,14 @@ def attn_prologue(q, k, v, pool: KVPagePool, rope: Optional[torch.Tensor], table
         positions, rot = rope.shape
     if out is None:
         out = torch.empty((T, hq, d), dtype=pool.dtype, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, T * hq * d, pool.dtype, dev, "out")
     _check(_lib.load().attn_prologue(
         qp, qs, kp, ks, vp, vs, pool._h, layer, _arg(rope, positions * rot, f32, dev, "rope"), positions, rot,
         1 if interleaved else 0, _arg(q_norm, d, f32, dev, "q_norm"), _arg(k_norm, d, f32, dev, "k_norm"), eps, tab,
         max_pages, _arg(seq_len, rows, i32, dev, "seq_len"), _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"),
-        _arg(out, T * hq * d, pool.dtype, dev, "out"), hq, rows, T, pool._code, _raw_stream(dev)))
+        op, hq, rows, T, pool._code, _raw_stream(dev)))
     return out
 
 
@@ -805,16 +808,20 @@ def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int 
     qp, qs = _token_rows(q, T, hq, pool, "q")
     if out is None:
         out = torch.empty((T, hq, d), dtype=pool.dtype, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, T * hq * d, pool.dtype, dev, "out")
     L = _lib.load()
     if workspace is None:
-        need = L.paged_attention_workspace_bytes(pool._h, hq, rows, T)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        nbytes = L.paged_attention_workspace_bytes(pool._h, hq, rows, T)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, nbytes = _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size()
     _check(L.paged_attention(
         qp, qs, pool._h, layer, tab, max_pages, _arg(seq_len, rows, i32, dev, "seq_len"),
         _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"), d ** -0.5 if scale is None else scale,
-        _arg(out, T * hq * d, pool.dtype, dev, "out"), hq, rows, T, _ptr(workspace, "workspace", None, dev), nbytes,
-        pool._code, _raw_stream(dev)))
+        op, hq, rows, T, wp, nbytes, pool._code, _raw_stream(dev)))
     return out
 
 

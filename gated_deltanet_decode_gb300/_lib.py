@@ -133,6 +133,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libgdn_decode.so (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if build_if_missing else _build.LIB_PATH
