@@ -117,6 +117,12 @@ __device__ __forceinline__ void commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ bool elect() // one lane of a converged warp
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -231,13 +237,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     const Run run = plan_run<G::THREADS, KT>(p, mt, ctl.scan, ctl.found);
     zero_dead<bf16, D, G::THREADS>(p);
     bool alive = true; // false once a bounded wait ran out
-    auto wait1 = [&](unsigned long long &b, uint32_t parity) { // by one lane
-        if (alive && !mbar_wait(bar(b), parity)) {
-            alive = false;
-            report(a.err, GDN_DEVERR_TIMEOUT);
-        }
-        return alive;
-    };
     auto wait = [&](unsigned long long &b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
         if (alive && !__all_sync(0xffffffffu, mbar_wait(bar(b), parity))) {
             alive = false;
@@ -367,73 +366,81 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     mbar_wait(bar(ctl.full[i % G::STAGES]), (i / G::STAGES) & 1);
             }
         } else if (warp == 1) {
-            // ---- the products, issued by one lane
-            if (lane == 0) {
-                unsigned place0 = 0, qc = 0, scnt[2] = {0, 0};
-                for (int q = 0;; ++q) {
-                    const int slot = q % kQueue;
-                    if (!wait1(ctl.ifull[slot], (q / kQueue) & 1))
-                        break;
-                    const Item it = ctl.item[slot];
+            // ---- the products.  The whole warp walks, on values that the broadcasts make uniform to the compiler, and
+            // one elected lane issues: an issue loop in a divergent branch took 1,970 cycles a step, twice the products'.
+            unsigned place0 = 0, qc = 0, scnt[2] = {0, 0};
+            for (int q = 0;; ++q) {
+                const int slot = q % kQueue;
+                if (!wait(ctl.ifull[slot], (q / kQueue) & 1))
+                    break;
+                const int ntok = __shfl_sync(0xffffffffu, ctl.item[slot].ntok, 0);
+                const int n = __shfl_sync(0xffffffffu, ctl.item[slot].jb - ctl.item[slot].ja, 0);
+                __syncwarp();
+                if (lane == 0)
                     mbar_arrive(bar(ctl.iempty[slot]));
-                    if (it.ntok == 0)
-                        break;
-                    const bool pair = G::NO == 2 && it.ntok > p.tq;
-                    const int n = it.jb - it.ja, steps = pair ? 2 * n : n;
-                    const int qn = pair ? 2 : 1;
-                    for (int i = 0; i < qn; ++i)
-                        wait1(ctl.qfull[(qc + i) % G::NQ], ((qc + i) / G::NQ) & 1);
-                    auto s_step = [&](int i) {
-                        const int j = pair ? i >> 1 : i, b = i & 1;
-                        const unsigned pl = place0 + k_place(pair, j);
-                        const int st = pl % G::STAGES;
-                        if (!wait1(ctl.full[st], (pl / G::STAGES) & 1))
-                            return;
-                        after_sync();
-                        const uint32_t qa = sbase + ((qc + (pair ? b : 0)) % G::NQ) * G::QBYTES, ka = stage_addr(st);
+                if (ntok == 0)
+                    break;
+                const bool pair = G::NO == 2 && ntok > p.tq;
+                const int steps = pair ? 2 * n : n, qn = pair ? 2 : 1;
+                for (int i = 0; i < qn; ++i)
+                    wait(ctl.qfull[(qc + i) % G::NQ], ((qc + i) / G::NQ) & 1);
+                auto s_step = [&](int i) {
+                    const int j = pair ? i >> 1 : i, b = i & 1;
+                    const unsigned pl = place0 + k_place(pair, j);
+                    const int st = pl % G::STAGES;
+                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
+                        return;
+                    after_sync();
+                    const uint64_t qd = desc_k(sbase + ((qc + (pair ? b : 0)) % G::NQ) * G::QBYTES), kd = desc_k(stage_addr(st));
+                    if (elect()) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_ss(tmem + G::S0 + b * KT, desc_k(qa + (k >> 2) * 128 * 128 + (k & 3) * 32),
-                                   desc_k(ka + (k >> 2) * KT * 128 + (k & 3) * 32), idesc(KT, false), k > 0);
+                            mma_ss(tmem + G::S0 + b * KT, qd + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
+                                   kd + (((k >> 2) * KT * 128 + (k & 3) * 32) >> 4), idesc(KT, false), k > 0);
                         commit(bar(ctl.sready[b]));
                         if (!pair || b)
                             commit(bar(ctl.empty[st]));
                         if (i == steps - 1)
                             for (int k = 0; k < qn; ++k)
                                 commit(bar(ctl.qempty[(qc + k) % G::NQ]));
-                    };
-                    if (!alive)
+                    }
+                    __syncwarp();
+                };
+                if (!alive)
+                    break;
+                s_step(0);
+                if (steps > 1)
+                    s_step(1);
+                for (int i = 0; i < steps && alive; ++i) {
+                    const int j = pair ? i >> 1 : i, b = i & 1, o = G::NO == 2 ? b : 0;
+                    const unsigned pl = place0 + v_place(pair, j, n);
+                    const int st = pl % G::STAGES;
+                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1) || !wait(ctl.pready[b], scnt[b] & 1))
                         break;
-                    s_step(0);
-                    if (steps > 1)
-                        s_step(1);
-                    for (int i = 0; i < steps && alive; ++i) {
-                        const int j = pair ? i >> 1 : i, b = i & 1, o = G::NO == 2 ? b : 0;
-                        const unsigned pl = place0 + v_place(pair, j, n);
-                        const int st = pl % G::STAGES;
-                        if (!wait1(ctl.full[st], (pl / G::STAGES) & 1) || !wait1(ctl.pready[b], scnt[b] & 1))
-                            break;
-                        ++scnt[b];
-                        after_sync();
-                        const uint32_t va = stage_addr(st);
-                        const bool more = G::NO == 2 ? i >= 2 : i >= 1;
+                    ++scnt[b];
+                    after_sync();
+                    const uint64_t vd = desc_mn(stage_addr(st), KT * 128);
+                    const bool more = G::NO == 2 ? i >= 2 : i >= 1;
+                    if (elect()) {
 #pragma unroll
                         for (int k = 0; k < KT / 16; ++k)
-                            mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, desc_mn(va + k * 2048, KT * 128),
-                                   idesc(D, true), more || k > 0);
-                        commit(bar(ctl.odone[b]));
+                            mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, vd + k * (2048 >> 4), idesc(D, true),
+                                   k > 0 || more);
+                        // O is waited for at an item's end and, with one group, before it is rescaled
+                        if (G::NO == 1 || i + 2 >= steps)
+                            commit(bar(ctl.odone[b]));
                         if (!pair || b)
                             commit(bar(ctl.empty[st]));
-                        if (i + 2 < steps)
-                            s_step(i + 2);
                     }
-                    place0 += 2 * n;
-                    qc += qn;
-                    if (!alive)
-                        break;
+                    __syncwarp();
+                    if (i + 2 < steps)
+                        s_step(i + 2);
                 }
+                place0 += 2 * n;
+                qc += qn;
+                if (!alive)
+                    break;
             }
-            __syncwarp();
         } else {
             // ---- Q tiles, by 16-byte asynchronous copies
             unsigned qc = 0;
@@ -482,7 +489,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // 32 tensor-memory lanes a warp
         const float c = a.scale * 1.44269504088896341f;    // weights are 2^(c (s - m))
         const int tok = row / p.g;
-        unsigned cnt[2] = {0, 0}; // steps done, by step parity
+        unsigned cnt[2] = {0, 0};  // steps done, by step parity
+        unsigned ends[2] = {0, 0}; // items done that have steps of the parity
         unsigned tiles = 0, place0 = 0, meets = 0;
         auto meet = [&] { // of the two groups
             __syncwarp();
@@ -544,13 +552,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                         l *= f;
                         const bool has_o = G::NO == 2 ? i >= 2 : i >= 1;
                         if (has_o) {
-                            // the last product into O is done: this group's last step's, whose step parity is b, or
-                            // the other with one group.  The product before that one is done, since S of this step
-                            // was issued after it, so the parity tells the two apart.
-                            const int last = G::NO == 2 ? b : b ^ 1;
-                            if (!wait(ctl.odone[last], (G::NO == 2 ? cnt[b] - 2 : cnt[b ^ 1] - 1) & 1))
-                                break;
-                            after_sync();
+                            // The products into O are done: with two groups all, as this step's S was issued after them;
+                            // with one group the last step's may be under way, and the one before it is done, so the
+                            // parity tells the two apart.
+                            if (G::NO == 1) {
+                                if (!wait(ctl.odone[b ^ 1], (cnt[b ^ 1] - 1) & 1))
+                                    break;
+                                after_sync();
+                            }
 #pragma unroll
                             for (int k = 0; k < D; k += 32) {
                                 uint32_t r[32];
@@ -646,8 +655,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 const int last = (steps - 1) & 1; // with one group: the last step's product is after all others
                 const bool own0 = G::NO == 1 ? last == 0 : !pair || grp == 0;
                 const bool own1 = G::NO == 1 ? last == 1 : both || (pair && grp == 1);
-                if ((own0 && !wait(ctl.odone[0], (cnt[0] - 1) & 1)) || (own1 && !wait(ctl.odone[1], (cnt[1] - 1) & 1)))
+                // completions so far: one a step with one group, else one an item
+                const unsigned c0 = G::NO == 1 ? cnt[0] : ends[0] + 1, c1 = G::NO == 1 ? cnt[1] : ends[1] + 1;
+                if ((own0 && !wait(ctl.odone[0], (c0 - 1) & 1)) || (own1 && !wait(ctl.odone[1], (c1 - 1) & 1)))
                     break;
+                ++ends[0];
+                ends[1] += steps > 1;
                 after_sync();
             }
             const bool bad = see > broken;
