@@ -36,7 +36,8 @@ template <int D> struct Geo32 {
 };
 
 struct Ctrl32 {
-    long long scan[kThreads / 32], found[2];
+    long long scan[kThreads / 32];
+    Found found;
     Item item;
     int more, broken, dirty;
     float2 ml[8 * 16]; // (m, l) by (share, row): 128 pairs in every form
@@ -169,7 +170,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Run run = plan_run<kThreads, KT>(p, p.tq, ctl.scan, ctl.found);
-    zero_dead<float, D, kThreads>(p);
+    zero_dead<float, D, kThreads>(p, tid);
     Walk walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
     for (;;) {
         __syncthreads();
@@ -335,7 +336,7 @@ template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
     e = launch_pdl(attn_f32_kernel<D>, dim3(kCtas), dim3(kThreads), (size_t)G::FLOATS * 4, s, p);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<float, D>, dim3(kCtas, p.rows_max > 32 ? 8 : 1), dim3(128), 0, s, p);
+    return launch_pdl(attn_combine_kernel<float, D>, dim3(kCtas, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
 }
 
 } // namespace

@@ -141,25 +141,31 @@ __device__ __forceinline__ long long scan64(long long v, long long *part, int wa
 struct Run {
     long long share, u0, u1, base;
     int row;
+    Row first; // the row it begins in
 };
-template <int THREADS, int KT>
-__device__ Run plan_run(const WorkArgs &p, int mt, long long *part, volatile long long *found)
+struct Found { // shared memory
+    long long base;
+    int row;
+    Row first;
+};
+template <int THREADS, int KT> __device__ Run plan_run(const WorkArgs &p, int mt, long long *part, Found &found)
 {
     const CacheRows &c = p.a.c;
     const int ps = p.a.pages.page_size, heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
-    auto cost_of = [&](int r, bool first) -> long long {
+    Row x{0, 0, 0, false, false};
+    auto cost_of = [&](int r) -> long long {
         if (r >= c.rows)
             return 0;
-        const Row x = row_of(c, ps, r);
-        if (first && x.bad && blockIdx.x == 0)
-            report(p.a.err, GDN_DEVERR_BAD_PAGE);
+        x = row_of(c, ps, r);
         return x.live ? head_tiles(x, mt, KT) * heads : 0;
     };
     Run run;
-    long long total = 0;
+    long long total = 0, cost = 0, before = 0, sum;
     for (int b = 0; b < c.rows; b += THREADS) {
-        long long sum;
-        scan64(cost_of(b + tid, true), part, THREADS / 32, sum);
+        cost = cost_of(b + tid);
+        if (x.bad && blockIdx.x == 0)
+            report(p.a.err, GDN_DEVERR_BAD_PAGE);
+        before = scan64(cost, part, THREADS / 32, sum);
         total += sum;
     }
     run.share = (total + gridDim.x - 1) / gridDim.x;
@@ -167,29 +173,35 @@ __device__ Run plan_run(const WorkArgs &p, int mt, long long *part, volatile lon
         run.share = 1;
     run.u0 = run.share * blockIdx.x;
     run.u1 = min(total, run.u0 + run.share);
-    long long seen = 0;
-    for (int b = 0; b < c.rows && seen <= run.u0 && run.u0 < total; b += THREADS) {
-        long long sum;
-        const long long cost = cost_of(b + tid, false);
-        const long long before = seen + scan64(cost, part, THREADS / 32, sum);
+    if (c.rows <= THREADS) { // the one pass has it
         if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
-            found[0] = b + tid, found[1] = before;
-        seen += sum;
+            found = {before, tid, x};
+    } else {
+        long long seen = 0;
+        for (int b = 0; b < c.rows && seen <= run.u0 && run.u0 < total; b += THREADS) {
+            cost = cost_of(b + tid);
+            before = seen + scan64(cost, part, THREADS / 32, sum);
+            if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
+                found = {before, b + tid, x};
+            seen += sum;
+        }
     }
     __syncthreads();
-    run.row = (int)found[0];
-    run.base = found[1];
+    run.row = found.row;
+    run.base = found.base;
+    run.first = found.first;
     return run;
 }
 
-// Zeros for the outputs of tokens that no live row has, by all CTAs together.
-template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkArgs &p)
+// Zeros for the outputs of tokens that no live row has, by THREADS threads (tid)
+// of all CTAs together.
+template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkArgs &p, int tid)
 {
     const CacheRows &c = p.a.c;
     const size_t vecs = (size_t)p.a.hq * D * sizeof(T) / 16; // a token's
     uint4 *const out = static_cast<uint4 *>(p.a.out);
     auto zero = [&](int t0, int t1) {
-        for (size_t i = (size_t)t0 * vecs + threadIdx.x; i < (size_t)t1 * vecs; i += THREADS)
+        for (size_t i = (size_t)t0 * vecs + tid; i < (size_t)t1 * vecs; i += THREADS)
             out[i] = make_uint4(0, 0, 0, 0);
     };
     for (int r = blockIdx.x; r < c.rows; r += gridDim.x) {
@@ -203,7 +215,7 @@ template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkAr
             zero(0, min(first, c.total_tokens));
         if (last >= 0 && last < c.total_tokens)
             zero(last, c.total_tokens);
-        if (threadIdx.x == 0 && (first != 0 || last != c.total_tokens))
+        if (tid == 0 && (first != 0 || last != c.total_tokens))
             report(p.a.err, GDN_DEVERR_BAD_PAGE);
     }
 }
@@ -226,7 +238,24 @@ struct Walk {
         if (lane == 0)
             p.cuts[blockIdx.x].parts = 0;
         __syncwarp();
-        fetch();
+        fetch(); // the next rows' lengths, while the first row's items are handed out
+        if (u < run.u1) {
+            enter(run.first);
+            const long long per = head_tiles(x, mt, kt);
+            long long rem = u - run.base; // the run begins inside this row
+            h = (int)(rem / per);
+            rem -= h * per;
+            while (rem >= item_tiles(x, t, mt, kt))
+                rem -= item_tiles(x, t++, mt, kt);
+            ja = (int)rem;
+        }
+    }
+    __device__ void enter(const Row &row)
+    {
+        x = row;
+        in_row = true;
+        items = items_of(x, mt);
+        h = t = ja = 0;
     }
     __device__ void fetch()
     {
@@ -246,23 +275,13 @@ struct Walk {
             x.b = __shfl_sync(0xffffffffu, mine.b, r - win);
             x.n = __shfl_sync(0xffffffffu, mine.n, r - win);
             x.len = __shfl_sync(0xffffffffu, mine.len, r - win);
+            x.live = true, x.bad = false;
             if (!__shfl_sync(0xffffffffu, (int)mine.live, r - win)) {
                 if (++r >= p.a.c.rows)
                     return false;
                 continue;
             }
-            in_row = true;
-            items = items_of(x, mt);
-            h = t = ja = 0;
-            if (u == run.u0) { // the run begins inside this row
-                const long long per = head_tiles(x, mt, kt);
-                long long rem = u - run.base;
-                h = (int)(rem / per);
-                rem -= h * per;
-                while (rem >= item_tiles(x, t, mt, kt))
-                    rem -= item_tiles(x, t++, mt, kt);
-                ja = (int)rem;
-            }
+            enter(x);
         }
         const int J = item_tiles(x, t, mt, kt);
         const int jb = (int)min((long long)J, ja + (run.u1 - u));
@@ -284,7 +303,8 @@ struct Walk {
 };
 
 // Joins the parts of cut items: block x holds the cut listed by run x, y
-// strides over its rows, a warp a row.
+// strides over its rows, a warp a row.  The lanes take a part's (m, l) each,
+// then all walk over the parts' O, four parts' loads in flight.
 template <typename T, int D> __global__ void __launch_bounds__(128) attn_combine_kernel(const WorkArgs p)
 {
     wait_prior_grid();
@@ -292,41 +312,69 @@ template <typename T, int D> __global__ void __launch_bounds__(128) attn_combine
     const Cut c = p.cuts[w];
     if (c.parts == 0)
         return;
+    constexpr int V = D / 32 < 4 ? D / 32 : 4, N = D / (32 * V); // a lane's columns: N runs of V
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = c.ntok > p.tq ? p.second + (c.ntok - p.tq) * p.g : c.ntok * p.g;
     const float k2 = p.a.scale * 1.44269504088896341f;
     // the first part lies in run w - 1 (its last item), the others are the first items of runs w ..
-    auto slot = [&](int i) { return i == 0 ? 2 * (w - 1) + 1 : 2 * (w + i - 1); };
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * (w - 1) + 1 : 2 * (w + i - 1)) * p.rows_max; };
     for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
         const int tile = p.second && row >= p.second, in = row - tile * p.second, t = in / p.g, tok = t + tile * p.tq;
         if (t >= p.tq || tok >= c.ntok)
             continue;
-        float m = -INFINITY;
+        float m = -INFINITY, l = 0.f, x[N][V];
         bool bad = false;
-        for (int i = 0; i < c.parts; ++i) {
-            const float mi = p.part_ml[(size_t)slot(i) * p.rows_max + row].x;
-            bad |= mi != mi;
-            m = fmaxf(m, mi);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                x[n][e] = 0.f;
+        for (int i0 = 0; i0 < c.parts; i0 += 32) {
+            const bool there = i0 + lane < c.parts;
+            const float2 ml = there ? p.part_ml[slot(i0 + lane) + row] : make_float2(-INFINITY, 0.f);
+            bad |= __any_sync(0xffffffffu, ml.x != ml.x);
+            float top = fmaxf(m, ml.x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float old = m == -INFINITY ? 0.f : ex2((m - top) * k2); // of what the parts before gave
+            const float f = ml.x == -INFINITY ? 0.f : ex2((ml.x - top) * k2);
+            m = top;
+            float sum = ml.y * f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = fmaf(l, old, sum);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    x[n][e] *= old;
+            const int here = min(32, c.parts - i0);
+#pragma unroll 4
+            for (int i = 0; i < here; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const float *const o = p.part_o + (slot(i0 + i) + row) * D + V * lane;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    float y[V];
+                    if constexpr (V == 4)
+                        *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(o + 32 * V * n);
+                    else
+                        *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(o + 32 * V * n);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) // a part without keys for this row has weight zero, and zeros
+                        x[n][e] = fmaf(y[e], fi, x[n][e]);
+                }
+            }
         }
-        float l = 0.f, x[D / 32];
+        T *const out = static_cast<T *>(p.a.out) + ((size_t)(c.tok + tok) * p.a.hq + c.head * p.g + (in - t * p.g)) * D + V * lane;
+        const float inv = 1.f / l;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            x[e] = 0.f;
-        for (int i = 0; i < c.parts; ++i) {
-            const float2 ml = p.part_ml[(size_t)slot(i) * p.rows_max + row];
-            if (ml.x == -INFINITY)
-                continue;
-            const float f = ex2((ml.x - m) * k2);
-            l = fmaf(ml.y, f, l);
-            const float *o = p.part_o + ((size_t)slot(i) * p.rows_max + row) * D;
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                x[e] = fmaf(o[e * 32 + lane], f, x[e]);
-        }
-        T *const out = static_cast<T *>(p.a.out) + ((size_t)(c.tok + tok) * p.a.hq + c.head * p.g + (in - t * p.g)) * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            out[e * 32 + lane] = from_f<T>(bad ? 0.f : x[e] / l);
+            for (int e = 0; e < V; ++e)
+                out[32 * V * n + e] = from_f<T>(bad ? 0.f : x[n][e] * inv);
     }
 }
 

@@ -21,6 +21,14 @@
 // merged at the item's end.  At d = 256 tensor memory holds one O, so one
 // group takes all steps.
 //
+// The products go out in the steps' order, P V of step i and then S of step i +
+// 2, so that one group's softmax runs beside the other's products; with a
+// product warp for each group the two fell into step and took turns with the
+// tensor cores instead (297 us against 286 for a 2,048-token chunk over 16 k).
+// The queue of products is a few deep, so the issuing warp is held up until
+// they are nearly done; the weights are handed over by halves, so that the
+// first half's product runs while the second half's are computed.
+//
 // O is rescaled only when a row's maximum has grown by over 2^8 since the
 // value in use (kLazy): weights then stay below 2^8 and sums in fp32 lose
 // nothing.
@@ -56,6 +64,7 @@ template <int D> struct Geo {
     static constexpr int NQ = NO;                        // Q tiles in shared memory
     static constexpr int THREADS = 128 + 128 * NO;
     static constexpr int QUEUE_READERS = 3 + 4 * NO;     // warps 0, 1, 2 and the softmax warps
+    static constexpr int HALVES = KT / 64;               // parts in which a step's weights are handed over
     // tensor memory columns
     static constexpr int S0 = 0;                         // S (and P) of step parity b: S0 + b KT
     static constexpr int O0 = 2 * KT;                    // O of accumulator o: O0 + o D
@@ -68,13 +77,14 @@ template <int D> struct Geo {
 struct Ctrl {
     unsigned long long full[12], empty[12];    // ring
     unsigned long long qfull[2], qempty[2];
-    unsigned long long sready[2], pready[2], odone[2];
+    unsigned long long sready[2], pready[2][2], odone[2];
     unsigned long long ifull[kQueue], iempty[kQueue];
+    unsigned long long drain; // the last products
     unsigned long long merge; // the two softmax groups, at the end of a single tile's item
     Item item[kQueue];
     int valid[kMeta];       // good rows of a key tile, by the tile's count
     long long scan[13];
-    long long found[2];     // this run's first row, by the plan
+    Found found;            // this run's first row, by the plan
     uint32_t tmem;
     float ml[2][128][2];    // (m, l) of the two groups' rows, for the merge
     int bad[2];             // first key that could not be read, by group
@@ -133,6 +143,20 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
 // Two bf16: whether both are finite; with zeros in the place of those that are not.
 __device__ __forceinline__ bool finite2(uint32_t w)
 {
@@ -159,7 +183,22 @@ __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
 #define R16(r, i) R4(r, i), R4(r, i + 4), R4(r, i + 8), R4(r, i + 12)
 #define I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
 #define I16(r, i) I4(r, i), I4(r, i + 4), I4(r, i + 8), I4(r, i + 12)
-// 64, 32 consecutive columns of this thread's lane
+// 128, 64, 32 consecutive columns of this thread's lane
+__device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[128])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+                 "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
+                 "%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+                 "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,"
+                 "%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,"
+                 "%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,"
+                 "%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127"
+                 "}, [%128];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R16(r, 0), R16(r, 16), R16(r, 32), R16(r, 48), R16(r, 64), R16(r, 80), R16(r, 96), R16(r, 112)
+                 : "r"(a)
+                 : "memory");
+}
 __device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[64])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
@@ -219,10 +258,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             mbar_init(bar(ctl.full[i]), 1), mbar_init(bar(ctl.empty[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ctl.qfull[i]), 1), mbar_init(bar(ctl.qempty[i]), 1);
-            mbar_init(bar(ctl.sready[i]), 1), mbar_init(bar(ctl.pready[i]), 4), mbar_init(bar(ctl.odone[i]), 1);
+            mbar_init(bar(ctl.sready[i]), 1), mbar_init(bar(ctl.odone[i]), 1);
+            mbar_init(bar(ctl.pready[i][0]), 4), mbar_init(bar(ctl.pready[i][1]), 4);
         }
         for (int i = 0; i < kQueue; ++i)
             mbar_init(bar(ctl.ifull[i]), 1), mbar_init(bar(ctl.iempty[i]), G::QUEUE_READERS);
+        mbar_init(bar(ctl.drain), 1);
         mbar_init(bar(ctl.merge), 8);
         ctl.dirty = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -235,7 +276,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const Run run = plan_run<G::THREADS, KT>(p, mt, ctl.scan, ctl.found);
-    zero_dead<bf16, D, G::THREADS>(p);
     bool alive = true; // false once a bounded wait ran out
     auto wait = [&](unsigned long long &b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
         if (alive && !__all_sync(0xffffffffu, mbar_wait(bar(b), parity))) {
@@ -252,7 +292,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
 
     if (warp < 4) {
         if constexpr (G::NO == 2)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 3) {
             // ---- the walk: this run's items, in order
             Walk walk(p, run, mt, KT);
@@ -359,16 +399,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 }
                 tiles += n;
             }
-            // after a wait that ran out: let the copies in flight land (each bounded)
-            if (!alive) {
-                const unsigned from = issued > (unsigned)G::STAGES ? issued - G::STAGES : 0;
-                for (unsigned i = from; i < issued; ++i)
-                    mbar_wait(bar(ctl.full[i % G::STAGES]), (i / G::STAGES) & 1);
-            }
+            // the last copies land before the CTA leaves, whoever still waits for them
+            for (unsigned i = issued > (unsigned)G::STAGES ? issued - G::STAGES : 0; i < issued; ++i)
+                mbar_wait(bar(ctl.full[i % G::STAGES]), (i / G::STAGES) & 1);
         } else if (warp == 1) {
             // ---- the products.  The whole warp walks, on values that the broadcasts make uniform to the compiler, and
             // one elected lane issues: an issue loop in a divergent branch took 1,970 cycles a step, twice the products'.
-            unsigned place0 = 0, qc = 0, scnt[2] = {0, 0};
+            unsigned place0 = 0, qc = 0, cnt[2] = {0, 0};
             for (int q = 0;; ++q) {
                 const int slot = q % kQueue;
                 if (!wait(ctl.ifull[slot], (q / kQueue) & 1))
@@ -384,6 +421,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 const int steps = pair ? 2 * n : n, qn = pair ? 2 : 1;
                 for (int i = 0; i < qn; ++i)
                     wait(ctl.qfull[(qc + i) % G::NQ], ((qc + i) / G::NQ) & 1);
+                // The places of the ring are waited for in order, every one: a parity wait tells a phase only from the
+                // one before it, and copies may land out of order.
                 auto s_step = [&](int i) {
                     const int j = pair ? i >> 1 : i, b = i & 1;
                     const unsigned pl = place0 + k_place(pair, j);
@@ -415,18 +454,28 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     const int j = pair ? i >> 1 : i, b = i & 1, o = G::NO == 2 ? b : 0;
                     const unsigned pl = place0 + v_place(pair, j, n);
                     const int st = pl % G::STAGES;
-                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1) || !wait(ctl.pready[b], scnt[b] & 1))
+                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
                         break;
-                    ++scnt[b];
-                    after_sync();
                     const uint64_t vd = desc_mn(stage_addr(st), KT * 128);
-                    const bool more = G::NO == 2 ? i >= 2 : i >= 1;
-                    if (elect()) {
+                    const bool more = i >= G::NO;
 #pragma unroll
-                        for (int k = 0; k < KT / 16; ++k)
-                            mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, vd + k * (2048 >> 4), idesc(D, true),
-                                   k > 0 || more);
-                        // O is waited for at an item's end and, with one group, before it is rescaled
+                    for (int half = 0; half < G::HALVES; ++half) {
+                        if (!wait(ctl.pready[b][half], cnt[b] & 1))
+                            break;
+                        after_sync();
+                        if (elect()) {
+#pragma unroll
+                            for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, vd + k * (2048 >> 4),
+                                       idesc(D, true), k > 0 || more);
+                        }
+                        __syncwarp();
+                    }
+                    ++cnt[b];
+                    if (!alive)
+                        break;
+                    // O is waited for at an item's end and, with one group, before it is rescaled
+                    if (elect()) {
                         if (G::NO == 1 || i + 2 >= steps)
                             commit(bar(ctl.odone[b]));
                         if (!pair || b)
@@ -441,6 +490,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 if (!alive)
                     break;
             }
+            // everything issued is done, and has said so, before tensor memory and the barriers go
+            if (elect())
+                commit(bar(ctl.drain));
+            __syncwarp();
+            mbar_wait(bar(ctl.drain), 0);
         } else {
             // ---- Q tiles, by 16-byte asynchronous copies
             unsigned qc = 0;
@@ -483,8 +537,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
         }
     } else {
         if constexpr (G::NO == 2)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        // ---- softmax: a thread a row
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        // ---- softmax: a thread a row; first, zeros where no live row writes
+        zero_dead<bf16, D, 128 * G::NO>(p, tid - 128);
         const int grp = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // 32 tensor-memory lanes a warp
         const float c = a.scale * 1.44269504088896341f;    // weights are 2^(c (s - m))
@@ -527,23 +582,52 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 const int valid = *reinterpret_cast<volatile int *>(&ctl.valid[(tiles + j) % kMeta]);
                 if (valid < min(KT, end - key))
                     broken = min(broken, key + valid);
+                const int later = max(0, it.see - key); // keys of the tile from here on are hidden from some tokens
+                // A weight of zero does not hide a NaN or an infinity.  Rows of V past the good ones may hold anything:
+                // they become zeros.  Elements that only some tokens see become zeros too where they are not finite,
+                // and the item's end adds them to the rows that do see them.
+                auto clean = [&] {
+                    if (later >= KT)
+                        return true;
+                    const unsigned pl = place0 + v_place(pair, j, n);
+                    const int st = pl % G::STAGES;
+                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
+                        return false;
+                    unsigned char *const v = smem + G::RING + st * G::SBYTES;
+                    for (int x = row; x < (KT - later) * 8 * G::CH; x += 128) {
+                        const int ch = x / ((KT - later) * 8), y = x - ch * (KT - later) * 8;
+                        uint4 *const at = reinterpret_cast<uint4 *>(v + ch * KT * 128 + later * 128 + y * 16);
+                        if (later + (y >> 3) >= valid) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            uint4 z = *at;
+                            if (!(finite2(z.x) && finite2(z.y) && finite2(z.z) && finite2(z.w))) {
+                                *reinterpret_cast<volatile int *>(&ctl.dirty) = q + 1;
+                                __threadfence_block(); // before the zeros: the other group may scan this tile too
+                                z.x = drop2(z.x), z.y = drop2(z.y), z.z = drop2(z.z), z.w = drop2(z.w);
+                                *at = z;
+                            }
+                        }
+                    }
+                    smem_to_async();
+                    __syncwarp(); // what follows is for whole warps
+                    return true;
+                };
                 if (!idle) {
                     const uint32_t sa = tmem + lanes + G::S0 + b * KT;
                     float s[KT];
-#pragma unroll
-                    for (int k = 0; k < KT; k += 64)
-                        tld(sa + k, *reinterpret_cast<uint32_t(*)[64]>(&s[k]));
+                    tld(sa, *reinterpret_cast<uint32_t(*)[KT]>(&s[0]));
                     const int nv = min(valid, see - key);
                     if (__any_sync(0xffffffffu, nv < KT)) {
 #pragma unroll
                         for (int k = 0; k < KT; ++k)
                             s[k] = k < nv ? s[k] : -INFINITY;
                     }
-                    float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+                    float t[4] = {m, s[0], s[1], s[2]};
 #pragma unroll
-                    for (int k = 4; k < KT; k += 4)
-                        t0 = fmaxf(t0, s[k]), t1 = fmaxf(t1, s[k + 1]), t2 = fmaxf(t2, s[k + 2]), t3 = fmaxf(t3, s[k + 3]);
-                    const float top = fmaxf(m, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
+                    for (int k = 3; k + 1 < KT; k += 2)
+                        t[(k >> 1) & 3] = max3(t[(k >> 1) & 3], s[k], s[k + 1]);
+                    const float top = fmaxf(max3(t[0], t[1], t[2]), fmaxf(t[3], s[KT - 1]));
                     const bool grow = (top - m) * c > kLazy; // -inf to -inf is no growth
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2((m - top) * c) : 1.f;
@@ -573,56 +657,42 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     }
                     const float shift = m == -INFINITY ? 0.f : -m * c;
                     const float2 c2 = make_float2(c, c), sh2 = make_float2(shift, shift);
-                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+                    if (!clean())
+                        break;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int k0 = 0; k0 < KT; k0 += 64) {
+                    for (int half = 0; half < G::HALVES; ++half) {
                         uint32_t w[32];
 #pragma unroll
-                        for (int k = 0; k < 64; k += 4) {
-                            float2 x = fma2(make_float2(s[k0 + k], s[k0 + k + 1]), c2, sh2);
-                            float2 y = fma2(make_float2(s[k0 + k + 2], s[k0 + k + 3]), c2, sh2);
-                            x.x = ex2(x.x), x.y = ex2(x.y), y.x = ex2(y.x), y.y = ex2(y.y);
-                            l0 += x.x, l1 += x.y, l2 += y.x, l3 += y.y;
-                            const __nv_bfloat162 hx = __floats2bfloat162_rn(x.x, x.y), hy = __floats2bfloat162_rn(y.x, y.y);
+                        for (int k = 0; k < 64; k += 2) {
+                            float2 x = fma2(make_float2(s[64 * half + k], s[64 * half + k + 1]), c2, sh2);
+                            x.x = ex2(x.x), x.y = ex2(x.y);
+                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], x);
+                            const __nv_bfloat162 hx = __floats2bfloat162_rn(x.x, x.y);
                             w[k / 2] = *reinterpret_cast<const uint32_t *>(&hx);
-                            w[k / 2 + 1] = *reinterpret_cast<const uint32_t *>(&hy);
                         }
-                        tst(sa + k0 / 2, w);
+                        tst(sa + 32 * half, w);
+                        tst_wait();
+                        before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(ctl.pready[b][half]));
+                        __syncwarp();
                     }
-                    l += (l0 + l1) + (l2 + l3);
-                    tst_wait();
-                }
-                const int later = max(0, it.see - key); // keys of the tile from here on are hidden from some tokens
-                if (later < KT) {
-                    // A weight of zero does not hide a NaN or an infinity.  Rows of V past the good ones may hold
-                    // anything: they become zeros.  Elements that only some tokens see become zeros too where they
-                    // are not finite, and the item's end adds them to the rows that do see them.
-                    const unsigned pl = place0 + v_place(pair, j, n);
-                    const int st = pl % G::STAGES;
-                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+                } else {
+                    if (!clean())
                         break;
-                    unsigned char *const v = smem + G::RING + st * G::SBYTES;
-                    for (int x = row; x < (KT - later) * 8 * G::CH; x += 128) {
-                        const int ch = x / ((KT - later) * 8), y = x - ch * (KT - later) * 8;
-                        uint4 *const at = reinterpret_cast<uint4 *>(v + ch * KT * 128 + later * 128 + y * 16);
-                        if (later + (y >> 3) >= valid) {
-                            *at = make_uint4(0, 0, 0, 0);
-                        } else {
-                            uint4 z = *at;
-                            if (!(finite2(z.x) && finite2(z.y) && finite2(z.z) && finite2(z.w))) {
-                                *reinterpret_cast<volatile int *>(&ctl.dirty) = q + 1;
-                                __threadfence_block(); // before the zeros: the other group may scan this tile too
-                                z.x = drop2(z.x), z.y = drop2(z.y), z.z = drop2(z.z), z.w = drop2(z.w);
-                                *at = z;
-                            }
-                        }
+                    before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(ctl.pready[b][0]));
+                        if (G::HALVES == 2)
+                            mbar_arrive(bar(ctl.pready[b][1]));
                     }
-                    smem_to_async();
+                    __syncwarp();
                 }
-                before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(ctl.pready[b]));
             }
             // steps of the other group, which its counters follow
             if (G::NO == 2)
@@ -807,7 +877,7 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
     e = launch_pdl(attn_tc_kernel<D>, dim3(kCtas), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<bf16, D>, dim3(kCtas, p.rows_max > 32 ? 8 : 1), dim3(128), 0, s, p);
+    return launch_pdl(attn_combine_kernel<bf16, D>, dim3(kCtas, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
 }
 
 } // namespace

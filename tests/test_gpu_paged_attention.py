@@ -71,6 +71,18 @@ def test_many_short_rows(gdn):
     check_attention(out, *attention_ref(c, q, new, 0.125), "bf16")
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (8, 2, 256)])
+def test_long_and_single_tile_rows_in_turn(gdn, hq, hkv, d):
+    """Runs of several rows each, of one key tile and of many: the parts of the kernel that take turns on tiles meet again."""
+    rng = np.random.default_rng(d)
+    lens = [int(rng.integers(1, 100)) if r % 4 else int(rng.integers(1500, 3000)) for r in range(160)]
+    new = [1 if r % 5 else min(70, lens[r]) for r in range(160)]
+    c = Cache(lens, "bf16", hkv, d, 16, seed=d, poison=float("nan"))
+    q, out = run(gdn, c, new, hq)
+    check_attention(out, *attention_ref(c, q, new, d ** -0.5), "bf16")
+    assert gdn.get_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_peaked_and_large_scores(gdn, dtype):
     """Scores of some hundreds, whose maximum comes late: earlier sums are scaled down to nothing."""
