@@ -277,13 +277,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
 
     const Run run = plan_run<G::THREADS, KT>(p, mt, ctl.scan, ctl.found);
     bool alive = true; // false once a bounded wait ran out
-    auto wait = [&](unsigned long long &b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
-        if (alive && !__all_sync(0xffffffffu, mbar_wait(bar(b), parity))) {
+    auto wait_at = [&](uint32_t b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
+        if (!__all_sync(0xffffffffu, mbar_try(b, parity)) && alive && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
             alive = false;
             report(a.err, GDN_DEVERR_TIMEOUT);
         }
         return alive;
     };
+    auto wait = [&](unsigned long long &b, uint32_t parity) { return wait_at(bar(b), parity); };
     auto stage_addr = [&](int s) { return sbase + G::RING + s * G::SBYTES; };
     // place of the item's K and V tiles in the ring's order: one tile at a time K0 K1 V0 K2 V1 ... (a single tile's
     // steps look one key tile ahead), in pairs K0 V0 K1 V1 ...
@@ -405,7 +406,20 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
         } else if (warp == 1) {
             // ---- the products.  The whole warp walks, on values that the broadcasts make uniform to the compiler, and
             // one elected lane issues: an issue loop in a divergent branch took 1,970 cycles a step, twice the products'.
-            unsigned place0 = 0, qc = 0, cnt[2] = {0, 0};
+            // The queue runs dry in the time between a step's last product and the next one's first: what can be waited
+            // for ahead is.
+            const bool leader = elect();
+            int st = 0, kst = 0, vst = 0; // the ring's next place; the places of the K and V tiles in use
+            uint32_t parity = 0, pparity[2] = {0, 0};
+            unsigned qc = 0;
+            const uint32_t full0 = bar(ctl.full[0]), empty0 = bar(ctl.empty[0]);
+            // The places of the ring are waited for in order, every one: a parity wait tells a phase only from the one
+            // before it, and copies may land out of order.
+            auto advance = [&](int &at) {
+                at = st;
+                if (++st == G::STAGES)
+                    st = 0, parity ^= 1;
+            };
             for (int q = 0;; ++q) {
                 const int slot = q % kQueue;
                 if (!wait(ctl.ifull[slot], (q / kQueue) & 1))
@@ -421,77 +435,83 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 const int steps = pair ? 2 * n : n, qn = pair ? 2 : 1;
                 for (int i = 0; i < qn; ++i)
                     wait(ctl.qfull[(qc + i) % G::NQ], ((qc + i) / G::NQ) & 1);
-                // The places of the ring are waited for in order, every one: a parity wait tells a phase only from the
-                // one before it, and copies may land out of order.
-                auto s_step = [&](int i) {
-                    const int j = pair ? i >> 1 : i, b = i & 1;
-                    const unsigned pl = place0 + k_place(pair, j);
-                    const int st = pl % G::STAGES;
-                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
-                        return;
+                const uint32_t q0 = sbase + (qc % G::NQ) * G::QBYTES, q1 = pair ? sbase + ((qc + 1) % G::NQ) * G::QBYTES : q0;
+                bool v_here = false; // the next V tile has landed
+                // S of a step of parity b
+                auto s_step = [&](int i, const int b) {
+                    if (!pair || b == 0) {
+                        if (!wait_at(full0 + 8 * st, parity))
+                            return;
+                        advance(kst);
+                    }
+                    // V of the step whose product is next (in pairs a V tile serves two steps)
+                    v_here = (!pair || b == 1) && i > 1 && __all_sync(0xffffffffu, mbar_try(full0 + 8 * st, parity));
                     after_sync();
-                    const uint64_t qd = desc_k(sbase + ((qc + (pair ? b : 0)) % G::NQ) * G::QBYTES), kd = desc_k(stage_addr(st));
-                    if (elect()) {
+                    const uint64_t qd = desc_k(b ? q1 : q0), kd = desc_k(stage_addr(kst));
+                    if (leader) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             mma_ss(tmem + G::S0 + b * KT, qd + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
                                    kd + (((k >> 2) * KT * 128 + (k & 3) * 32) >> 4), idesc(KT, false), k > 0);
                         commit(bar(ctl.sready[b]));
                         if (!pair || b)
-                            commit(bar(ctl.empty[st]));
+                            commit(empty0 + 8 * kst);
                         if (i == steps - 1)
                             for (int k = 0; k < qn; ++k)
                                 commit(bar(ctl.qempty[(qc + k) % G::NQ]));
                     }
-                    __syncwarp();
                 };
-                if (!alive)
-                    break;
-                s_step(0);
-                if (steps > 1)
-                    s_step(1);
-                for (int i = 0; i < steps && alive; ++i) {
-                    const int j = pair ? i >> 1 : i, b = i & 1, o = G::NO == 2 ? b : 0;
-                    const unsigned pl = place0 + v_place(pair, j, n);
-                    const int st = pl % G::STAGES;
-                    if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
-                        break;
-                    const uint64_t vd = desc_mn(stage_addr(st), KT * 128);
+                // P V of step i, of parity b, then S of step i + 2
+                auto step = [&](int i, const int b) {
+                    const int o = G::NO == 2 ? b : 0;
+                    if (!pair || b == 0) {
+                        if (!v_here && !wait_at(full0 + 8 * st, parity))
+                            return;
+                        advance(vst);
+                    }
+                    v_here = false;
+                    const uint64_t vd = desc_mn(stage_addr(vst), KT * 128);
                     const bool more = i >= G::NO;
 #pragma unroll
                     for (int half = 0; half < G::HALVES; ++half) {
-                        if (!wait(ctl.pready[b][half], cnt[b] & 1))
-                            break;
+                        if (!wait(ctl.pready[b][half], pparity[b]))
+                            return;
                         after_sync();
-                        if (elect()) {
+                        if (leader) {
 #pragma unroll
                             for (int k = 4 * half; k < 4 * half + 4; ++k)
                                 mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, vd + k * (2048 >> 4),
                                        idesc(D, true), k > 0 || more);
+                            if (half == G::HALVES - 1) {
+                                // O is waited for at an item's end and, with one group, before it is rescaled
+                                if (G::NO == 1 || i + 2 >= steps)
+                                    commit(bar(ctl.odone[b]));
+                                if (!pair || b)
+                                    commit(empty0 + 8 * vst);
+                            }
                         }
-                        __syncwarp();
                     }
-                    ++cnt[b];
-                    if (!alive)
-                        break;
-                    // O is waited for at an item's end and, with one group, before it is rescaled
-                    if (elect()) {
-                        if (G::NO == 1 || i + 2 >= steps)
-                            commit(bar(ctl.odone[b]));
-                        if (!pair || b)
-                            commit(bar(ctl.empty[st]));
-                    }
-                    __syncwarp();
+                    pparity[b] ^= 1;
                     if (i + 2 < steps)
-                        s_step(i + 2);
+                        s_step(i + 2, b);
+                };
+                if (!alive)
+                    break;
+                s_step(0, 0);
+                if (steps > 1)
+                    s_step(1, 1);
+                for (int i = 0; i < steps && alive; i += 2) {
+                    step(i, 0);
+                    if (i + 1 < steps)
+                        step(i + 1, 1);
                 }
-                place0 += 2 * n;
                 qc += qn;
                 if (!alive)
                     break;
             }
             // everything issued is done, and has said so, before tensor memory and the barriers go
-            if (elect())
+            __syncwarp();
+            if (leader)
                 commit(bar(ctl.drain));
             __syncwarp();
             mbar_wait(bar(ctl.drain), 0);
