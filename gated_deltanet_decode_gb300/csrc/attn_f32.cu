@@ -11,11 +11,11 @@
 // stand as WR row blocks of 16 x WK shares of a tile's keys.  Few rows (decode)
 // take WR small and split the keys instead.  Each warp keeps its own O, m and
 // l; the shares are joined through shared memory at the item's end.  K and V
-// tiles come by 16-byte asynchronous copies, one tile ahead.
+// tiles come by 16-byte asynchronous copies, three tiles ahead.
 //
 // A weight of zero does not hide a NaN or an infinity, and infinity has no
-// tail: elements of V that are not finite are left out of the products, and
-// the item's end adds them to the rows that see them.
+// tail: elements of V that are not finite are zeroed as they land, and the
+// item's end adds them to the rows that see them.
 #include "attn_plan.cuh"
 
 #include <atomic>
@@ -26,13 +26,15 @@ namespace {
 constexpr int kThreads = 256;
 
 template <int D> struct Geo32 {
-    static constexpr int KT = D == 256 ? 32 : 64;  // keys a tile
+    static constexpr int KT = D == 256 ? 16 : 32;  // keys a tile
     static constexpr int LD = D + 4;               // row stride: fragment reads hit 32 banks
-    static constexpr int WRB = D == 256 ? 4 : 8;   // row blocks with many rows,
-    static constexpr int WRS = D == 256 ? 2 : 1;   // and with up to 16 WRS rows
+    static constexpr int WRB = D == 256 ? 4 : 8;   // row blocks with many rows: 8 / WRB shares of a tile,
+    static constexpr int WRS = D == 256 ? 2 : 1;   // and with up to 16 WRS rows: 8 / WRS shares of two tiles
     static constexpr int M = 16 * WRB;
     static constexpr int TILE = KT * LD;           // floats of a K or V tile
-    static constexpr int FLOATS = M * LD + 4 * TILE;
+    static constexpr int STAGES = 4;               // tiles of K and V in shared memory: about 100 KB an SM under way
+    static constexpr int FLOATS = M * LD + 2 * STAGES * TILE;
+    static constexpr int PER_SM = D == 64 ? 2 : 1; // CTAs an SM, by shared memory
 };
 
 struct Ctrl32 {
@@ -43,11 +45,18 @@ struct Ctrl32 {
     float2 ml[8 * 16]; // (m, l) by (share, row): 128 pairs in every form
 };
 
+// The head is x cut to the 11 bits that a product reads; the tail, exact, has 13,
+// of which it reads 11.  (Rounding the head would save one of them, and the
+// conversion costs as much as a product.)
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
 {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    lo = __float_as_uint(x - __uint_as_float(hi)); // the product reads its leading 11 bits
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
+template <int N> struct Width {
+    static constexpr int value = N;
+};
+__device__ __forceinline__ bool odd(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; } // not finite
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -68,11 +77,11 @@ __device__ __forceinline__ void copy16(float *dst, const float *src, bool there)
 // 4, so the weights are an A fragment as they stand.
 template <int D, int NT>
 __device__ __forceinline__ void tile_step(const float *q, const float *k, const float *v, int see0, int see8, float c2,
-                                          float (&o)[D / 8][4], float &m0, float &m8, float &l0, float &l8, bool &odd)
+                                          float (&o)[D / 8][4], float &m0, float &m8, float &l0, float &l8)
 {
     constexpr int LD = Geo32<D>::LD;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    constexpr int CHAINS = NT == 1 ? 2 : 1; // a single column tile: two sums, for latency
+    constexpr int CHAINS = NT == 1 ? 4 : 1; // a single column tile: four sums, for latency
     float s[NT][CHAINS][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -95,7 +104,7 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
             uint32_t h0, h1, t0, t1;
             split(kp[0], h0, t0);
             split(kp[4], h1, t1);
-            float(&d)[4] = s[n][CHAINS == 2 ? ks & 1 : 0];
+            float(&d)[4] = s[n][ks % CHAINS];
             mma8(d, al, h0, h1);
             mma8(d, ah, t0, t1);
             mma8(d, ah, h0, h1);
@@ -107,9 +116,9 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            if (CHAINS == 2) {
-                s[n][0][e] += s[n][CHAINS - 1][e];
-                s[n][0][e + 2] += s[n][CHAINS - 1][e + 2];
+            if (CHAINS == 4) {
+                s[n][0][e] = (s[n][0][e] + s[n][1 % CHAINS][e]) + (s[n][2 % CHAINS][e] + s[n][3 % CHAINS][e]);
+                s[n][0][e + 2] = (s[n][0][e + 2] + s[n][1 % CHAINS][e + 2]) + (s[n][2 % CHAINS][e + 2] + s[n][3 % CHAINS][e + 2]);
             }
             const int at = 8 * n + 2 * c + e;
             s[n][0][e] = at < see0 ? s[n][0][e] : -INFINITY;
@@ -142,13 +151,9 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
         const float *vp = v + (8 * n + 2 * c) * LD + g;
 #pragma unroll
         for (int e = 0; e < D / 8; ++e) {
-            float x = vp[8 * e], y = vp[8 * e + LD];
-            const bool fx = fabsf(x) < INFINITY, fy = fabsf(y) < INFINITY;
-            odd |= !fx | !fy;
-            x = fx ? x : 0.f, y = fy ? y : 0.f;
             uint32_t h0, h1, t0, t1;
-            split(x, h0, t0);
-            split(y, h1, t1);
+            split(vp[8 * e], h0, t0);
+            split(vp[8 * e + LD], h1, t1);
             mma8(o[e], al, h0, h1);
             mma8(o[e], ah, t0, t1);
             mma8(o[e], ah, h0, h1);
@@ -156,7 +161,7 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
     }
 }
 
-template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const WorkArgs p)
+template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(const WorkArgs p)
 {
     typedef Geo32<D> G;
     constexpr int KT = G::KT, LD = G::LD;
@@ -189,7 +194,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(
         const int32_t *const table = a.c.table + (size_t)it.row * a.c.max_pages;
         const int kvh = it.head / p.groups, rows = it.ntok * p.g, end = it.see + it.ntok - 1;
         const bool few = rows <= 16 * G::WRS;
-        const int wr_n = few ? G::WRS : G::WRB, wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n;
+        const int wr_n = few ? G::WRS : G::WRB, wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n; // row block, share
         // Q: token rows of this head group
         {
             const float *const src = static_cast<const float *>(a.q) + (size_t)it.tok * a.q_stride + (size_t)it.head * p.g * D;
@@ -199,52 +204,87 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(
                 copy16(Q + row * LD + 4 * vec, there ? src + (size_t)t * a.q_stride + (row - t * p.g) * D + 4 * vec : src, there);
             }
         }
-        auto load = [&](int j) {
-            float *const K = ring + (j & 1) * 2 * G::TILE, *const V = K + G::TILE;
-            for (int x = tid; x < KT * (D / 4); x += kThreads) {
-                const int row = x / (D / 4), vec = x - row * (D / 4), key = (it.ja + j) * KT + row;
-                int page = 0;
-                if (key < end) {
-                    page = table[key >> a.pages.page_shift];
-                    if (page <= 0 || page >= a.pages.num_pages) {
-                        page = 0;
-                        atomicMin(&ctl.broken, key);
-                        report(a.err, GDN_DEVERR_BAD_PAGE);
+        const int n = it.jb - it.ja;
+        auto load = [&](int j) { // a group a tile, empty past the last; a thread keeps its column
+            constexpr int VR = D / 4 < kThreads ? D / 4 : kThreads, RP = kThreads / VR; // vectors a row, rows a pass
+            float *const K = ring + j % G::STAGES * 2 * G::TILE, *const V = K + G::TILE;
+            const int col = 4 * (tid % VR);
+            if (j < n) {
+#pragma unroll
+                for (int r = 0; r < KT; r += RP) {
+                    const int row = r + tid / VR, key = (it.ja + j) * KT + row;
+                    int page = 0;
+                    if (key < end) {
+                        page = table[key >> a.pages.page_shift];
+                        if (page <= 0 || page >= a.pages.num_pages) {
+                            page = 0;
+                            atomicMin(&ctl.broken, key);
+                            report(a.err, GDN_DEVERR_BAD_PAGE);
+                        }
                     }
+                    const size_t at = (((size_t)page * hkv + kvh) * ps + (key & (ps - 1))) * D + col;
+                    copy16(K + row * LD + col, static_cast<const float *>(a.pages.k) + at, page > 0);
+                    copy16(V + row * LD + col, static_cast<const float *>(a.pages.v) + at, page > 0);
                 }
-                const size_t at = (((size_t)page * hkv + kvh) * ps + (key & (ps - 1))) * D + 4 * vec;
-                copy16(K + row * LD + 4 * vec, static_cast<const float *>(a.pages.k) + at, page > 0);
-                copy16(V + row * LD + 4 * vec, static_cast<const float *>(a.pages.v) + at, page > 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // the elements of V that this thread copied: what is not finite becomes zero
+        auto scan = [&](int j) {
+            constexpr int VR = D / 4 < kThreads ? D / 4 : kThreads, RP = kThreads / VR;
+            float *const V = ring + (j % G::STAGES * 2 + 1) * G::TILE;
+#pragma unroll
+            for (int r = 0; r < KT; r += RP) {
+                uint4 *const at = reinterpret_cast<uint4 *>(V + (r + tid / VR) * LD + 4 * (tid % VR));
+                uint4 v = *at;
+                if (odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w)) {
+                    v = make_uint4(odd(v.x) ? 0u : v.x, odd(v.y) ? 0u : v.y, odd(v.z) ? 0u : v.z, odd(v.w) ? 0u : v.w);
+                    *at = v;
+                    ctl.dirty = 1;
+                }
+            }
         };
         const int r0 = 16 * wr + g, r8 = r0 + 8;
         const int s0 = r0 < rows ? it.see + r0 / p.g : 0, s8 = r8 < rows ? it.see + r8 / p.g : 0; // keys the rows see
         float o[D / 8][4], m0 = -INFINITY, m8 = -INFINITY, l0 = 0.f, l8 = 0.f;
-        bool odd = false;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        const int n = it.jb - it.ja;
-        load(0);
-        for (int j = 0; j < n; ++j) {
-            if (j + 1 < n) {
-                load(j + 1);
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // this warp's step on tile j, on keys kb .. of it
+        auto work = [&](int j, int kb, auto nt) {
+            const int key = (it.ja + j) * KT + kb;
+            const float *const K = ring + j % G::STAGES * 2 * G::TILE + kb * LD;
+            tile_step<D, decltype(nt)::value>(Q + 16 * wr * LD, K, K + G::TILE, s0 - key, s8 - key, c2, o, m0, m8, l0, l8);
+        };
+        for (int j = 0; j < G::STAGES - 1; ++j)
+            load(j);
+        if (few) { // two tiles at a time: 8 keys a warp
+            constexpr int SH = KT / 8; // shares of a tile
+            for (int j = 0; j < n; j += 2) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(G::STAGES - 3) : "memory");
+                scan(j);
+                if (j + 1 < n)
+                    scan(j + 1);
+                __syncthreads(); // the tiles are there for all
+                load(j + G::STAGES - 1);
+                const int mine = j + wk / SH;
+                if (16 * wr < rows && mine < n)
+                    work(mine, wk % SH * 8, Width<1>());
+                __syncthreads(); // and done with
+                load(j + G::STAGES);
             }
-            __syncthreads();
-            if (16 * wr < rows) {
-                const int kb = wk * (KT / wk_n), key = (it.ja + j) * KT + kb;
-                const float *const K = ring + (j & 1) * 2 * G::TILE + kb * LD, *const V = K + G::TILE;
-                if (few)
-                    tile_step<D, KT * G::WRS / 64>(Q + 16 * wr * LD, K, V, s0 - key, s8 - key, c2, o, m0, m8, l0, l8, odd);
-                else
-                    tile_step<D, KT * G::WRB / 64>(Q + 16 * wr * LD, K, V, s0 - key, s8 - key, c2, o, m0, m8, l0, l8, odd);
+        } else {
+            for (int j = 0; j < n; ++j) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(G::STAGES - 2) : "memory");
+                scan(j);
+                __syncthreads(); // the tile is there for all, and the one before it is done with
+                load(j + G::STAGES - 1);
+                if (16 * wr < rows)
+                    work(j, wk * (KT / (8 / G::WRB)), Width<KT * G::WRB / 64>());
             }
-            __syncthreads();
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
         // the shares' sums to shared memory, in place of the tiles
 #pragma unroll
         for (int x = 1; x < 4; x <<= 1) {
@@ -260,8 +300,6 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(
             }
             if (c == 0)
                 ctl.ml[wk * 16 * wr_n + r0] = make_float2(m0, l0), ctl.ml[wk * 16 * wr_n + r8] = make_float2(m8, l8);
-            if (odd)
-                ctl.dirty = 1;
         }
         __syncthreads();
         const float NaN = __int_as_float(0x7fc00000);
@@ -330,21 +368,22 @@ template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
     p.g = group_heads(a.hq, a.pages.hkv, G::M);
     p.groups = a.hq / a.pages.hkv / p.g;
     p.tq = G::M / p.g;
+    p.runs = kSms * G::PER_SM;
     p.rows_max = slot_rows32(G::M, p.g, a.c.total_tokens);
     p.second = 0;
     work_layout(p);
-    e = launch_pdl(attn_f32_kernel<D>, dim3(kCtas), dim3(kThreads), (size_t)G::FLOATS * 4, s, p);
+    e = launch_pdl(attn_f32_kernel<D>, dim3(p.runs), dim3(kThreads), (size_t)G::FLOATS * 4, s, p);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<float, D>, dim3(kCtas, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
+    return launch_pdl(attn_combine_kernel<float, D>, dim3(p.runs, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
 }
 
 } // namespace
 
 size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens)
 {
-    const int m = d == 256 ? Geo32<256>::M : Geo32<128>::M;
-    return work_bytes(d, slot_rows32(m, group_heads(hq, hkv, m), total_tokens));
+    const int m = d == 256 ? Geo32<256>::M : Geo32<128>::M; // 64 as 128
+    return work_bytes(d, kSms * (d == 64 ? Geo32<64>::PER_SM : 1), slot_rows32(m, group_heads(hq, hkv, m), total_tokens));
 }
 
 cudaError_t launch_paged_attention_f32(const AttentionArgs &a, cudaStream_t s)

@@ -15,7 +15,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kCtas = 152; // runs: one CTA an SM
+constexpr int kSms = 152;
 
 struct Item {
     int tok, ntok, head, row; // first token, tokens, head group, cache row
@@ -35,23 +35,24 @@ struct Cut {
 struct WorkArgs {
     AttentionArgs a;
     int g, groups, tq; // heads a group, groups a key head, tokens a tile
+    int runs;          // CTAs
     int rows_max;      // rows of a workspace slot
     int second;        // rows before an item's second tile (0: items have one tile)
-    float *part_o;     // [2 kCtas][rows_max][D]
+    float *part_o;     // [2 runs][rows_max][D]
     float2 *part_ml;
-    Cut *cuts;         // [kCtas]
+    Cut *cuts;         // [runs]
 };
 
 // The workspace: cuts, then (m, l) and O of the cut items' parts.
-inline size_t work_bytes(int d, int rows_max)
+inline size_t work_bytes(int d, int runs, int rows_max)
 {
-    return sizeof(Cut) * kCtas + 2 * (size_t)kCtas * rows_max * (sizeof(float2) + sizeof(float) * d);
+    return sizeof(Cut) * runs + 2 * (size_t)runs * rows_max * (sizeof(float2) + sizeof(float) * d);
 }
 inline void work_layout(WorkArgs &p)
 {
     p.cuts = static_cast<Cut *>(p.a.work);
-    p.part_ml = reinterpret_cast<float2 *>(p.cuts + kCtas);
-    p.part_o = reinterpret_cast<float *>(p.part_ml + 2 * (size_t)kCtas * p.rows_max);
+    p.part_ml = reinterpret_cast<float2 *>(p.cuts + p.runs);
+    p.part_o = reinterpret_cast<float *>(p.part_ml + 2 * (size_t)p.runs * p.rows_max);
 }
 // Heads a group: the largest divisor of hq / hkv that a tile of `rows` rows holds.
 inline int group_heads(int hq, int hkv, int rows)

@@ -882,6 +882,7 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
     p.g = group_heads(a.hq, a.pages.hkv, 128);
     p.groups = a.hq / a.pages.hkv / p.g;
     p.tq = 128 / p.g;
+    p.runs = kSms; // one CTA an SM: its tensor memory is taken whole
     p.rows_max = slot_rows(D, p.g, a.c.total_tokens);
     p.second = G::NO == 2 ? 128 : 0;
     work_layout(p);
@@ -894,17 +895,17 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
             pool.mapped = true;
         }
     }
-    e = launch_pdl(attn_tc_kernel<D>, dim3(kCtas), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
+    e = launch_pdl(attn_tc_kernel<D>, dim3(p.runs), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<bf16, D>, dim3(kCtas, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
+    return launch_pdl(attn_combine_kernel<bf16, D>, dim3(p.runs, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
 }
 
 } // namespace
 
 size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens)
 {
-    return work_bytes(d, slot_rows(d, group_heads(hq, hkv, 128), total_tokens));
+    return work_bytes(d, kSms, slot_rows(d, group_heads(hq, hkv, 128), total_tokens));
 }
 
 cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s)
