@@ -689,6 +689,8 @@ class KVPagePool:
         _check(L.kv_page_pool_wrap(_ptr(k, "k"), _ptr(v, "v", None, k.device), num_pages, page_size, layers, hkv, d,
                                    self._code, ctypes.byref(h)))
         self._h = h
+        self._fast = _lib.fast()  # the C++ binding and the pool as it takes it
+        self._p = self._fast.make_pool(h.value, hkv, d, self._code, self.device.index) if self._fast else None
 
     @property
     def handle(self):
@@ -698,10 +700,12 @@ class KVPagePool:
         h = getattr(self, "_h", None)
         if h is not None and h.value:
             try:
+                if self._p:
+                    self._fast.drop_pool(self._p)
                 _lib.load().kv_page_pool_destroy(h)
             except Exception:
                 pass
-            self._h = None
+            self._h = self._p = None
 
 
 class KVPageMoves:
@@ -721,8 +725,16 @@ class KVPageMoves:
                 _arg(self.count, 1, i32, dev, "moves"))
 
 
-# A decode step makes a few of these calls a layer, each of some microseconds on the GPU: the helpers below look at a
-# tensor once, and only then at what is wrong with it.
+# A decode step makes a few of these calls a layer, each of some microseconds on the GPU.  The C++ binding makes those
+# that are in order; the helpers below, for the others and where it was not built, look at a tensor once, and only then at
+# what is wrong with it.
+
+
+def _made(r):
+    """What the C++ binding returned, with a status raised as an error."""
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def _raw_stream(dev: torch.device) -> int:
@@ -767,6 +779,11 @@ def attn_prologue(q, k, v, pool: KVPagePool, rope: Optional[torch.Tensor], table
     q [T][hq][d], k, v [T][hkv][d] (views of a packed projection are fine); row r's tokens are cu_seqlens[r] ..
     cu_seqlens[r+1], and seq_len[r] counts them already.  rope is a table of rope_table (its width says how much of a
     head is rotated) or None.  Returns the rotated q, [T][hq][d]."""
+    if pool._p:
+        r = pool._fast.attn_prologue(q, k, v, pool._p, rope, table, seq_len, cu_seqlens, layer, q_norm, k_norm, eps,
+                                     interleaved, out)
+        if r is not None:
+            return _made(r)
     dev, d, hkv, i32, f32 = pool.device, pool.d, pool.hkv, torch.int32, torch.float32
     T, hq = q.shape[:2]
     tab, rows, max_pages = _table(table, dev)
@@ -802,6 +819,12 @@ def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int 
 
     scale defaults to d^-1/2.  workspace is a uint8 tensor of paged_attention_workspace_bytes (allocated here when none
     is given).  Returns [T][hq][d]."""
+    if scale is None:
+        scale = pool.d ** -0.5
+    if pool._p:
+        r = pool._fast.paged_attention(q, pool._p, table, seq_len, cu_seqlens, layer, scale, out, workspace)
+        if r is not None:
+            return _made(r)
     dev, d, i32 = pool.device, pool.d, torch.int32
     T, hq = q.shape[:2]
     tab, rows, max_pages = _table(table, dev)
@@ -820,7 +843,7 @@ def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int 
         wp, nbytes = _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size()
     _check(L.paged_attention(
         qp, qs, pool._h, layer, tab, max_pages, _arg(seq_len, rows, i32, dev, "seq_len"),
-        _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"), d ** -0.5 if scale is None else scale,
+        _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"), scale,
         op, hq, rows, T, wp, nbytes, pool._code, _raw_stream(dev)))
     return out
 
@@ -841,6 +864,13 @@ def kv_pages_reserve(table, refs, rows, tokens, page_size: int, status: Optional
 def kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size: int, moves: KVPageMoves) -> KVPageMoves:
     """Make the empty rows dst_rows copies of src_rows: full pages are shared, partial last pages get a free page each,
     whose copies are listed in `moves` (then kv_pages_copy(pool, moves))."""
+    f = _lib.fast()
+    if f:
+        r = f.kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size, moves.src, moves.dst, moves.count,
+                            moves.status)
+        if r is not None:
+            _made(r)
+            return moves
     dev, n, i32 = table.device, src_rows.numel(), torch.int32
     tab, trows, max_pages = _table(table, dev)
     pages = refs.numel()
@@ -853,6 +883,12 @@ def kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size: int, move
 
 def kv_pages_free(table, seq_len, refs, rows) -> None:
     """Give up the pages of the listed rows and set their lengths to 0."""
+    f = _lib.fast()
+    if f:
+        r = f.kv_pages_free(table, seq_len, refs, rows)
+        if r is not None:
+            _made(r)
+            return
     dev, n, i32 = table.device, rows.numel(), torch.int32
     tab, trows, max_pages = _table(table, dev)
     pages = refs.numel()
@@ -880,6 +916,11 @@ def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.
 
 def kv_pages_copy(pool: KVPagePool, moves: KVPageMoves) -> None:
     """Copy the listed pages, K and V of all layers."""
+    if pool._p:
+        r = pool._fast.kv_pages_copy(pool._p, moves.src, moves.dst, moves.count)
+        if r is not None:
+            _made(r)
+            return
     dev, n = pool.device, moves.src.numel()
     src, dst, count = moves._pointers(n, dev)
     _check(_lib.load().kv_pages_copy(pool._h, src, dst, n, count, _raw_stream(dev)))

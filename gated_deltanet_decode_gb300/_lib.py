@@ -124,6 +124,28 @@ _SIGS = {
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the C++ binding of the attention layers, where it was built
+
+
+def _load_fast(L):
+    """The C++ binding, told where the library's functions are; None without it."""
+    import importlib.machinery
+    import importlib.util
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_fast_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast_binding", loader, origin=path))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(L, f), _P).value for f in (
+        "attn_prologue", "paged_attention_workspace_bytes", "paged_attention", "kv_pages_fork", "kv_pages_free",
+        "kv_pages_copy")))
+    return module
+
+
+def fast():
+    load()
+    return _fast
 
 
 def lib_path() -> str:
@@ -132,7 +154,7 @@ def lib_path() -> str:
 
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libgdn_decode.so (building it first if it is missing or stale)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -145,5 +167,6 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args
+            _fast = _load_fast(L)
             _lib = L
     return _lib

@@ -1,7 +1,9 @@
 """Build the CUDA library ``libgdn_decode.so`` in-tree with nvcc (sm_103a).
 
 Each translation unit compiles in its own process (in parallel), then nvcc
-links them into one shared library against the shared CUDA runtime.
+links them into one shared library against the shared CUDA runtime.  Beside it
+g++ compiles the attention layers' binding for the installed PyTorch; without
+it the package makes the same calls through ctypes.
 """
 from __future__ import annotations
 
@@ -40,8 +42,58 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+BINDING_SOURCE = os.path.join(CSRC, "fast_binding.cpp")
+
+
+def binding_path() -> str:
+    import torch
+    return os.path.join(PKG, f"_fast_binding-torch{torch.__version__.split('+')[0]}.so")
+
+
+def _start_binding(force: bool):
+    """The compiler's process for the binding, and where its output goes; None if it is up to date or cannot be made."""
+    import sysconfig
+
+    import torch
+    path = binding_path()
+    newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, os.path.join(ROOT, "include", "gdn_decode.h")))
+    if not force and os.path.exists(path) and os.path.getmtime(path) >= newest:
+        return None
+    gxx, nvcc = shutil.which("g++"), _nvcc()
+    if not gxx:
+        return None
+    base = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in inc), BINDING_SOURCE, "-o", tmp,
+           f"-L{os.path.join(base, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp, path
+
+
+def _end_binding(started) -> None:
+    if started is None:
+        return
+    proc, tmp, path = started
+    out, _ = proc.communicate()
+    if proc.returncode == 0:
+        os.replace(tmp, path)
+    else:
+        print("the C++ binding did not build; the package calls through ctypes\n" + out.decode(errors="replace")[-2000:],
+              file=sys.stderr)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link unless the library is up to date. Returns its path."""
+    """Compile and link what is not up to date. Returns the library's path."""
+    binding = _start_binding(force)
+    try:
+        return _build_library(force, verbose)
+    finally:
+        _end_binding(binding)
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and not _stale():
         return LIB_PATH
     nvcc = _nvcc()
