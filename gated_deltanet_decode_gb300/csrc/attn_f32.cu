@@ -45,12 +45,14 @@ struct Ctrl32 {
     float2 ml[8 * 16]; // (m, l) by (share, row): 128 pairs in every form
 };
 
-// The head is x cut to the 11 bits that a product reads; the tail, exact, has 13,
-// of which it reads 11.  (Rounding the head would save one of them, and the
-// conversion costs as much as a product.)
+// The head is x rounded to the 11 bits that a product reads (by an addition to
+// its bits: the conversion instruction costs as much as a product); the tail,
+// exact, has 12, of which it reads 11.  A head cut short instead leaves tails
+// twice as large, and the tails' product, left out, showed (5.6e-6 of a
+// result's norm, against 8e-7 for plain fp32).
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
 {
-    hi = __float_as_uint(x) & 0xffffe000u;
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 template <int N> struct Width {
@@ -81,34 +83,51 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
 {
     constexpr int LD = Geo32<D>::LD;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    constexpr int CHAINS = NT == 1 ? 4 : 1; // a single column tile: four sums, for latency
-    float s[NT][CHAINS][4];
+    // The tensor cores cut their sums short instead of rounding them, which showed (5e-6 of a result's norm) in the sums
+    // over a head's dimensions and over all keys.  So they only sum four steps of eight dimensions, or a tile's keys, and
+    // the rest is fp32 additions.  A single column tile takes the four steps apart, for latency.
+    float s[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < CHAINS; ++h)
+        for (int e = 0; e < 4; ++e)
+            s[n][e] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < D / 8; k0 += 4) {
+        constexpr int APART = NT == 1 ? 4 : 1;
+        float t[NT][APART][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < APART; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    t[n][h][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const float *qp = q + g * LD + 8 * (k0 + ks) + c;
+            uint32_t ah[4], al[4];
+            split(qp[0], ah[0], al[0]);
+            split(qp[8 * LD], ah[1], al[1]);
+            split(qp[4], ah[2], al[2]);
+            split(qp[8 * LD + 4], ah[3], al[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float *kp = k + (8 * n + g) * LD + 8 * (k0 + ks) + c;
+                uint32_t h0, h1, t0, t1;
+                split(kp[0], h0, t0);
+                split(kp[4], h1, t1);
+                float(&d)[4] = t[n][ks % APART];
+                mma8(d, al, h0, h1);
+                mma8(d, ah, t0, t1);
+                mma8(d, ah, h0, h1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                s[n][h][e] = 0.f;
-#pragma unroll 4
-    for (int ks = 0; ks < D / 8; ++ks) {
-        const float *qp = q + g * LD + 8 * ks + c;
-        uint32_t ah[4], al[4];
-        split(qp[0], ah[0], al[0]);
-        split(qp[8 * LD], ah[1], al[1]);
-        split(qp[4], ah[2], al[2]);
-        split(qp[8 * LD + 4], ah[3], al[3]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float *kp = k + (8 * n + g) * LD + 8 * ks + c;
-            uint32_t h0, h1, t0, t1;
-            split(kp[0], h0, t0);
-            split(kp[4], h1, t1);
-            float(&d)[4] = s[n][ks % CHAINS];
-            mma8(d, al, h0, h1);
-            mma8(d, ah, t0, t1);
-            mma8(d, ah, h0, h1);
-        }
+                s[n][e] += APART == 4 ? (t[n][0][e] + t[n][1 % APART][e]) + (t[n][2 % APART][e] + t[n][3 % APART][e]) : t[n][0][e];
     }
     // weights 2^(c2 (s - m))
     float top0 = m0, top8 = m8;
@@ -116,15 +135,11 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            if (CHAINS == 4) {
-                s[n][0][e] = (s[n][0][e] + s[n][1 % CHAINS][e]) + (s[n][2 % CHAINS][e] + s[n][3 % CHAINS][e]);
-                s[n][0][e + 2] = (s[n][0][e + 2] + s[n][1 % CHAINS][e + 2]) + (s[n][2 % CHAINS][e + 2] + s[n][3 % CHAINS][e + 2]);
-            }
             const int at = 8 * n + 2 * c + e;
-            s[n][0][e] = at < see0 ? s[n][0][e] : -INFINITY;
-            s[n][0][e + 2] = at < see8 ? s[n][0][e + 2] : -INFINITY;
-            top0 = fmaxf(top0, s[n][0][e]);
-            top8 = fmaxf(top8, s[n][0][e + 2]);
+            s[n][e] = at < see0 ? s[n][e] : -INFINITY;
+            s[n][e + 2] = at < see8 ? s[n][e + 2] : -INFINITY;
+            top0 = fmaxf(top0, s[n][e]);
+            top8 = fmaxf(top8, s[n][e + 2]);
         }
 #pragma unroll
     for (int x = 1; x < 4; x <<= 1) {
@@ -132,32 +147,36 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
         top8 = fmaxf(top8, __shfl_xor_sync(0xffffffffu, top8, x));
     }
     const float z0 = top0 == -INFINITY ? 0.f : -top0 * c2, z8 = top8 == -INFINITY ? 0.f : -top8 * c2;
-    const float f0 = m0 == -INFINITY ? 0.f : ex2(fmaf(m0, c2, z0)), f8 = m8 == -INFINITY ? 0.f : ex2(fmaf(m8, c2, z8));
+    // (exactly one where the maximum stays: a factor of 1 + 10^-7 a tile adds up)
+    const float f0 = m0 == -INFINITY ? 0.f : ex2((m0 - top0) * c2), f8 = m8 == -INFINITY ? 0.f : ex2((m8 - top8) * c2);
     m0 = top0, m8 = top8;
     l0 *= f0, l8 *= f8;
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-        o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f8, o[n][3] *= f8;
+    uint32_t ah[NT][4], al[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const float p0 = ex2(fmaf(s[n][0][0], c2, z0)), p1 = ex2(fmaf(s[n][0][1], c2, z0));
-        const float p2 = ex2(fmaf(s[n][0][2], c2, z8)), p3 = ex2(fmaf(s[n][0][3], c2, z8));
+        const float p0 = ex2(fmaf(s[n][0], c2, z0)), p1 = ex2(fmaf(s[n][1], c2, z0));
+        const float p2 = ex2(fmaf(s[n][2], c2, z8)), p3 = ex2(fmaf(s[n][3], c2, z8));
         l0 += p0 + p1, l8 += p2 + p3;
-        uint32_t ah[4], al[4];
-        split(p0, ah[0], al[0]);
-        split(p2, ah[1], al[1]);
-        split(p1, ah[2], al[2]);
-        split(p3, ah[3], al[3]);
-        const float *vp = v + (8 * n + 2 * c) * LD + g;
+        split(p0, ah[n][0], al[n][0]);
+        split(p2, ah[n][1], al[n][1]);
+        split(p1, ah[n][2], al[n][2]);
+        split(p3, ah[n][3], al[n][3]);
+    }
+    const float *vp = v + 2 * c * LD + g;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
+    for (int e = 0; e < D / 8; ++e) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             uint32_t h0, h1, t0, t1;
-            split(vp[8 * e], h0, t0);
-            split(vp[8 * e + LD], h1, t1);
-            mma8(o[e], al, h0, h1);
-            mma8(o[e], ah, t0, t1);
-            mma8(o[e], ah, h0, h1);
+            split(vp[8 * n * LD + 8 * e], h0, t0);
+            split(vp[8 * n * LD + 8 * e + LD], h1, t1);
+            mma8(d, al[n], h0, h1);
+            mma8(d, ah[n], t0, t1);
+            mma8(d, ah[n], h0, h1);
         }
+        o[e][0] = fmaf(o[e][0], f0, d[0]), o[e][1] = fmaf(o[e][1], f0, d[1]);
+        o[e][2] = fmaf(o[e][2], f8, d[2]), o[e][3] = fmaf(o[e][3], f8, d[3]);
     }
 }
 
