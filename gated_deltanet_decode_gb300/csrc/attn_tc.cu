@@ -406,8 +406,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
         } else if (warp == 1) {
             // ---- the products.  The whole warp walks, on values that the broadcasts make uniform to the compiler, and
             // one elected lane issues: an issue loop in a divergent branch took 1,970 cycles a step, twice the products'.
-            // The queue runs dry in the time between a step's last product and the next one's first: what can be waited
-            // for ahead is.
             const bool leader = elect();
             int st = 0, kst = 0, vst = 0; // the ring's next place; the places of the K and V tiles in use
             uint32_t parity = 0, pparity[2] = {0, 0};
@@ -436,7 +434,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 for (int i = 0; i < qn; ++i)
                     wait(ctl.qfull[(qc + i) % G::NQ], ((qc + i) / G::NQ) & 1);
                 const uint32_t q0 = sbase + (qc % G::NQ) * G::QBYTES, q1 = pair ? sbase + ((qc + 1) % G::NQ) * G::QBYTES : q0;
-                bool v_here = false; // the next V tile has landed
                 // S of a step of parity b
                 auto s_step = [&](int i, const int b) {
                     if (!pair || b == 0) {
@@ -444,8 +441,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                             return;
                         advance(kst);
                     }
-                    // V of the step whose product is next (in pairs a V tile serves two steps)
-                    v_here = (!pair || b == 1) && i > 1 && __all_sync(0xffffffffu, mbar_try(full0 + 8 * st, parity));
                     after_sync();
                     const uint64_t qd = desc_k(b ? q1 : q0), kd = desc_k(stage_addr(kst));
                     if (leader) {
@@ -465,11 +460,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 auto step = [&](int i, const int b) {
                     const int o = G::NO == 2 ? b : 0;
                     if (!pair || b == 0) {
-                        if (!v_here && !wait_at(full0 + 8 * st, parity))
+                        if (!wait_at(full0 + 8 * st, parity))
                             return;
                         advance(vst);
                     }
-                    v_here = false;
                     const uint64_t vd = desc_mn(stage_addr(vst), KT * 128);
                     const bool more = i >= G::NO;
 #pragma unroll
@@ -637,7 +631,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     const uint32_t sa = tmem + lanes + G::S0 + b * KT;
                     float s[KT];
                     tld(sa, *reinterpret_cast<uint32_t(*)[KT]>(&s[0]));
-                    const int nv = min(valid, see - key);
+                    // rows that are no token's are left to compute what they hold: masking them cost decode steps, where
+                    // most rows of the warp are such, as much as the weights
+                    const int nv = mine ? min(valid, see - key) : KT;
                     if (__any_sync(0xffffffffu, nv < KT)) {
 #pragma unroll
                         for (int k = 0; k < KT; ++k)
@@ -648,7 +644,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     for (int k = 3; k + 1 < KT; k += 2)
                         t[(k >> 1) & 3] = max3(t[(k >> 1) & 3], s[k], s[k + 1]);
                     const float top = fmaxf(max3(t[0], t[1], t[2]), fmaxf(t[3], s[KT - 1]));
-                    const bool grow = (top - m) * c > kLazy; // -inf to -inf is no growth
+                    const bool grow = mine && (top - m) * c > kLazy; // -inf to -inf is no growth
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2((m - top) * c) : 1.f;
                         if (grow)
