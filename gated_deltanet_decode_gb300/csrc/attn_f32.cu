@@ -394,7 +394,7 @@ template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
     e = launch_pdl(attn_f32_kernel<D>, dim3(p.runs), dim3(kThreads), (size_t)G::FLOATS * 4, s, p);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<float, D>, dim3(p.runs, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
+    return launch_combine<float, D>(p, s);
 }
 
 } // namespace

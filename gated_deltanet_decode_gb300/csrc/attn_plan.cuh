@@ -141,11 +141,12 @@ __device__ __forceinline__ long long scan64(long long v, long long *part, int wa
 // long long a warp, and `found` the place where one thread leaves the row.
 struct Run {
     long long share, u0, u1, base;
+    long long per; // key tiles a head of the row it begins in
     int row;
-    Row first; // the row it begins in
+    Row first;     // that row
 };
 struct Found { // shared memory
-    long long base;
+    long long base, per;
     int row;
     Row first;
 };
@@ -154,11 +155,13 @@ template <int THREADS, int KT> __device__ Run plan_run(const WorkArgs &p, int mt
     const CacheRows &c = p.a.c;
     const int ps = p.a.pages.page_size, heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
     Row x{0, 0, 0, false, false};
+    long long per = 0;
     auto cost_of = [&](int r) -> long long {
         if (r >= c.rows)
             return 0;
         x = row_of(c, ps, r);
-        return x.live ? head_tiles(x, mt, KT) * heads : 0;
+        per = x.live ? head_tiles(x, mt, KT) : 0;
+        return per * heads;
     };
     Run run;
     long long total = 0, cost = 0, before = 0, sum;
@@ -176,20 +179,21 @@ template <int THREADS, int KT> __device__ Run plan_run(const WorkArgs &p, int mt
     run.u1 = min(total, run.u0 + run.share);
     if (c.rows <= THREADS) { // the one pass has it
         if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
-            found = {before, tid, x};
+            found = {before, per, tid, x};
     } else {
         long long seen = 0;
         for (int b = 0; b < c.rows && seen <= run.u0 && run.u0 < total; b += THREADS) {
             cost = cost_of(b + tid);
             before = seen + scan64(cost, part, THREADS / 32, sum);
             if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
-                found = {before, b + tid, x};
+                found = {before, per, b + tid, x};
             seen += sum;
         }
     }
     __syncthreads();
     run.row = found.row;
     run.base = found.base;
+    run.per = found.per;
     run.first = found.first;
     return run;
 }
@@ -242,10 +246,9 @@ struct Walk {
         fetch(); // the next rows' lengths, while the first row's items are handed out
         if (u < run.u1) {
             enter(run.first);
-            const long long per = head_tiles(x, mt, kt);
             long long rem = u - run.base; // the run begins inside this row
-            h = (int)(rem / per);
-            rem -= h * per;
+            for (; rem >= run.per; ++h)
+                rem -= run.per;
             while (rem >= item_tiles(x, t, mt, kt))
                 rem -= item_tiles(x, t++, mt, kt);
             ja = (int)rem;
@@ -303,80 +306,123 @@ struct Walk {
     }
 };
 
-// Joins the parts of cut items: block x holds the cut listed by run x, y
-// strides over its rows, a warp a row.  The lanes take a part's (m, l) each,
-// then all walk over the parts' O, four parts' loads in flight.
-template <typename T, int D> __global__ void __launch_bounds__(128) attn_combine_kernel(const WorkArgs p)
+// Joins the parts of R rows of the cut that run w listed, by one warp.
+template <typename T, int D, int R> __device__ __forceinline__ void combine_rows(const WorkArgs &p, const Cut &c, int w, int row0, int rows)
 {
-    wait_prior_grid();
-    const int w = blockIdx.x;
-    const Cut c = p.cuts[w];
-    if (c.parts == 0)
-        return;
+    const int lane = threadIdx.x & 31;
     constexpr int V = D / 32 < 4 ? D / 32 : 4, N = D / (32 * V); // a lane's columns: N runs of V
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rows = c.ntok > p.tq ? p.second + (c.ntok - p.tq) * p.g : c.ntok * p.g;
     const float k2 = p.a.scale * 1.44269504088896341f;
     // the first part lies in run w - 1 (its last item), the others are the first items of runs w ..
     auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * (w - 1) + 1 : 2 * (w + i - 1)) * p.rows_max; };
-    for (int row = blockIdx.y * 4 + warp; row < rows; row += gridDim.y * 4) {
-        const int tile = p.second && row >= p.second, in = row - tile * p.second, t = in / p.g, tok = t + tile * p.tq;
-        if (t >= p.tq || tok >= c.ntok)
-            continue;
-        float m = -INFINITY, l = 0.f, x[N][V];
-        bool bad = false;
+    float m[R], l[R], x[R][N][V];
+    bool bad[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY, l[r] = 0.f, bad[r] = false;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                x[n][e] = 0.f;
-        for (int i0 = 0; i0 < c.parts; i0 += 32) {
-            const bool there = i0 + lane < c.parts;
-            const float2 ml = there ? p.part_ml[slot(i0 + lane) + row] : make_float2(-INFINITY, 0.f);
-            bad |= __any_sync(0xffffffffu, ml.x != ml.x);
-            float top = fmaxf(m, ml.x);
+                x[r][n][e] = 0.f;
+    }
+    for (int i0 = 0; i0 < c.parts; i0 += 32) {
+        const bool there = i0 + lane < c.parts;
+        float2 ml[R];
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            ml[r] = there && row0 + r < rows ? p.part_ml[slot(i0 + lane) + row0 + r] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            bad[r] |= __any_sync(0xffffffffu, ml[r].x != ml[r].x);
+            float top = fmaxf(m[r], ml[r].x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float old = m == -INFINITY ? 0.f : ex2((m - top) * k2); // of what the parts before gave
-            const float f = ml.x == -INFINITY ? 0.f : ex2((ml.x - top) * k2);
-            m = top;
-            float sum = ml.y * f;
+            const float old = m[r] == -INFINITY ? 0.f : ex2((m[r] - top) * k2); // of what the parts before gave
+            f[r] = ml[r].x == -INFINITY ? 0.f : ex2((ml[r].x - top) * k2);
+            m[r] = top;
+            float sum = ml[r].y * f[r];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = fmaf(l, old, sum);
+            l[r] = fmaf(l[r], old, sum);
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    x[n][e] *= old;
-            const int here = min(32, c.parts - i0);
-#pragma unroll 4
-            for (int i = 0; i < here; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float *const o = p.part_o + (slot(i0 + i) + row) * D + V * lane;
+                    x[r][n][e] *= old;
+        }
+        const int here = min(32, c.parts - i0);
+        constexpr int U = R == 1 ? (N == 1 ? 8 : 4) : 2;
+#pragma unroll U
+        for (int i = 0; i < here; ++i) {
+            float y[R][N][V];
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    float y[V];
-                    if constexpr (V == 4)
-                        *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(o + 32 * V * n);
-                    else
-                        *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(o + 32 * V * n);
+            for (int r = 0; r < R; ++r)
+                if (row0 + r < rows) {
+                    const float *const o = p.part_o + (slot(i0 + i) + row0 + r) * D + V * lane;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) // a part without keys for this row has weight zero, and zeros
-                        x[n][e] = fmaf(y[e], fi, x[n][e]);
+                    for (int n = 0; n < N; ++n) {
+                        if constexpr (V == 4)
+                            *reinterpret_cast<float4 *>(y[r][n]) = *reinterpret_cast<const float4 *>(o + 32 * V * n);
+                        else
+                            *reinterpret_cast<float2 *>(y[r][n]) = *reinterpret_cast<const float2 *>(o + 32 * V * n);
+                    }
+                }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float fi = __shfl_sync(0xffffffffu, f[r], i);
+                if (row0 + r < rows) {
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) // a part without keys for this row has weight zero, and zeros
+                            x[r][n][e] = fmaf(y[r][n][e], fi, x[r][n][e]);
                 }
             }
         }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = row0 + r;
+        const int tile = p.second && row >= p.second, in = row - tile * p.second, t = in / p.g, tok = t + tile * p.tq;
+        if (row >= rows || t >= p.tq || tok >= c.ntok)
+            continue;
         T *const out = static_cast<T *>(p.a.out) + ((size_t)(c.tok + tok) * p.a.hq + c.head * p.g + (in - t * p.g)) * D + V * lane;
-        const float inv = 1.f / l;
+        const float inv = 1.f / l[r];
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                out[32 * V * n + e] = from_f<T>(bad ? 0.f : x[n][e] * inv);
+                out[32 * V * n + e] = from_f<T>(bad[r] ? 0.f : x[r][n][e] * inv);
     }
+}
+
+// Joins the parts of cut items: block x holds the cut listed by run x.  Bound:
+// the latency of three loads in a row (the cut, a part's (m, l) a lane, the
+// parts' O), so much is in flight together: a row a warp and eight parts' loads
+// where the blocks have a warp for every row, else four rows a warp.
+template <typename T, int D> __global__ void __launch_bounds__(128) attn_combine_kernel(const WorkArgs p)
+{
+    wait_prior_grid();
+    const Cut c = p.cuts[blockIdx.x];
+    if (c.parts == 0)
+        return;
+    const int rows = c.ntok > p.tq ? p.second + (c.ntok - p.tq) * p.g : c.ntok * p.g;
+    const int w = blockIdx.y * 4 + (threadIdx.x >> 5);
+    if (rows <= 4 * (int)gridDim.y) {
+        if (w < rows)
+            combine_rows<T, D, 1>(p, c, blockIdx.x, w, rows);
+    } else if (4 * w < rows) {
+        combine_rows<T, D, 4>(p, c, blockIdx.x, 4 * w, rows);
+    }
+}
+
+template <typename T, int D> cudaError_t launch_combine(const WorkArgs &p, cudaStream_t s)
+{
+    const int blocks = p.rows_max <= 64 ? (p.rows_max + 3) / 4 : (p.rows_max + 15) / 16;
+    return launch_pdl(attn_combine_kernel<T, D>, dim3(p.runs, blocks), dim3(128), 0, s, p);
 }
 
 } // namespace

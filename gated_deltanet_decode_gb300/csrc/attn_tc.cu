@@ -253,6 +253,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (tid == 64) { // the copies' descriptors, while the lengths are looked up
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    }
     if (tid == 32) {
         for (int i = 0; i < G::STAGES; ++i)
             mbar_init(bar(ctl.full[i]), 1), mbar_init(bar(ctl.empty[i]), 1);
@@ -532,12 +536,18 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     const bf16 *const src = static_cast<const bf16 *>(a.q) + (size_t)(it.tok + i * p.tq) * a.q_stride +
                                             (size_t)it.head * p.g * D;
                     const uint32_t dst = sbase + s * G::QBYTES;
-                    for (int x = lane; x < rows * VR; x += 32) {
-                        const int row = x / VR, vec = x % VR, tok = row / p.g, head = row - tok * p.g;
-                        const uint32_t d = dst + (vec >> 3) * 128 * 128 + row * 128 + (((vec & 7) ^ (row & 7)) << 4);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d),
+                    constexpr int RP = 32 / VR;                                // rows a pass
+                    const int vec = lane % VR;
+                    int row = lane / VR, tok = row / p.g, head = row - tok * p.g;
+                    const uint32_t at = dst + (vec >> 3) * 128 * 128;
+#pragma unroll 4
+                    for (; row < rows; row += RP) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         at + row * 128 + (((vec & 7) ^ (row & 7)) << 4)),
                                      "l"(src + (size_t)tok * a.q_stride + head * D + vec * 8)
                                      : "memory");
+                        for (head += RP; head >= p.g; head -= p.g)
+                            ++tok;
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     smem_to_async();
@@ -894,7 +904,7 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
     e = launch_pdl(attn_tc_kernel<D>, dim3(p.runs), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_combine_kernel<bf16, D>, dim3(p.runs, (p.rows_max + 15) / 16), dim3(128), 0, s, p);
+    return launch_combine<bf16, D>(p, s);
 }
 
 } // namespace
