@@ -16,6 +16,8 @@ namespace {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t dtype_size(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
+constexpr long long kMaxTokens = 1ll << 30; // a row's; positions and their tiles' ends stay within an int
+
 bool page_size_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 
 int check_pool_geometry(int num_pages, int page_size, int layers, int hkv, int d, int dtype)
@@ -70,8 +72,8 @@ int check_rows(const kv_page_pool *pool, int layer, const int32_t *table, int ma
         return api_fail(GDN_EINVAL, "rows=%d total_tokens=%d", rows, total_tokens);
     if (max_pages < 1)
         return api_fail(GDN_EINVAL, "max_pages=%d < 1", max_pages);
-    if ((long long)max_pages * pool->page_size > 0x7fffffffll)
-        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^31 - 1 tokens", max_pages);
+    if ((long long)max_pages * pool->page_size > kMaxTokens)
+        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^30 tokens", max_pages);
     if (total_tokens > 0 && (!table || !seq_len || !cu_seqlens))
         return api_fail(GDN_EINVAL, "table, seq_len and cu_seqlens must be non-NULL");
     return GDN_OK;
@@ -285,8 +287,8 @@ int kv_pages_reserve(int32_t *table, int table_rows, int max_pages, int32_t *ref
         return rc;
     if (!page_size_ok(page_size))
         return api_fail(GDN_EUNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", page_size);
-    if ((long long)max_pages * page_size > 0x7fffffffll)
-        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^31 - 1 tokens", max_pages);
+    if ((long long)max_pages * page_size > kMaxTokens)
+        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^30 tokens", max_pages);
     if (n < 0 || n > GDN_MAX_PAGE_ROWS)
         return api_fail(GDN_EINVAL, "n=%d outside [0, %d]", n, GDN_MAX_PAGE_ROWS);
     if (n == 0)
@@ -309,8 +311,8 @@ int kv_pages_fork(int32_t *table, int table_rows, int max_pages, int32_t *seq_le
         return rc;
     if (!page_size_ok(page_size))
         return api_fail(GDN_EUNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", page_size);
-    if ((long long)max_pages * page_size > 0x7fffffffll)
-        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^31 - 1 tokens", max_pages);
+    if ((long long)max_pages * page_size > kMaxTokens)
+        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^30 tokens", max_pages);
     if (n < 0 || n > GDN_MAX_PAGE_ROWS)
         return api_fail(GDN_EINVAL, "n=%d outside [0, %d]", n, GDN_MAX_PAGE_ROWS);
     if (!move_count)

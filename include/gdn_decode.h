@@ -400,7 +400,8 @@ int gdn_commit(int32_t *read_slot, int32_t *write_slot, int rows, void *stream);
  *   seq_len  [rows] int32: tokens a row holds; 0 is a padding row
  *   refs     [num_pages] int32: how many table entries name a page; 0 is free
  *            (refs[0] is not used)
- * A row that has more pages than its tokens need has them in reserve. */
+ * A row that has more pages than its tokens need has them in reserve.  A row's
+ * pages hold at most 2^30 tokens. */
 typedef struct kv_page_pool kv_page_pool;
 
 /* Create allocates and zero-fills (GDN_ENOMEM when the device is full); wrap
@@ -435,7 +436,8 @@ int rope_table(const double *inv_freq, int rot, int positions, double mscale, fl
  * slot p % page_size receives k's and v.
  *   q [T][hq][d], k, v [T][hkv][d]: token strides in elements (at least
  *   heads*d; a token's heads are dense), base and strides 16-byte multiples
- *   q_out [T][hq][d], dense    rope [rope_positions][rot] fp32
+ *   q_out [T][hq][d], dense (q itself, where q is dense, will do)
+ *   rope [rope_positions][rot] fp32
  *   q_norm, k_norm [d] fp32 or NULL
  * Padding rows' tokens get zero q_out and write nothing.  So do, with
  * GDN_DEVERR_BAD_PAGE, tokens outside every row, of a row shorter than its

@@ -96,3 +96,23 @@ def test_table_refusals(L):
     for bad in ((8, 4, 1.0), (0, 4, 1.0), (20, 4, 1.0), (16, -1, 1.0), (16, 4, float("nan"))):
         assert L.rope_table(FAKE, *bad, FAKE, None) == EINVAL
     L.kv_page_pool_destroy(h)
+
+
+def test_rope_frequencies():
+    """The scalings' closed forms, on the CPU."""
+    import math
+
+    import torch
+
+    from gated_deltanet_decode_gb300 import rope_inv_freq
+    plain, one = rope_inv_freq(64, 500000.0)
+    assert one == 1.0 and plain.dtype == torch.float64 and plain.shape == (32,)
+    assert torch.allclose(plain, 500000.0 ** (-torch.arange(32, dtype=torch.float64) / 32), rtol=1e-14)
+    assert torch.allclose(rope_inv_freq(64, 500000.0, {"type": "linear", "factor": 8})[0], plain / 8, rtol=1e-14)
+    ntk = rope_inv_freq(64, 500000.0, {"type": "ntk", "factor": 8})[0]
+    assert ntk[0] == 1.0 and math.isclose(ntk[-1], plain[-1] / 8, rel_tol=1e-12)
+    y, m = rope_inv_freq(64, 500000.0, {"type": "yarn", "factor": 8, "original": 8192, "mscale": 1.5})
+    assert m == 1.5 and (y <= plain).all() and (y >= plain / 8 - 1e-18).all() and y[0] == plain[0]
+    for bad in ((63, 1e4, None), (0, 1e4, None), (64, 1e4, {"type": "other", "factor": 2}), (64, 1e4, {"type": "ntk", "factor": 0})):
+        with pytest.raises(ValueError):
+            rope_inv_freq(*bad)

@@ -81,6 +81,16 @@ def test_rows_by_the_thousand(gdn):
     check(gdn, "f32", 2, 1, 64, 32, True, [min(n, 1) if r % 3 else min(n, 2) for r, n in enumerate(lens)], lens)
 
 
+def test_in_place(gdn):
+    c = Cache([300, 40], "bf16", 2, 64, 16, seed=9)
+    q = torch.randn(270, 4, 64, generator=torch.Generator().manual_seed(2)).bfloat16().to(DEV)
+    k = torch.randn(270, 2, 64).bfloat16().to(DEV)
+    args = (k, k, c.pool(gdn), rope(300, 32).to(DEV), i32(c.table), i32(c.lens), i32([0, 250, 270]))
+    want = gdn.attn_prologue(q, *args)
+    assert gdn.attn_prologue(q, *args, out=q) is q
+    assert torch.equal(q, want)
+
+
 def test_bad_tokens_are_left_out(gdn):
     """A row shorter than its tokens, a position past the rotation table, bad pages, tokens outside every row."""
     lens, new = [30, 1, 100, 20, 16], [2, 3, 1, 1, 2]
