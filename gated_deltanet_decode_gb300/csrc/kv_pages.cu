@@ -161,12 +161,33 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageTables 
     }
 }
 
+// Entry e of the row that fork i makes: full pages shared, entries past the
+// row's pages zeroed.
+__device__ __forceinline__ void fork_entry(const PageTables &t, const int32_t *src_rows, const int32_t *dst_rows, int i, int e)
+{
+    const int s = src_rows[i], len = t.seq_len[s], full = len / t.page_size;
+    int32_t *const to = t.table + (size_t)dst_rows[i] * t.max_pages + e;
+    if (e < full) {
+        int page = t.table[(size_t)s * t.max_pages + e];
+        if (page > 0 && page < t.num_pages) {
+            atomicAdd(t.refs + page, 1);
+        } else {
+            report(t.err, GDN_DEVERR_BAD_PAGE);
+            page = 0;
+        }
+        *to = page;
+    } else if (e > full || len % t.page_size == 0) {
+        *to = 0;
+    }
+}
+
 // The pages that forks need for partial last pages, their lengths and move
-// list.  fork_rows_kernel then fills the rows of the entries with status 0.
+// list.  Where `rows` is set the rows of the entries with status 0 are filled
+// here too, else by fork_rows_kernel.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageTables t, const int32_t *src_rows,
                                                                  const int32_t *dst_rows, int n, int32_t *move_src,
                                                                  int32_t *move_dst, int32_t *move_count,
-                                                                 int32_t *status)
+                                                                 int32_t *status, int rows)
 {
     __shared__ int start[GDN_MAX_PAGE_ROWS]; // partial pages of the entries before this one
     __shared__ int owner[GDN_MAX_PAGE_ROWS]; // the entry that gets the free page of a rank
@@ -219,9 +240,17 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageTable
     }
     if (threadIdx.x == 0)
         *move_count = found;
+    if (!rows)
+        return;
+    __syncthreads(); // the statuses are written
+    for (long long x = threadIdx.x; x < (long long)n * t.max_pages; x += kPlanThreads) {
+        const int i = (int)(x / t.max_pages), e = (int)(x - (long long)i * t.max_pages);
+        if (status[i] == 0)
+            fork_entry(t, src_rows, dst_rows, i, e);
+    }
 }
 
-// One table entry a thread: full pages shared, entries past the row's pages zeroed.
+// One table entry a thread.
 __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PageTables t, const int32_t *src_rows,
                                                                 const int32_t *dst_rows, const int32_t *status,
                                                                 int chunks)
@@ -231,20 +260,7 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PageTables
     const int e = (blockIdx.x - i * chunks) * kRowThreads + threadIdx.x;
     if (e >= t.max_pages || status[i] != 0)
         return;
-    const int s = src_rows[i], len = t.seq_len[s], full = len / t.page_size;
-    int32_t *const to = t.table + (size_t)dst_rows[i] * t.max_pages + e;
-    if (e < full) {
-        int page = t.table[(size_t)s * t.max_pages + e];
-        if (page > 0 && page < t.num_pages) {
-            atomicAdd(t.refs + page, 1);
-        } else {
-            report(t.err, GDN_DEVERR_BAD_PAGE);
-            page = 0;
-        }
-        *to = page;
-    } else if (e > full || len % t.page_size == 0) {
-        *to = 0;
-    }
+    fork_entry(t, src_rows, dst_rows, i, e);
 }
 
 // One table entry a thread.  The exchange makes a row that is listed twice
@@ -464,9 +480,11 @@ cudaError_t launch_pages_fork(const PageTables &t, const int32_t *src_rows, cons
                               int32_t *move_src, int32_t *move_dst, int32_t *move_count, int32_t *status,
                               cudaStream_t s)
 {
+    // a second launch costs about 2 us, as does filling eight entries a thread in the first
+    const int rows = (long long)n * t.max_pages <= 8 * kPlanThreads;
     cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, t, src_rows, dst_rows, n, move_src,
-                               move_dst, move_count, status);
-    if (e != cudaSuccess || n == 0)
+                               move_dst, move_count, status, rows);
+    if (e != cudaSuccess || rows)
         return e;
     const int chunks = (t.max_pages + kRowThreads - 1) / kRowThreads;
     if ((long long)chunks * n > 0x7fffffffll)
