@@ -13,7 +13,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024; // one CTA plans a reservation or a fork
 constexpr int kRowThreads = 256;
-constexpr int kChunk = 4096;       // pages a CTA ranks in a compaction
+constexpr int kChunk = 1024;       // pages a CTA ranks in a compaction
 constexpr int kPer = kChunk / kRowThreads;
 
 // Exclusive sum of v over the CTA's threads (a multiple of 32, at most 1024);

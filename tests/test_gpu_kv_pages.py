@@ -154,7 +154,7 @@ def test_reservation_of_many_rows_out_of_pages(gdn):
     assert gdn.get_device_error() == NONE_LEFT
 
 
-@pytest.mark.parametrize("num_pages,live", [(1, 0), (2, 0.5), (37, 0.0), (37, 1.0), (4096, 0.3), (4097, 0.7), (30000, 0.5), (30000, 0.01)])
+@pytest.mark.parametrize("num_pages,live", [(1, 0), (2, 0.5), (37, 0.0), (37, 1.0), (1024, 0.5), (1025, 0.4), (4096, 0.3), (4097, 0.7), (30000, 0.5), (30000, 0.01)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compaction(gdn, num_pages, live, in_place):
     rng = np.random.default_rng(num_pages)
