@@ -32,8 +32,13 @@ template <int D> struct Geo32 {
     static constexpr int WRS = D == 256 ? 2 : 1;   // and with up to 16 WRS rows: 8 / WRS shares of two tiles
     static constexpr int M = 16 * WRB;
     static constexpr int TILE = KT * LD;           // floats of a K or V tile
+    static constexpr int ROOM = D == 64 ? 28600 : 57600; // floats: half or all of an SM's shared memory
     static constexpr int STAGES = 4;               // tiles of K and V in shared memory: about 100 KB an SM under way
-    static constexpr int FLOATS = M * LD + 2 * STAGES * TILE;
+    static constexpr int FEW = 16 * WRS;           // rows that count as few: less room for Q, more for tiles
+    static constexpr int STAGES_FEW = D == 256 ? 5 : 6;
+    static constexpr int FLOATS0 = M * LD + 2 * STAGES * TILE, FLOATS1 = FEW * LD + 2 * STAGES_FEW * TILE;
+    static constexpr int FLOATS = FLOATS0 > FLOATS1 ? FLOATS0 : FLOATS1;
+    static_assert(FLOATS <= ROOM, "shared memory");
     static constexpr int PER_SM = D == 64 ? 2 : 1; // CTAs an SM, by shared memory
 };
 
@@ -186,7 +191,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
     constexpr int KT = G::KT, LD = G::LD;
     extern __shared__ __align__(16) float sm[];
     __shared__ Ctrl32 ctl;
-    float *const Q = sm, *const ring = sm + G::M * LD;
+    float *const Q = sm;
     const AttentionArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int ps = a.pages.page_size, hkv = a.pages.hkv;
@@ -212,7 +217,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         const Item it = ctl.item;
         const int32_t *const table = a.c.table + (size_t)it.row * a.c.max_pages;
         const int kvh = it.head / p.groups, rows = it.ntok * p.g, end = it.see + it.ntok - 1;
-        const bool few = rows <= 16 * G::WRS;
+        const bool few = rows <= G::FEW;
+        float *const ring = sm + (few ? G::FEW : G::M) * LD;
         const int wr_n = few ? G::WRS : G::WRB, wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n; // row block, share
         // Q: token rows of this head group
         {
@@ -224,24 +230,31 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
             }
         }
         const int n = it.jb - it.ja;
-        auto load = [&](int j) { // a group a tile, empty past the last; a thread keeps its column
-            constexpr int VR = D / 4 < kThreads ? D / 4 : kThreads, RP = kThreads / VR; // vectors a row, rows a pass
-            float *const K = ring + j % G::STAGES * 2 * G::TILE, *const V = K + G::TILE;
-            const int col = 4 * (tid % VR);
-            if (j < n) {
+        // A group of copies a tile, empty past the last; a thread keeps its column.  Pages are looked up a step
+        // before their copies, so that no copy waits for the table.
+        constexpr int VR = D / 4 < kThreads ? D / 4 : kThreads, RP = kThreads / VR, NR = KT / RP; // vectors a row, rows a pass
+        const int vrow = tid / VR, col = 4 * (tid % VR);
+        typedef int Pages[NR];
+        auto look = [&](Pages &pages, int j) {
 #pragma unroll
-                for (int r = 0; r < KT; r += RP) {
-                    const int row = r + tid / VR, key = (it.ja + j) * KT + row;
-                    int page = 0;
-                    if (key < end) {
-                        page = table[key >> a.pages.page_shift];
-                        if (page <= 0 || page >= a.pages.num_pages) {
-                            page = 0;
-                            atomicMin(&ctl.broken, key);
-                            report(a.err, GDN_DEVERR_BAD_PAGE);
-                        }
+            for (int i = 0; i < NR; ++i) {
+                const int key = (it.ja + j) * KT + i * RP + vrow;
+                pages[i] = j < n && key < end ? table[key >> a.pages.page_shift] : -1;
+            }
+        };
+        auto load = [&](const Pages &pages, int j, int stage) {
+            if (j < n) {
+                float *const K = ring + stage * 2 * G::TILE, *const V = K + G::TILE;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const int row = i * RP + vrow, key = (it.ja + j) * KT + row;
+                    int page = pages[i];
+                    if (key < end && (page <= 0 || page >= a.pages.num_pages)) {
+                        page = 0;
+                        atomicMin(&ctl.broken, key);
+                        report(a.err, GDN_DEVERR_BAD_PAGE);
                     }
-                    const size_t at = (((size_t)page * hkv + kvh) * ps + (key & (ps - 1))) * D + col;
+                    const size_t at = (((size_t)max(page, 0) * hkv + kvh) * ps + (key & (ps - 1))) * D + col;
                     copy16(K + row * LD + col, static_cast<const float *>(a.pages.k) + at, page > 0);
                     copy16(V + row * LD + col, static_cast<const float *>(a.pages.v) + at, page > 0);
                 }
@@ -249,12 +262,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // the elements of V that this thread copied: what is not finite becomes zero
-        auto scan = [&](int j) {
-            constexpr int VR = D / 4 < kThreads ? D / 4 : kThreads, RP = kThreads / VR;
-            float *const V = ring + (j % G::STAGES * 2 + 1) * G::TILE;
+        auto scan = [&](int stage) {
+            float *const V = ring + (stage * 2 + 1) * G::TILE;
 #pragma unroll
-            for (int r = 0; r < KT; r += RP) {
-                uint4 *const at = reinterpret_cast<uint4 *>(V + (r + tid / VR) * LD + 4 * (tid % VR));
+            for (int i = 0; i < NR; ++i) {
+                uint4 *const at = reinterpret_cast<uint4 *>(V + (i * RP + vrow) * LD + col);
                 uint4 v = *at;
                 if (odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w)) {
                     v = make_uint4(odd(v.x) ? 0u : v.x, odd(v.y) ? 0u : v.y, odd(v.z) ? 0u : v.z, odd(v.w) ? 0u : v.w);
@@ -270,36 +282,52 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         for (int n = 0; n < D / 8; ++n)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         // this warp's step on tile j, on keys kb .. of it
-        auto work = [&](int j, int kb, auto nt) {
+        auto work = [&](int j, int stage, int kb, auto nt) {
             const int key = (it.ja + j) * KT + kb;
-            const float *const K = ring + j % G::STAGES * 2 * G::TILE + kb * LD;
+            const float *const K = ring + stage * 2 * G::TILE + kb * LD;
             tile_step<D, decltype(nt)::value>(Q + 16 * wr * LD, K, K + G::TILE, s0 - key, s8 - key, c2, o, m0, m8, l0, l8);
         };
-        for (int j = 0; j < G::STAGES - 1; ++j)
-            load(j);
-        if (few) { // two tiles at a time: 8 keys a warp
-            constexpr int SH = KT / 8; // shares of a tile
+        if (few) { // two tiles at a time, 8 keys a warp; SF - 2 tiles ahead
+            constexpr int SH = KT / 8, SF = G::STAGES_FEW, A = SF - 2; // shares of a tile
+            Pages pages[A];
+#pragma unroll
+            for (int i = 0; i < A; ++i)
+                look(pages[i], i);
+#pragma unroll
+            for (int i = 0; i < A; ++i)
+                load(pages[i], i, i);
+            look(pages[0], A), look(pages[1], A + 1);
             for (int j = 0; j < n; j += 2) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(G::STAGES - 3) : "memory");
-                scan(j);
+                asm volatile("cp.async.wait_group %0;" ::"n"(A - 2) : "memory");
+                scan(j % SF);
                 if (j + 1 < n)
-                    scan(j + 1);
-                __syncthreads(); // the tiles are there for all
-                load(j + G::STAGES - 1);
+                    scan((j + 1) % SF);
+                __syncthreads(); // the tiles are there for all, and those before them are done with
+                load(pages[0], j + A, (j + A) % SF);
+                load(pages[1], j + A + 1, (j + A + 1) % SF);
+                look(pages[0], j + A + 2), look(pages[1], j + A + 3);
                 const int mine = j + wk / SH;
                 if (16 * wr < rows && mine < n)
-                    work(mine, wk % SH * 8, Width<1>());
-                __syncthreads(); // and done with
-                load(j + G::STAGES);
+                    work(mine, mine % SF, wk % SH * 8, Width<1>());
             }
         } else {
+            constexpr int S = G::STAGES, A = S - 1;
+            Pages pages[A];
+#pragma unroll
+            for (int i = 0; i < A; ++i)
+                look(pages[i], i);
+#pragma unroll
+            for (int i = 0; i < A; ++i)
+                load(pages[i], i, i);
+            look(pages[0], A);
             for (int j = 0; j < n; ++j) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(G::STAGES - 2) : "memory");
-                scan(j);
+                asm volatile("cp.async.wait_group %0;" ::"n"(A - 1) : "memory");
+                scan(j % S);
                 __syncthreads(); // the tile is there for all, and the one before it is done with
-                load(j + G::STAGES - 1);
+                load(pages[0], j + A, (j + A) % S);
+                look(pages[0], j + A + 1);
                 if (16 * wr < rows)
-                    work(j, wk * (KT / (8 / G::WRB)), Width<KT * G::WRB / 64>());
+                    work(j, j % S, wk * (KT / (8 / G::WRB)), Width<KT * G::WRB / 64>());
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
