@@ -42,6 +42,16 @@ template <int D> struct Geo32 {
     static constexpr int PER_SM = D == 64 ? 2 : 1; // CTAs an SM, by shared memory
 };
 
+// Units of a tile, by its time: few rows; up to half of the row blocks at work; more.  (Measured: 1.25, 3.65 and 5.7 us
+// of a CTA at d = 64, 1.39, 3.8 and 5.5 at d = 128, 2.3, 4.0 and 4.0 at d = 256.)
+template <int D> struct Cost32 {
+    static constexpr int least = 4, half = D == 64 ? 12 : D == 128 ? 11 : 7, most = D == 64 ? 18 : D == 128 ? 16 : 7;
+    static __device__ __forceinline__ int of(int rows)
+    {
+        return rows <= 16 * Geo32<D>::WRS ? least : 2 * rows <= Geo32<D>::M ? half : most;
+    }
+};
+
 struct Ctrl32 {
     long long scan[kThreads / 32];
     Found found;
@@ -198,9 +208,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
     const float c2 = a.scale * 1.44269504088896341f;
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Run run = plan_run<kThreads, KT>(p, p.tq, ctl.scan, ctl.found);
+    const Run run = plan_run<kThreads, KT, Cost32<D>>(p, p.tq, ctl.scan, ctl.found);
     zero_dead<float, D, kThreads>(p, tid);
-    Walk walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
+    Walk<Cost32<D>> walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
     for (;;) {
         __syncthreads();
         if (warp == 0) {

@@ -3,8 +3,9 @@
 //
 // An item is one key head (or a share of its query heads, where it has more
 // than a tile holds) and up to `mt` consecutive new tokens of a cache row; its
-// keys come in tiles of KT.  All items' key tiles, in order, are cut into equal
-// runs, one a CTA: every CTA finds its run from the lengths on the device.
+// keys come in tiles of KT.  All items' key tiles, in order, are cut into runs
+// of equal cost, one a CTA: every CTA finds its run from the lengths on the
+// device.  Costs are in units, a tile's given by its item's rows.
 // Included by one translation unit a kernel; everything here has internal
 // linkage.
 #pragma once
@@ -28,6 +29,13 @@ struct Item {
 // item's second part.
 struct Cut {
     int parts, tok, ntok, head;
+};
+
+// Units of a key tile of an item with `rows` rows: kernels whose tiles cost the
+// same whatever the rows, and others.
+struct EvenCost {
+    static constexpr int least = 1, most = 1;
+    static __device__ __forceinline__ int of(int) { return 1; }
 };
 
 // A call's arguments with its division.  Query heads are taken g at a time
@@ -101,12 +109,12 @@ __device__ __forceinline__ int item_tiles(const Row &x, int t, int mt, int kt)
     return (x.len - x.n + last + kt - 1) / kt;
 }
 __device__ __forceinline__ int items_of(const Row &x, int mt) { return (x.n + mt - 1) / mt; }
-__device__ long long head_tiles(const Row &x, int mt, int kt) // of one key head
+template <typename Cost> __device__ long long head_units(const Row &x, int mt, int kt, int g) // of one key head
 {
     long long s = 0;
     const int n = items_of(x, mt);
     for (int t = 0; t < n; ++t)
-        s += item_tiles(x, t, mt, kt);
+        s += item_tiles(x, t, mt, kt) * (long long)Cost::of(min(mt, x.n - t * mt) * g);
     return s;
 }
 
@@ -136,12 +144,14 @@ __device__ __forceinline__ long long scan64(long long v, long long *part, int wa
     return before;
 }
 
-// This CTA's run of the units (key tiles) 0 .. total: [u0, u1), beginning in
-// `row`, whose units begin at `base`.  Called by the whole CTA; `part` is a
-// long long a warp, and `found` the place where one thread leaves the row.
+// This CTA's run of the units 0 .. total, the tiles that begin in [u0, u1): u0
+// lies in `row`, whose units begin at `base`.  A run is no shorter than a tile,
+// so that every run between an item's first and last has a part of it.  Called
+// by the whole CTA; `part` is a long long a warp, and `found` the place where
+// one thread leaves the row.
 struct Run {
     long long share, u0, u1, base;
-    long long per; // key tiles a head of the row it begins in
+    long long per; // units a head of the row it begins in
     int row;
     Row first;     // that row
 };
@@ -150,7 +160,7 @@ struct Found { // shared memory
     int row;
     Row first;
 };
-template <int THREADS, int KT> __device__ Run plan_run(const WorkArgs &p, int mt, long long *part, Found &found)
+template <int THREADS, int KT, typename Cost> __device__ Run plan_run(const WorkArgs &p, int mt, long long *part, Found &found)
 {
     const CacheRows &c = p.a.c;
     const int ps = p.a.pages.page_size, heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
@@ -160,21 +170,26 @@ template <int THREADS, int KT> __device__ Run plan_run(const WorkArgs &p, int mt
         if (r >= c.rows)
             return 0;
         x = row_of(c, ps, r);
-        per = x.live ? head_tiles(x, mt, KT) : 0;
+        per = x.live ? head_units<Cost>(x, mt, KT, p.g) : 0;
         return per * heads;
     };
+    int dearest = 1; // tile of this thread's rows
     Run run;
     long long total = 0, cost = 0, before = 0, sum;
     for (int b = 0; b < c.rows; b += THREADS) {
         cost = cost_of(b + tid);
+        if (cost > 0)
+            dearest = max(dearest, Cost::of(min(x.n, mt) * p.g));
         if (x.bad && blockIdx.x == 0)
             report(p.a.err, GDN_DEVERR_BAD_PAGE);
         before = scan64(cost, part, THREADS / 32, sum);
         total += sum;
     }
     run.share = (total + gridDim.x - 1) / gridDim.x;
-    if (run.share < 1)
-        run.share = 1;
+    // (Cost's values are few, and one barrier tells whether a thread has seen more than the least)
+    const int least = Cost::least, tile = Cost::most == least ? least : __syncthreads_or(dearest > least) ? Cost::most : least;
+    if (run.share < tile)
+        run.share = tile;
     run.u0 = run.share * blockIdx.x;
     run.u1 = min(total, run.u0 + run.share);
     if (c.rows <= THREADS) { // the one pass has it
@@ -226,11 +241,11 @@ template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkAr
 }
 
 // The items of a run, in order, by one warp.
-struct Walk {
+template <typename Cost> struct Walk {
     const WorkArgs &p;
     const Run &run;
     int mt, kt, heads, lane;
-    long long u;     // the next unit
+    long long u;     // where the next tile begins
     int r, win;      // row; rows win .. win + 31 are in the lanes
     Row mine, x;     // a lane's row; the current one
     int items, h, t, ja;
@@ -249,9 +264,26 @@ struct Walk {
             long long rem = u - run.base; // the run begins inside this row
             for (; rem >= run.per; ++h)
                 rem -= run.per;
-            while (rem >= item_tiles(x, t, mt, kt))
-                rem -= item_tiles(x, t++, mt, kt);
-            ja = (int)rem;
+            for (;; ++t) {
+                const long long units = item_tiles(x, t, mt, kt) * (long long)unit();
+                if (rem < units)
+                    break;
+                rem -= units;
+            }
+            ja = (int)((rem + unit() - 1) / unit());
+            u += (long long)ja * unit() - rem; // a tile that began before u0 is the run's before
+            if (ja == item_tiles(x, t, mt, kt))
+                done();
+        }
+    }
+    __device__ int unit() const { return Cost::of(min(mt, x.n - t * mt) * p.g); }
+    __device__ void done() // with item t
+    {
+        ja = 0;
+        if (++t == items) {
+            t = 0;
+            if (++h == heads)
+                in_row = false, ++r;
         }
     }
     __device__ void enter(const Row &row)
@@ -288,20 +320,16 @@ struct Walk {
             enter(x);
         }
         const int J = item_tiles(x, t, mt, kt);
-        const int jb = (int)min((long long)J, ja + (run.u1 - u));
+        const int w = unit(), jb = (int)min((long long)J, ja + (run.u1 - u + w - 1) / w);
         const int t0 = t * mt, ntok = min(mt, x.n - t0);
         it = {x.b + t0, ntok, h, r, x.len - x.n + t0 + 1, ja, jb,
               ja > 0 || jb < J ? 2 * (int)blockIdx.x + (ja > 0 ? 0 : 1) : -1};
         // the run that holds an item's second part lists it for the combining kernel
-        if (lane == 0 && ja > 0 && u - run.share <= u - ja)
-            p.cuts[blockIdx.x] = {1 + (int)((J - ja + run.share - 1) / run.share), x.b + t0, ntok, h};
-        u += jb - ja;
-        ja = 0;
-        if (++t == items) {
-            t = 0;
-            if (++h == heads)
-                in_row = false, ++r;
-        }
+        const long long start = u - (long long)ja * w;
+        if (lane == 0 && ja > 0 && start >= run.u0 - run.share)
+            p.cuts[blockIdx.x] = {2 + (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x, x.b + t0, ntok, h};
+        u += (long long)(jb - ja) * w;
+        done();
         return true;
     }
 };

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const Run run = plan_run<G::THREADS, KT>(p, mt, ctl.scan, ctl.found);
+    const Run run = plan_run<G::THREADS, KT, EvenCost>(p, mt, ctl.scan, ctl.found);
     bool alive = true; // false once a bounded wait ran out
     auto wait_at = [&](uint32_t b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
         if (!__all_sync(0xffffffffu, mbar_try(b, parity)) && alive && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 3) {
             // ---- the walk: this run's items, in order
-            Walk walk(p, run, mt, KT);
+            Walk<EvenCost> walk(p, run, mt, KT);
             Item it;
             for (int q = 0; alive; ++q) {
                 const bool more = walk.next(it);
