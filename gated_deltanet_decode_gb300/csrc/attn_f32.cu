@@ -107,7 +107,7 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             s[n][e] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
     for (int k0 = 0; k0 < D / 8; k0 += 4) {
         constexpr int APART = NT == 1 ? 4 : 1;
         float t[NT][APART][4];
