@@ -14,7 +14,7 @@
 // tiles come by 16-byte asynchronous copies, three or four tiles ahead.
 //
 // Bound: issue slots and the products together.  Of 13 rows of 1 to 250 tokens
-// over up to 2.1 k (12 heads over 4 of 64), 160 us, the products' own time is
+// over up to 2.1 k (12 heads over 4 of 64), 148 us, the products' own time is
 // 64 at 301 TFLOP/s (packed fp32 FMAs would take 81), and splitting operands
 // takes as many slots.  Decode streams at 3.6 to 4 TB/s.
 //
@@ -24,6 +24,8 @@
 #include "attn_plan.cuh"
 
 #include <atomic>
+
+#include "gdn_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -74,6 +76,13 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
 {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// Two at a time: the tails by one instruction.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &xh, uint32_t &xl, uint32_t &yh, uint32_t &yl)
+{
+    xh = (__float_as_uint(x) + 0x1000u) & 0xffffe000u, yh = (__float_as_uint(y) + 0x1000u) & 0xffffe000u;
+    const float2 t = fma2(make_float2(__uint_as_float(xh), __uint_as_float(yh)), make_float2(-1.f, -1.f), make_float2(x, y));
+    xl = __float_as_uint(t.x), yl = __float_as_uint(t.y);
 }
 template <int N> struct Width {
     static constexpr int value = N;
@@ -135,8 +144,7 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
             for (int n = 0; n < NT; ++n) {
                 const float *kp = k + (8 * n + g) * LD + 8 * (k0 + ks) + c;
                 uint32_t h0, h1, t0, t1;
-                split(kp[0], h0, t0);
-                split(kp[4], h1, t1);
+                split2(kp[0], kp[4], h0, t0, h1, t1);
                 float(&d)[4] = t[n][ks % APART];
                 mma8(d, al, h0, h1);
                 mma8(d, ah, t0, t1);
@@ -189,8 +197,7 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             uint32_t h0, h1, t0, t1;
-            split(vp[8 * n * LD + 8 * e], h0, t0);
-            split(vp[8 * n * LD + 8 * e + LD], h1, t1);
+            split2(vp[8 * n * LD + 8 * e], vp[8 * n * LD + 8 * e + LD], h0, t0, h1, t1);
             mma8(d, al[n], h0, h1);
             mma8(d, ah[n], t0, t1);
             mma8(d, ah[n], h0, h1);
@@ -347,12 +354,32 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        // the shares' sums to shared memory, in place of the tiles
 #pragma unroll
         for (int x = 1; x < 4; x <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, x);
             l8 += __shfl_xor_sync(0xffffffffu, l8, x);
         }
+        const float NaN = __int_as_float(0x7fc00000);
+        if (wk_n == 1 && !ctl.dirty) { // a warp has all of its rows' sums: out of its registers
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int row = x ? r8 : r0, t = row / p.g;
+                const bool bad = (x ? s8 : s0) > ctl.broken;
+                const float m = x ? m8 : m0, l = x ? l8 : l0, i = it.part >= 0 ? 1.f : 1.f / l;
+                float *const to = it.part >= 0 ? p.part_o + ((size_t)it.part * p.rows_max + row) * D
+                                               : static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + it.head * p.g + (row - t * p.g)) * D;
+                if (row < rows) {
+                    if (it.part >= 0 && c == 0)
+                        p.part_ml[(size_t)it.part * p.rows_max + row] = make_float2(bad ? NaN : m, l);
+#pragma unroll
+                    for (int e = 0; e < D / 8; ++e)
+                        *reinterpret_cast<float2 *>(to + 8 * e + 2 * c) = it.part < 0 && bad ? make_float2(0.f, 0.f)
+                                                                                             : make_float2(o[e][2 * x] * i, o[e][2 * x + 1] * i);
+                }
+            }
+            continue;
+        }
+        // the shares' sums to shared memory, in place of the tiles
         float *const mine = ring + (size_t)(wk * 16 * wr_n + r0) * LD;
         if (16 * wr < rows) {
 #pragma unroll
@@ -364,7 +391,6 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
                 ctl.ml[wk * 16 * wr_n + r0] = make_float2(m0, l0), ctl.ml[wk * 16 * wr_n + r8] = make_float2(m8, l8);
         }
         __syncthreads();
-        const float NaN = __int_as_float(0x7fc00000);
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), col = 4 * (x - row * (D / 4)), t = row / p.g, see = it.see + t;
             const bool bad = see > ctl.broken;
