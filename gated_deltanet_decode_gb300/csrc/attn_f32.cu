@@ -14,9 +14,9 @@
 // tiles come by 16-byte asynchronous copies, three or four tiles ahead.
 //
 // Bound: issue slots and the products together.  Of 13 rows of 1 to 250 tokens
-// over up to 2.1 k (12 heads over 4 of 64), 148 us, the products' own time is
+// over up to 2.1 k (12 heads over 4 of 64), 144 us, the products' own time is
 // 64 at 301 TFLOP/s (packed fp32 FMAs would take 81), and splitting operands
-// takes as many slots.  Decode streams at 3.6 to 4 TB/s.
+// takes as many slots.  Decode streams at 4.1 to 4.4 TB/s (d = 256: 2.4).
 //
 // A weight of zero does not hide a NaN or an infinity, and infinity has no
 // tail.  So an item whose sums come out finite is done; otherwise a second pass
@@ -40,6 +40,13 @@ template <int D> struct Geo32 {
     static constexpr int WRB = D == 256 ? 4 : 8;   // row blocks with many rows: 8 / WRB shares of a tile,
     static constexpr int WRS = D == 256 ? 2 : 1;   // and with up to 16 WRS rows: 8 / WRS shares of two tiles
     static constexpr int M = 16 * WRB;
+    // Row blocks with more than few rows: up to 32 rows two, with four shares of the keys (a CTA's tile takes 2.0 us
+    // instead of 3.0 at d = 64 and of 3.6 at d = 128); up to 64 four at d = 128 (3.0 us; at d = 64, where two CTAs share an
+    // SM, it makes no difference).
+    static __device__ __forceinline__ int blocks(int rows)
+    {
+        return D == 256 ? WRB : rows <= 32 ? 2 : D == 128 && rows <= 64 ? 4 : WRB;
+    }
     static constexpr int TILE = KT * LD;           // floats of a K or V tile
     static constexpr int ROOM = D == 64 ? 28600 : 57600; // floats: half or all of an SM's shared memory
     static constexpr int STAGES = 4;               // tiles of K and V in shared memory: about 100 KB an SM under way
@@ -51,13 +58,13 @@ template <int D> struct Geo32 {
     static constexpr int PER_SM = D == 64 ? 2 : 1; // CTAs an SM, by shared memory
 };
 
-// Units of a tile, by its time: few rows; up to half of the row blocks at work; more.  (Measured: 1.25, 3.65 and 5.7 us
-// of a CTA at d = 64, 1.39, 3.8 and 5.5 at d = 128, 2.3, 4.0 and 4.0 at d = 256.)
+// Units of a tile, by its time.  (Measured, us of a CTA: up to 16, 32, 64 and 128 rows 1.13, 2.0, 3.1 and 5.3 at d = 64
+// and 1.19, 2.0, 3.0 and 5.3 at d = 128; up to 32 and 64 rows 2.0 and 3.7 at d = 256.)
 template <int D> struct Cost32 {
-    static constexpr int least = 4, half = D == 64 ? 12 : D == 128 ? 11 : 7, most = D == 64 ? 18 : D == 128 ? 16 : 7;
+    static constexpr int least = 4, most = D == 256 ? 7 : 18;
     static __device__ __forceinline__ int of(int rows)
     {
-        return rows <= 16 * Geo32<D>::WRS ? least : 2 * rows <= Geo32<D>::M ? half : most;
+        return rows <= 16 * Geo32<D>::WRS ? least : D == 256 ? most : rows <= 32 ? 7 : rows <= 64 ? 11 : most;
     }
 };
 
@@ -243,7 +250,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         const int kvh = it.head / p.groups, rows = it.ntok * p.g, end = it.see + it.ntok - 1;
         const bool few = rows <= G::FEW;
         float *const ring = sm + (few ? G::FEW : G::M) * LD;
-        const int wr_n = few ? G::WRS : G::WRB, wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n; // row block, share
+        const int wr_n = few ? G::WRS : G::blocks(rows), wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n; // row block, share
         // Q: token rows of this head group
         {
             const float *const src = static_cast<const float *>(a.q) + (size_t)it.tok * a.q_stride + (size_t)it.head * p.g * D;
@@ -356,8 +363,15 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
                     __syncthreads(); // the tile is there for all, and the one before it is done with
                     load(pages[0], j + A, (j + A) % S);
                     look(pages[0], j + A + 1);
-                    if (16 * wr < rows)
-                        work(j, j % S, wk * (KT / (8 / G::WRB)), Width<KT * G::WRB / 64>());
+                    const int kb = wk * (KT / wk_n);
+                    if (16 * wr >= rows)
+                        continue;
+                    if (D == 256 || wr_n == 2)
+                        work(j, j % S, kb, Width<1>());
+                    else if (D == 128 && wr_n == 4)
+                        work(j, j % S, kb, Width<2>());
+                    else
+                        work(j, j % S, kb, Width<KT / 8>());
                 }
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
