@@ -113,6 +113,35 @@ def test_later_tokens_of_a_chunk_do_not_reach_earlier_ones(gdn, dtype, bad):
     assert not torch.isfinite(out[50:70].float()).all(-1).any() or bad == float("inf")
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(12, 4, 64), (16, 4, 128), (14, 2, 256), (2, 2, 128)])
+def test_fp32_items_of_every_number_of_rows(gdn, hq, hkv, d):
+    """Tokens about where the rows of a tile take more or fewer of its warps, in runs of unequal cost."""
+    new = [1, 4, 5, 6, 8, 9, 10, 11, 16, 17, 21, 22, 33, 42, 43, 65]
+    lens = [n + 37 * (i % 5) + (900 if i % 3 == 0 else 0) for i, n in enumerate(new)]
+    c = Cache(lens, "f32", hkv, d, 16, seed=hq, poison=float("nan"))
+    q, out = run(gdn, c, new, hq)
+    check_attention(out, *attention_ref(c, q, new, d ** -0.5), "f32")
+    assert gdn.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_values_that_are_not_finite_stay_in_their_columns(gdn, dtype, n):
+    """A long row cut into many parts: the columns of V that hold an infinity or a NaN, and no others, show it, for the
+    tokens that see it."""
+    c = Cache([9001], dtype, 1, 128, 16, seed=n)
+    q, want = run(gdn, c, [n], 4)
+    late = 9000  # the last token's own key
+    for at, col, bad in ((5000, 3, float("inf")), (5001, 3, float("inf")), (8000, 77, float("nan")), (late, 100, float("inf"))):
+        c.v[0, c.table[0, at // 16], 0, at % 16, col] = bad
+    q, out = run(gdn, c, [n], 4, q=q)
+    assert (out[:, :, 3] == float("inf")).all() and torch.isnan(out[:, :, 77]).all()
+    assert (out[-1, :, 100] == float("inf")).all() and torch.isfinite(out[:-1, :, 100]).all()
+    rest = [x for x in range(128) if x not in (3, 77, 100)]
+    ref, mag = attention_ref(c, q, [n], 128 ** -0.5)
+    check_attention(out[:, :, rest], ref[:, :, rest], mag[:, :, rest], dtype)
+
+
 def test_layers_strides_and_given_buffers(gdn):
     c = Cache([77, 130], "bf16", 2, 128, 16, layers=3, seed=6)
     new, hq = [3, 60], 6
