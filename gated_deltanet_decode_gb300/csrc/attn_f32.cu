@@ -9,9 +9,9 @@
 //
 // Rows (token, head) are packed as in the bf16 kernel, 16 WR a tile; 8 warps
 // stand as WR row blocks of 16 x WK shares of a tile's keys.  Few rows (decode,
-// verification) take WR small and split the keys instead.  Each warp keeps its own O, m and
-// l; the shares are joined through shared memory at the item's end.  K and V
-// tiles come by 16-byte asynchronous copies, three or four tiles ahead.
+// verification) take WR small and split the keys instead.  Each warp keeps its
+// own O, m and l; shares are joined through shared memory at the item's end.  K
+// and V tiles come by 16-byte asynchronous copies, three or four tiles ahead.
 //
 // Bound: issue slots and the products together.  Of 13 rows of 1 to 250 tokens
 // over up to 2.1 k (12 heads over 4 of 64), 145 us, the products' own time is

@@ -80,7 +80,7 @@ template <int D> struct Geo {
     static constexpr int O0 = 2 * KT;                    // O of accumulator o: O0 + o D
     static constexpr int RING = QBYTES * NQ;
     static constexpr int CTRL = RING + SBYTES * STAGES;
-    static constexpr int TOTAL = CTRL + 3072;            // and the control block
+    static constexpr int TOTAL = CTRL + 3 * 1024;            // and the control block
 };
 
 // The control block in shared memory, after Q and the ring.
@@ -100,7 +100,7 @@ struct Ctrl {
     int bad[2];             // first key that could not be read, by group
     int dirty;              // 1 + the last item with a non-finite V element that only some of its tokens see
 };
-static_assert(sizeof(Ctrl) <= 3072, "control block");
+static_assert(sizeof(Ctrl) <= 3 * 1024, "control block");
 
 // ---- tensor core and copy wrappers ----
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart
