@@ -98,7 +98,10 @@ struct Ctrl {
     uint32_t tmem;
     float ml[2][128][2];    // (m, l) of the two groups' rows, for the merge
     int bad[2];             // first key that could not be read, by group
-    int dirty;              // 1 + the last item with a non-finite V element that only some of its tokens see
+    // 1 + the last item of a queue parity with a non-finite V element that only some of its tokens see.  Two words, as the
+    // groups of a pair do not meet at its end: a warp may be in item q + 1 before another has looked at item q's word.  None
+    // is in item q + 2 then, whose scores come after weights that every warp hands over in item q + 1, or after a meeting.
+    int dirty[2];
 };
 static_assert(sizeof(Ctrl) <= 3 * 1024, "control block");
 
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             mbar_init(bar(ctl.ifull[i]), 1), mbar_init(bar(ctl.iempty[i]), G::QUEUE_READERS);
         mbar_init(bar(ctl.drain), 1);
         mbar_init(bar(ctl.merge), 8);
-        ctl.dirty = 0;
+        ctl.dirty[0] = ctl.dirty[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     before_sync();
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                         } else {
                             uint4 z = *at;
                             if (!(finite2(z.x) && finite2(z.y) && finite2(z.z) && finite2(z.w))) {
-                                *reinterpret_cast<volatile int *>(&ctl.dirty) = q + 1;
+                                *reinterpret_cast<volatile int *>(&ctl.dirty[q & 1]) = q + 1;
                                 __threadfence_block(); // before the zeros: the other group may scan this tile too
                                 z.x = drop2(z.x), z.y = drop2(z.y), z.z = drop2(z.z), z.w = drop2(z.w);
                                 *at = z;
@@ -770,7 +773,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 after_sync();
             }
             const bool bad = see > broken;
-            const bool dirty = *reinterpret_cast<volatile int *>(&ctl.dirty) == q + 1;
+            const bool dirty = *reinterpret_cast<volatile int *>(&ctl.dirty[q & 1]) == q + 1;
             if (!idle) {
                 const int o = pair ? grp : 0;
                 const int k0 = G::NO == 2 && !pair ? grp * (D / 2) : 0, k1 = G::NO == 2 && !pair ? k0 + D / 2 : D;

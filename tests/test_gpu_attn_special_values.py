@@ -1,0 +1,51 @@
+"""paged_attention on the GPU where keys or values are infinite, NaN or at the top of their type's range: against the
+definition in 64 bits, in which such a value reaches the tokens that see it and no others."""
+import numpy as np
+import pytest
+import torch
+
+from attn_helpers import DEV, TYPES, Cache, attention_ref, i32, packed
+
+pytestmark = pytest.mark.gpu
+
+
+def run(G, c, new, hq, seed=1, scale=None, q=None):
+    if q is None:
+        q = torch.randn(sum(new), hq, c.d, generator=torch.Generator().manual_seed(seed)).to(TYPES[c.dtype])
+    return q, G.paged_attention(q.to(DEV), c.pool(G), i32(c.table), i32(c.lens), i32(packed(new)), scale=scale)
+
+
+def place(c, row, key):
+    """Index of a row's key in the pools, without the head and the column."""
+    return c.table[row, key // c.page], key % c.page
+
+
+def check(out, ref, mag, dtype):
+    """The tolerances of the parity tests where the definition is finite, and its very values where it is not."""
+    o = out.double().cpu()
+    fine = torch.isfinite(ref)
+    tol = 2.0 ** -8 * (ref.abs() + mag) if dtype == "bf16" else 4e-5 * mag
+    assert (torch.isnan(o) == torch.isnan(ref)).all()
+    assert (o[torch.isinf(ref)] == ref[torch.isinf(ref)]).all()
+    worst = ((o - ref).abs() - tol)[fine].max().item()
+    assert worst <= 0, f"out of tolerance by {worst:.3g}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (4, 2, 256)])
+def test_items_in_a_row_with_values_that_are_not_finite(gdn, dtype, hq, hkv, d):
+    """Prompts of one or two tiles of tokens, several to a run, whose keys are hidden from some of their own tokens: each
+    item keeps its own infinities and NaN, whatever the next one finds."""
+    rng = np.random.default_rng(d)
+    rows = 260
+    new = [int(rng.integers(50, 64)) for _ in range(rows)]
+    lens = [n + int(rng.integers(0, 40)) for n in new]
+    c = Cache(lens, dtype, hkv, d, 16, seed=d, poison=float("nan"))
+    for r in range(rows):
+        for x in range(int(rng.integers(1, 3))):
+            key = int(rng.integers(lens[r] - new[r], lens[r]))
+            page, slot = place(c, r, key)
+            c.v[0, page, int(rng.integers(0, hkv)), slot, int(rng.integers(0, d))] = (float("inf"), float("nan"), -float("inf"))[r % 3]
+    q, out = run(gdn, c, new, hq)
+    check(out, *attention_ref(c, q, new, d ** -0.5), dtype)
+    assert gdn.get_device_error() == 0
