@@ -27,11 +27,18 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 
 
-def _nvcc() -> str:
+def _find_nvcc():
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
             return cand
-    raise RuntimeError("nvcc not found: the GDN decode library needs the CUDA toolkit to build")
+    return None
+
+
+def _nvcc() -> str:
+    nvcc = _find_nvcc()
+    if nvcc is None:
+        raise RuntimeError("nvcc not found: the GDN decode library needs the CUDA toolkit to build")
+    return nvcc
 
 
 def _stale() -> bool:
@@ -59,8 +66,8 @@ def _start_binding(force: bool):
     newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, os.path.join(ROOT, "include", "gdn_decode.h")))
     if not force and os.path.exists(path) and os.path.getmtime(path) >= newest:
         return None
-    gxx, nvcc = shutil.which("g++"), _nvcc()
-    if not gxx:
+    gxx, nvcc = shutil.which("g++"), _find_nvcc()  # the toolkit's headers lie beside nvcc
+    if not gxx or not nvcc:
         return None
     base = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),

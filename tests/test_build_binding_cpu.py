@@ -1,0 +1,48 @@
+"""The compiled binding is optional: the package loads, and calls through ctypes, wherever the binding cannot be made or
+used.  Each case loads a copy of the package in a process of its own."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = "gated_deltanet_decode_gb300"
+
+LOAD = """
+import os, shutil, sys
+hidden = sys.argv[1].split(",")
+which, exists = shutil.which, os.path.exists
+shutil.which = lambda name, *a, **k: None if name in hidden else which(name, *a, **k)
+os.path.exists = lambda p: not ("nvcc" in hidden and str(p).endswith("bin/nvcc")) and exists(p)
+from gated_deltanet_decode_gb300 import _lib
+assert _lib.load().paged_attention
+print("binding" if _lib.fast() else "ctypes")
+"""
+
+
+@pytest.fixture
+def package(tmp_path):
+    """A copy of the package with its library, up to date, and no binding."""
+    from gated_deltanet_decode_gb300 import build
+    build.build()
+    shutil.copytree(os.path.join(ROOT, PKG), tmp_path / PKG,
+                    ignore=shutil.ignore_patterns("_fast_binding*", "__pycache__", "_build"))
+    shutil.copytree(os.path.join(ROOT, "include"), tmp_path / "include")
+    return tmp_path
+
+
+def load(package, without="", path=None):
+    """How the copy makes its calls, where the programs of `without` are missing."""
+    env = dict(os.environ, PYTHONPATH=str(package))
+    if path:
+        env["PATH"] = f"{path}{os.pathsep}{env['PATH']}"
+    r = subprocess.run([sys.executable, "-c", LOAD, without], cwd=package, env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    return r.stdout.split()[-1]
+
+
+def test_without_a_toolkit_the_built_library_loads(package):
+    assert load(package, without="nvcc") == "ctypes"
+    assert load(package, without="g++") == "ctypes"
