@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 from . import build as _build
 
@@ -128,15 +129,19 @@ _fast = None  # the C++ binding of the attention layers, where it was built
 
 
 def _load_fast(L):
-    """The C++ binding, told where the library's functions are; None without it."""
+    """The C++ binding, told where the library's functions are; None without one that loads."""
     import importlib.machinery
     import importlib.util
     path = _build.binding_path()
     if not os.path.exists(path):
         return None
-    loader = importlib.machinery.ExtensionFileLoader("_fast_binding", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast_binding", loader, origin=path))
-    loader.exec_module(module)
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_fast_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast_binding", loader, origin=path))
+        loader.exec_module(module)
+    except Exception as e:  # a broken file, or one that was built for another PyTorch
+        warnings.warn(f"the C++ binding does not load ({e}); the package calls through ctypes")
+        return None
     module.bind(*(ctypes.cast(getattr(L, f), _P).value for f in (
         "attn_prologue", "paged_attention_workspace_bytes", "paged_attention", "kv_pages_fork", "kv_pages_free",
         "kv_pages_copy")))

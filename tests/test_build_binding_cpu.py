@@ -1,6 +1,7 @@
 """The compiled binding is optional: the package loads, and calls through ctypes, wherever the binding cannot be made or
 used.  Each case loads a copy of the package in a process of its own."""
 import os
+import pathlib
 import shutil
 import subprocess
 import sys
@@ -33,6 +34,15 @@ def package(tmp_path):
     return tmp_path
 
 
+def give_binding(package):
+    """The binding that was built here, put into the copy."""
+    from gated_deltanet_decode_gb300 import build
+    name = os.path.basename(build.binding_path())
+    if not os.path.exists(build.binding_path()):
+        pytest.skip("no compiler for the binding")
+    return pathlib.Path(shutil.copy2(build.binding_path(), package / PKG / name))
+
+
 def load(package, without="", path=None):
     """How the copy makes its calls, where the programs of `without` are missing."""
     env = dict(os.environ, PYTHONPATH=str(package))
@@ -46,3 +56,10 @@ def load(package, without="", path=None):
 def test_without_a_toolkit_the_built_library_loads(package):
     assert load(package, without="nvcc") == "ctypes"
     assert load(package, without="g++") == "ctypes"
+
+
+def test_a_binding_that_cannot_be_loaded_is_left_alone(package):
+    binding = give_binding(package)
+    assert load(package) == "binding"
+    binding.write_bytes(b"not a shared library")
+    assert load(package) == "ctypes"
