@@ -53,8 +53,11 @@ BINDING_SOURCE = os.path.join(CSRC, "fast_binding.cpp")
 
 
 def binding_path() -> str:
+    """Where the binding for this interpreter and this PyTorch lies: it fits no other."""
+    import sysconfig
+
     import torch
-    return os.path.join(PKG, f"_fast_binding-torch{torch.__version__.split('+')[0]}.so")
+    return os.path.join(PKG, f"_fast_binding-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _start_binding(force: bool):

@@ -63,3 +63,17 @@ def test_a_binding_that_cannot_be_loaded_is_left_alone(package):
     assert load(package) == "binding"
     binding.write_bytes(b"not a shared library")
     assert load(package) == "ctypes"
+
+
+def test_a_binding_belongs_to_one_interpreter_and_one_pytorch(monkeypatch):
+    import sysconfig
+
+    import torch
+
+    from gated_deltanet_decode_gb300 import build
+    here = build.binding_path()
+    monkeypatch.setattr(torch, "__version__", torch.__version__.split("+")[0] + "+cu999")
+    other = build.binding_path()
+    assert other != here
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so" if name == "EXT_SUFFIX" else None)
+    assert build.binding_path() not in (here, other)
