@@ -132,9 +132,9 @@ def _load_fast(L):
     """The C++ binding, told where the library's functions are; None without one that loads."""
     import importlib.machinery
     import importlib.util
-    path = _build.binding_path()
-    if not os.path.exists(path):
+    if not _build.binding_fresh():
         return None
+    path = _build.binding_path()
     try:
         loader = importlib.machinery.ExtensionFileLoader("_fast_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast_binding", loader, origin=path))

@@ -60,14 +60,23 @@ def binding_path() -> str:
     return os.path.join(PKG, f"_fast_binding-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
+def binding_fresh() -> bool:
+    """Whether the binding is there and as new as its sources, whose calls it makes by address."""
+    path = binding_path()
+    return os.path.exists(path) and os.path.getmtime(path) >= _binding_sources_time()
+
+
+def _binding_sources_time() -> float:
+    return max(os.path.getmtime(f) for f in (BINDING_SOURCE, os.path.join(ROOT, "include", "gdn_decode.h")))
+
+
 def _start_binding(force: bool):
     """The compiler's process for the binding, and where its output goes; None if it is up to date or cannot be made."""
     import sysconfig
 
     import torch
     path = binding_path()
-    newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, os.path.join(ROOT, "include", "gdn_decode.h")))
-    if not force and os.path.exists(path) and os.path.getmtime(path) >= newest:
+    if not force and binding_fresh():
         return None
     gxx, nvcc = shutil.which("g++"), _find_nvcc()  # the toolkit's headers lie beside nvcc
     if not gxx or not nvcc:

@@ -77,3 +77,10 @@ def test_a_binding_belongs_to_one_interpreter_and_one_pytorch(monkeypatch):
     assert other != here
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so" if name == "EXT_SUFFIX" else None)
     assert build.binding_path() not in (here, other)
+
+
+def test_a_binding_older_than_its_sources_is_not_used(package):
+    binding = give_binding(package)
+    assert load(package, without="g++") == "binding"
+    os.utime(binding, (1, 1))
+    assert load(package, without="g++") == "ctypes"
