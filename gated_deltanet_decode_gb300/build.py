@@ -49,6 +49,10 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _newer(path: str, t: float) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= t
+
+
 BINDING_SOURCE = os.path.join(CSRC, "fast_binding.cpp")
 
 
@@ -62,8 +66,12 @@ def binding_path() -> str:
 
 def binding_fresh() -> bool:
     """Whether the binding is there and as new as its sources, whose calls it makes by address."""
-    path = binding_path()
-    return os.path.exists(path) and os.path.getmtime(path) >= _binding_sources_time()
+    return _newer(binding_path(), _binding_sources_time())
+
+
+def _binding_failed() -> str:
+    """What the compiler said when the binding did not compile: it is asked again once the sources are newer."""
+    return os.path.join(BUILD_DIR, os.path.basename(binding_path()) + ".failed")
 
 
 def _binding_sources_time() -> float:
@@ -76,10 +84,10 @@ def _start_binding(force: bool):
 
     import torch
     path = binding_path()
-    if not force and binding_fresh():
+    if not force and (binding_fresh() or _newer(_binding_failed(), _binding_sources_time())):
         return None
     gxx, nvcc = shutil.which("g++"), _find_nvcc()  # the toolkit's headers lie beside nvcc
-    if not gxx or not nvcc:
+    if not gxx or not nvcc or not os.access(PKG, os.W_OK):
         return None
     base = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
@@ -99,6 +107,9 @@ def _end_binding(started) -> None:
     if proc.returncode == 0:
         os.replace(tmp, path)
     else:
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        with open(_binding_failed(), "wb") as f:
+            f.write(out)
         print("the C++ binding did not build; the package calls through ctypes\n" + out.decode(errors="replace")[-2000:],
               file=sys.stderr)
 

@@ -84,3 +84,19 @@ def test_a_binding_older_than_its_sources_is_not_used(package):
     assert load(package, without="g++") == "binding"
     os.utime(binding, (1, 1))
     assert load(package, without="g++") == "ctypes"
+
+
+def test_a_binding_that_does_not_compile_is_tried_once(package):
+    """The compiler is asked again only when a source has changed since."""
+    tools, log = package / "tools", package / "asked"
+    tools.mkdir()
+    (tools / "g++").write_text(f"#!/bin/sh\necho asked >> {log}\nexit 1\n")
+    (tools / "g++").chmod(0o755)
+    assert load(package, path=tools) == "ctypes"
+    assert load(package, path=tools) == "ctypes"
+    assert log.read_text().count("asked") == 1
+    source = package / PKG / "csrc" / "fast_binding.cpp"
+    later = os.path.getmtime(log) + 10
+    os.utime(source, (later, later))
+    assert load(package, path=tools) == "ctypes"
+    assert log.read_text().count("asked") == 2
