@@ -741,6 +741,16 @@ def _raw_stream(dev: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _on(dev: torch.device, call, *args):
+    """call(*args, dev's stream) with dev as the current device: a stream's handle need not name its device, as 0,
+    PyTorch's default stream, is the current device's."""
+    if torch.cuda.current_device() == dev.index:
+        _check(call(*args, _raw_stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(*args, _raw_stream(dev)))
+
+
 def _arg(t: Optional[torch.Tensor], n: int, dtype, dev: torch.device, what: str):
     """Device pointer of a contiguous tensor of n elements (or None)."""
     if t is None:
@@ -800,11 +810,11 @@ def attn_prologue(q, k, v, pool: KVPagePool, rope: Optional[torch.Tensor], table
         op = out.data_ptr()
     else:
         op = _arg(out, T * hq * d, pool.dtype, dev, "out")
-    _check(_lib.load().attn_prologue(
+    _on(dev, _lib.load().attn_prologue,
         qp, qs, kp, ks, vp, vs, pool._h, layer, _arg(rope, positions * rot, f32, dev, "rope"), positions, rot,
         1 if interleaved else 0, _arg(q_norm, d, f32, dev, "q_norm"), _arg(k_norm, d, f32, dev, "k_norm"), eps, tab,
         max_pages, _arg(seq_len, rows, i32, dev, "seq_len"), _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"),
-        op, hq, rows, T, pool._code, _raw_stream(dev)))
+        op, hq, rows, T, pool._code)
     return out
 
 
@@ -841,10 +851,10 @@ def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int 
         wp = workspace.data_ptr()
     else:
         wp, nbytes = _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size()
-    _check(L.paged_attention(
+    _on(dev, L.paged_attention,
         qp, qs, pool._h, layer, tab, max_pages, _arg(seq_len, rows, i32, dev, "seq_len"),
         _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"), scale,
-        op, hq, rows, T, wp, nbytes, pool._code, _raw_stream(dev)))
+        op, hq, rows, T, wp, nbytes, pool._code)
     return out
 
 
@@ -855,9 +865,9 @@ def kv_pages_reserve(table, refs, rows, tokens, page_size: int, status: Optional
     if status is None:
         status = torch.empty(n, dtype=i32, device=dev)
     pages = refs.numel()
-    _check(_lib.load().kv_pages_reserve(
+    _on(dev, _lib.load().kv_pages_reserve,
         tab, trows, max_pages, _arg(refs, pages, i32, dev, "refs"), pages, page_size, _arg(rows, n, i32, dev, "rows"),
-        _arg(tokens, n, i32, dev, "tokens"), n, _arg(status, n, i32, dev, "status"), _raw_stream(dev)))
+        _arg(tokens, n, i32, dev, "tokens"), n, _arg(status, n, i32, dev, "status"))
     return status
 
 
@@ -874,10 +884,10 @@ def kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size: int, move
     dev, n, i32 = table.device, src_rows.numel(), torch.int32
     tab, trows, max_pages = _table(table, dev)
     pages = refs.numel()
-    _check(_lib.load().kv_pages_fork(
+    _on(dev, _lib.load().kv_pages_fork,
         tab, trows, max_pages, _arg(seq_len, trows, i32, dev, "seq_len"), _arg(refs, pages, i32, dev, "refs"), pages,
         page_size, _arg(src_rows, n, i32, dev, "src_rows"), _arg(dst_rows, n, i32, dev, "dst_rows"), n,
-        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"), _raw_stream(dev)))
+        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"))
     return moves
 
 
@@ -892,9 +902,9 @@ def kv_pages_free(table, seq_len, refs, rows) -> None:
     dev, n, i32 = table.device, rows.numel(), torch.int32
     tab, trows, max_pages = _table(table, dev)
     pages = refs.numel()
-    _check(_lib.load().kv_pages_free(
+    _on(dev, _lib.load().kv_pages_free,
         tab, trows, max_pages, _arg(seq_len, trows, i32, dev, "seq_len"), _arg(refs, pages, i32, dev, "refs"), pages,
-        _arg(rows, n, i32, dev, "rows"), n, _raw_stream(dev)))
+        _arg(rows, n, i32, dev, "rows"), n)
 
 
 def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.Tensor] = None,
@@ -906,11 +916,11 @@ def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.
     tab, trows, max_pages = _table(table, dev)
     remap = torch.empty(n, dtype=i32, device=dev) if remap is None else remap
     refp = _arg(refs, n, i32, dev, "refs")
-    _check(_lib.load().kv_pages_compact(
+    _on(dev, _lib.load().kv_pages_compact,
         tab, trows, max_pages, refp, n,
         tab if table_out is None else _arg(table_out, trows * max_pages, i32, dev, "table_out"),
         refp if refs_out is None else _arg(refs_out, n, i32, dev, "refs_out"), _arg(remap, n, i32, dev, "remap"),
-        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"), _raw_stream(dev)))
+        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"))
     return remap
 
 
@@ -923,7 +933,7 @@ def kv_pages_copy(pool: KVPagePool, moves: KVPageMoves) -> None:
             return
     dev, n = pool.device, moves.src.numel()
     src, dst, count = moves._pointers(n, dev)
-    _check(_lib.load().kv_pages_copy(pool._h, src, dst, n, count, _raw_stream(dev)))
+    _on(dev, _lib.load().kv_pages_copy, pool._h, src, dst, n, count)
 
 
 __all__ += ["rope_inv_freq", "rope_table", "KVPagePool", "KVPageMoves", "attn_prologue",

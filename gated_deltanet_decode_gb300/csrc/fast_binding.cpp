@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -90,6 +91,10 @@ struct Table {
 
 Pool *pool_of(PyObject *o) { return static_cast<Pool *>(PyLong_AsVoidPtr(o)); }
 
+// A launch goes to the current device where the stream's handle does not name one (0, PyTorch's default stream).  Tensors
+// of another device are left to the package, which changes over for the call.
+bool current(int device) { return c10::cuda::current_device() == device; }
+
 void *stream_of(int device) { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 
 at::Tensor cuda_empty(at::IntArrayRef size, at::ScalarType type, int device)
@@ -107,7 +112,7 @@ PyObject *prologue(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tokens q(a[0], pool), k(a[1], pool), v(a[2], pool);
     const Table table(a[5]);
     const at::Tensor *rope = a[4] == Py_None ? nullptr : tensor(a[4]);
-    if (!q.ok || !k.ok || !v.ok || !table.ok || table.device != dev || k.tokens != q.tokens || v.tokens != q.tokens ||
+    if (!current(dev) || !q.ok || !k.ok || !v.ok || !table.ok || table.device != dev || k.tokens != q.tokens || v.tokens != q.tokens ||
         k.heads != pool.hkv || v.heads != pool.hkv ||
         (a[4] != Py_None && (!rope || rope->dim() != 2 || !plain(*rope, at::kFloat, dev))))
         Py_RETURN_NONE;
@@ -152,7 +157,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int dev = pool.device;
     const Tokens q(a[0], pool);
     const Table table(a[2]);
-    if (!q.ok || !table.ok || table.device != dev)
+    if (!current(dev) || !q.ok || !table.ok || table.device != dev)
         Py_RETURN_NONE;
     const Arg seq(a[3], table.rows, at::kInt, dev), cu(a[4], table.rows + 1, at::kInt, dev);
     const Arg given(a[7], q.tokens * q.heads * pool.d, pool.type, dev, true);
@@ -202,7 +207,7 @@ PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_RETURN_NONE;
     const Table table(a[0]);
     const at::Tensor *refs = tensor(a[2]), *src = tensor(a[3]);
-    if (!table.ok || !refs || !src || !plain(*refs, at::kInt, table.device) || !plain(*src, at::kInt, table.device))
+    if (!table.ok || !current(table.device) || !refs || !src || !plain(*refs, at::kInt, table.device) || !plain(*src, at::kInt, table.device))
         Py_RETURN_NONE;
     const int dev = table.device;
     const int64_t rows = src->numel();
@@ -228,7 +233,7 @@ PyObject *free_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_RETURN_NONE;
     const Table table(a[0]);
     const at::Tensor *refs = tensor(a[2]), *rows = tensor(a[3]);
-    if (!table.ok || !refs || !rows || !plain(*refs, at::kInt, table.device) || !plain(*rows, at::kInt, table.device))
+    if (!table.ok || !current(table.device) || !refs || !rows || !plain(*refs, at::kInt, table.device) || !plain(*rows, at::kInt, table.device))
         Py_RETURN_NONE;
     const Arg seq(a[1], table.rows, at::kInt, table.device);
     if (!seq.ok)
@@ -245,7 +250,7 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_RETURN_NONE;
     const Pool &pool = *pool_of(a[0]);
     const at::Tensor *src = tensor(a[1]);
-    if (!src || !plain(*src, at::kInt, pool.device))
+    if (!current(pool.device) || !src || !plain(*src, at::kInt, pool.device))
         Py_RETURN_NONE;
     const Arg dst(a[2], src->numel(), at::kInt, pool.device), count(a[3], 1, at::kInt, pool.device);
     if (!dst.ok || !count.ok)
