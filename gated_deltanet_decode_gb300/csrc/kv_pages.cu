@@ -15,6 +15,7 @@ constexpr int kPlanThreads = 1024; // one CTA plans a reservation or a fork
 constexpr int kRowThreads = 256;
 constexpr int kChunk = 1024;       // pages a CTA ranks in a compaction
 constexpr int kPer = kChunk / kRowThreads;
+constexpr int kLook = 8;           // entries a lane loads together when a fork's source is looked over
 
 // Exclusive sum of v over the CTA's threads (a multiple of 32, at most 1024);
 // `total` gets the whole sum.  `part` is 33 ints of shared memory.
@@ -162,7 +163,9 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageTables 
 }
 
 // Entry e of the row that fork i makes: full pages shared, entries past the
-// row's pages zeroed.
+// row's pages zeroed.  (The plan has looked at the source's pages; they are
+// looked at again only so that a source which the call itself makes, against
+// the contract, counts no page out of range.)
 __device__ __forceinline__ void fork_entry(const PageTables &t, const int32_t *src_rows, const int32_t *dst_rows, int i, int e)
 {
     const int s = src_rows[i], len = t.seq_len[s], full = len / t.page_size;
@@ -193,23 +196,55 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageTable
     __shared__ int owner[GDN_MAX_PAGE_ROWS]; // the entry that gets the free page of a rank
     __shared__ int part[33];
     wait_prior_grid();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int s = src_rows[i], d = dst_rows[i];
-        bool good = s >= 0 && s < t.table_rows && d >= 0 && d < t.table_rows && s != d;
-        int ask = 0;
-        if (good) {
-            const int len = t.seq_len[s];
-            good = len >= 0 && len <= (long long)t.max_pages * t.page_size && t.table[(size_t)d * t.max_pages] == 0;
-            if (good && len % t.page_size != 0) {
-                const int page = t.table[(size_t)s * t.max_pages + len / t.page_size];
-                good = page > 0 && page < t.num_pages;
-                ask = good;
+    // A fork is done whole or not at all, so all pages of its source are looked at before any is given out.  A warp takes up
+    // to 32 forks together, the rows and length of one a lane, then a source's entries at a time; a source that repeats is
+    // looked at once (a prompt sampled several times).  This takes 0.2 us for a row of 63 pages and 2.4 us for 192 forks of
+    // 48 rows of up to 375.
+    const int lane = threadIdx.x & 31, warps = kPlanThreads / 32, per = min(32, (n + warps - 1) / warps);
+    for (int i0 = (threadIdx.x >> 5) * per; i0 < n; i0 += warps * per) {
+        const int i = i0 + lane;
+        const bool mine = lane < per && i < n;
+        int s = -1, len = 0;
+        bool good = false;
+        if (mine) {
+            s = src_rows[i];
+            const int d = dst_rows[i];
+            if (s >= 0 && s < t.table_rows && d >= 0 && d < t.table_rows && s != d) {
+                len = t.seq_len[s];
+                good = len >= 0 && len <= (long long)t.max_pages * t.page_size && t.table[(size_t)d * t.max_pages] == 0;
             }
         }
-        if (!good)
-            report(t.err, GDN_DEVERR_BAD_PAGE);
-        status[i] = good ? 0 : GDN_DEVERR_BAD_PAGE;
-        start[i] = ask;
+        const int held = good ? (len + t.page_size - 1) / t.page_size : 0;
+        int row = -1;
+        bool whole = true; // row's pages are pages
+        for (int k = 0; k < per; ++k) {
+            const int h = __shfl_sync(0xffffffffu, held, k), from = __shfl_sync(0xffffffffu, s, k);
+            if (h == 0)
+                continue;
+            if (from != row) {
+                row = from;
+                const int32_t *const entries = t.table + (size_t)row * t.max_pages;
+                bool bad = false;
+                for (int j0 = lane; j0 < h; j0 += 32 * kLook) {
+                    int page[kLook]; // past the last entry: the last again
+#pragma unroll
+                    for (int j = 0; j < kLook; ++j)
+                        page[j] = entries[min(j0 + 32 * j, h - 1)];
+#pragma unroll
+                    for (int j = 0; j < kLook; ++j)
+                        bad |= page[j] <= 0 || page[j] >= t.num_pages;
+                }
+                whole = !__any_sync(0xffffffffu, bad);
+            }
+            if (lane == k)
+                good = whole;
+        }
+        if (mine) {
+            if (!good)
+                report(t.err, GDN_DEVERR_BAD_PAGE);
+            status[i] = good ? 0 : GDN_DEVERR_BAD_PAGE;
+            start[i] = good && len % t.page_size != 0;
+        }
     }
     __syncthreads();
     const int want = scan_array(start, n, part);
