@@ -65,23 +65,26 @@ class Decoder:
         return torch.tensor(values, dtype=torch.int32, device=self.device)
 
     def step(self, x, new):
-        """x [sum(new)][HIDDEN]: new[r] tokens of row r (0 for a row that rests).  Returns the last layer's output."""
+        """x [sum(new)][HIDDEN]: new[r] tokens of row r (0 for a row that rests).  Returns the last layer's output.  A row
+        that gets no pages (self.status) rests too: its length, pages and states stay, and its outputs mean nothing."""
         counts = self.ints(new)
         cu = torch.zeros(self.rows + 1, dtype=torch.int32, device=self.device)
         torch.cumsum(counts, 0, out=cu[1:])
         # the attention layers' rows: lengths with the new tokens, pages for them
         held = self.length + counts
         status = G.kv_pages_reserve(self.table, self.refs, self.all_rows, held, PAGE)
-        self.length.copy_(held)
-        busy = torch.where(counts > 0, self.slots, 0).to(torch.int32)
+        served = status == 0
+        self.length.copy_(torch.where(served, held, self.length))
+        seen = torch.where(served, held, 0)  # a padding row, where there are no pages for its tokens
+        busy = torch.where(served & (counts > 0), self.slots, 0).to(torch.int32)
         decode = all(n == 1 for n in new)
         for layer, w in enumerate(self.weights):
             if is_attention(layer):
                 y = (x @ w["qkv"]).view(len(x), HQ + 2 * HKV, D)
                 q, k, v = y[:, :HQ], y[:, HQ:HQ + HKV], y[:, HQ + HKV:]
-                q = G.attn_prologue(q, k, v, self.pool, self.rope, self.table, self.length, cu, layer=layer // 4,
+                q = G.attn_prologue(q, k, v, self.pool, self.rope, self.table, seen, cu, layer=layer // 4,
                                     q_norm=w["q_norm"], k_norm=w["k_norm"])
-                o = G.paged_attention(q, self.pool, self.table, self.length, cu, layer=layer // 4)
+                o = G.paged_attention(q, self.pool, self.table, seen, cu, layer=layer // 4)
             else:
                 conv, state = self.gdn[layer]
                 y, ab = x @ w["x"], x @ w["ab"]

@@ -1,0 +1,28 @@
+"""The example's hybrid decoder when the page pool runs out: the row that gets no pages rests, keeps what it had, and goes on
+later as if nothing had been asked."""
+import pytest
+import torch
+
+from test_gpu_hybrid_example import ex, tokens  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("second", [1, 4])  # a decode step, a chunk
+def test_a_row_without_pages_rests(gdn, ex, second):  # noqa: F811
+    a, b = ex.Decoder(2, 64, 5), ex.Decoder(2, 64, 40)  # four pages, and enough
+    x = tokens(ex, 48 + 16, 5)
+    for m in (a, b):
+        m.step(x, [48, 16])
+    y = tokens(ex, second, 6)
+    held = lambda: [a.table, a.length] + [p.tensor for layer in a.gdn.values() for p in layer]  # noqa: E731
+    before = [t.clone() for t in held()]
+    a.step(torch.cat([y, y]), [second, second])  # neither has room
+    assert a.status.tolist() == [gdn.GDN_DEVERR_NO_PAGES] * 2 and gdn.get_device_error() == gdn.GDN_DEVERR_NO_PAGES
+    assert all(torch.equal(x, y) for x, y in zip(held(), before))
+    for m in (a, b):
+        m.release([0])
+    for t in range(3):
+        z = tokens(ex, second, 20 + t)
+        assert torch.equal(a.step(z, [0, second]), b.step(z, [0, second]))
+    assert torch.equal(a.length, b.length) and gdn.get_device_error() == 0
