@@ -102,13 +102,16 @@ class Decoder:
         return x
 
     def fork(self, src, dst):
-        """Rows dst (empty) go on from where rows src are: slots and partial pages copied, full pages shared."""
+        """Rows dst (empty) go on from where rows src are: slots and partial pages copied, full pages shared.  Where the
+        status is not 0 nothing is done."""
         moves = G.KVPageMoves(len(src), device=self.device)
         G.kv_pages_fork(self.table, self.length, self.refs, self.ints(src), self.ints(dst), PAGE, moves)
         G.kv_pages_copy(self.pool, moves)
+        done = moves.status == 0
+        src, dst = self.slots[self.ints(src)[done]], self.slots[self.ints(dst)[done]]
         for conv, state in self.gdn.values():
             for pool in (conv, state):
-                pool.copy_slots(self.ints([r + 1 for r in src]), self.ints([r + 1 for r in dst]))
+                pool.copy_slots(src, dst)
         return moves.status
 
     def release(self, rows):

@@ -26,3 +26,17 @@ def test_a_row_without_pages_rests(gdn, ex, second):  # noqa: F811
         z = tokens(ex, second, 20 + t)
         assert torch.equal(a.step(z, [0, second]), b.step(z, [0, second]))
     assert torch.equal(a.length, b.length) and gdn.get_device_error() == 0
+
+
+def test_a_fork_without_pages_leaves_its_row_empty(gdn, ex):  # noqa: F811
+    a, b = ex.Decoder(3, 64, 4), ex.Decoder(3, 64, 4)  # three pages
+    x = tokens(ex, 40, 7)
+    for m in (a, b):
+        m.step(x, [40, 0, 0])
+    assert a.fork([0, 0], [1, 2]).tolist() == [gdn.GDN_DEVERR_NO_PAGES] * 2
+    assert gdn.get_device_error() == gdn.GDN_DEVERR_NO_PAGES
+    for m in (a, b):
+        m.release([0])
+    y = tokens(ex, 5, 8)
+    assert torch.equal(a.step(y, [0, 4, 1]), b.step(y, [0, 4, 1]))
+    assert gdn.get_device_error() == 0
