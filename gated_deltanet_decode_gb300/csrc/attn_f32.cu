@@ -18,11 +18,12 @@
 // 64 at 301 TFLOP/s (packed fp32 FMAs would take 81), and splitting operands
 // takes as many slots.  Decode streams at 4.1 to 4.4 TB/s (d = 256: 2.4).
 //
-// A weight of zero does not hide a NaN or an infinity, and infinity has no
-// tail.  So an item whose sums come out finite is done; otherwise a second pass
-// takes the elements of V that are not finite as zero, and the item's end adds
-// them to the rows that see them.  (Looking at every tile as it lands cost
-// decode up to 11 %.)
+// A weight of zero does not hide a NaN or an infinity, infinity has no tail,
+// and rounding to a head takes the largest finite values out of the range.  So
+// an item whose sums come out finite is done; otherwise a second pass takes the
+// elements of V that are not finite as zero, and the item's end adds them to
+// the rows that see them; it also splits with care for the range.  (Looking at
+// every tile as it lands cost decode up to 11 %.)
 #include "attn_plan.cuh"
 
 #include <atomic>
@@ -97,6 +98,15 @@ template <int N> struct Width {
     static constexpr int value = N;
 };
 __device__ __forceinline__ bool odd(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; } // not finite
+// The second pass's: a head that rounding up would take out of the range (from 3.402e38 on) is cut short instead.
+__device__ __forceinline__ void split_any(float x, uint32_t &hi, uint32_t &lo)
+{
+    split(x, hi, lo);
+    if (odd(hi)) {
+        hi = __float_as_uint(x) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi));
+    }
+}
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -114,8 +124,9 @@ __device__ __forceinline__ void copy16(float *dst, const float *src, bool there)
 // (g = lane / 4, c = lane % 4).  Fragments: A (row g, k c), (g + 8, c), (g, c +
 // 4), (g + 8, c + 4); B (k c, n g), (c + 4, g); D (g, 2c), (g, 2c + 1), (g + 8,
 // 2c), (g + 8, 2c + 1).  P V names key 2c as its k = c and key 2c + 1 as k = c +
-// 4, so the weights are an A fragment as they stand.
-template <int D, int NT>
+// 4, so the weights are an A fragment as they stand.  ANY: the operands may be
+// at the top of the range.
+template <int D, int NT, bool ANY>
 __device__ __forceinline__ void tile_step(const float *q, const float *k, const float *v, int see0, int see8, float c2,
                                           float (&o)[D / 8][4], float &m0, float &m8, float &l0, float &l8)
 {
@@ -145,15 +156,18 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
         for (int ks = 0; ks < 4; ++ks) {
             const float *qp = q + g * LD + 8 * (k0 + ks) + c;
             uint32_t ah[4], al[4];
-            split(qp[0], ah[0], al[0]);
-            split(qp[8 * LD], ah[1], al[1]);
-            split(qp[4], ah[2], al[2]);
-            split(qp[8 * LD + 4], ah[3], al[3]);
+            const float qv[4] = {qp[0], qp[8 * LD], qp[4], qp[8 * LD + 4]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ANY ? split_any(qv[e], ah[e], al[e]) : split(qv[e], ah[e], al[e]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float *kp = k + (8 * n + g) * LD + 8 * (k0 + ks) + c;
                 uint32_t h0, h1, t0, t1;
-                split2(kp[0], kp[4], h0, t0, h1, t1);
+                if constexpr (ANY)
+                    split_any(kp[0], h0, t0), split_any(kp[4], h1, t1);
+                else
+                    split2(kp[0], kp[4], h0, t0, h1, t1);
                 float(&d)[4] = t[n][ks % APART];
                 mma8(d, al, h0, h1);
                 mma8(d, ah, t0, t1);
@@ -206,7 +220,11 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             uint32_t h0, h1, t0, t1;
-            split2(vp[8 * n * LD + 8 * e], vp[8 * n * LD + 8 * e + LD], h0, t0, h1, t1);
+            const float v0 = vp[8 * n * LD + 8 * e], v1 = vp[8 * n * LD + 8 * e + LD];
+            if constexpr (ANY)
+                split_any(v0, h0, t0), split_any(v1, h1, t1);
+            else
+                split2(v0, v1, h0, t0, h1, t1);
             mma8(d, al[n], h0, h1);
             mma8(d, ah[n], t0, t1);
             mma8(d, ah[n], h0, h1);
@@ -310,10 +328,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         const int s0 = r0 < rows ? it.see + r0 / p.g : 0, s8 = r8 < rows ? it.see + r8 / p.g : 0; // keys the rows see
         float o[D / 8][4], m0, m8, l0, l8;
         // this warp's step on tile j, on keys kb .. of it
-        auto work = [&](int j, int stage, int kb, auto nt) {
+        auto work = [&](int j, int stage, int kb, auto nt, auto again) {
             const int key = (it.ja + j) * KT + kb;
             const float *const K = ring + stage * 2 * G::TILE + kb * LD;
-            tile_step<D, decltype(nt)::value>(Q + 16 * wr * LD, K, K + G::TILE, s0 - key, s8 - key, c2, o, m0, m8, l0, l8);
+            tile_step<D, decltype(nt)::value, decltype(again)::value != 0>(Q + 16 * wr * LD, K, K + G::TILE, s0 - key, s8 - key, c2, o, m0, m8, l0, l8);
         };
         auto pass = [&](auto second) { // true where every sum is finite
             constexpr bool again = decltype(second)::value;
@@ -344,7 +362,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
                     look(pages[0], j + A + 2), look(pages[1], j + A + 3);
                     const int mine = j + wk / SH;
                     if (16 * wr < rows && mine < n)
-                        work(mine, mine % SF, wk % SH * 8, Width<1>());
+                        work(mine, mine % SF, wk % SH * 8, Width<1>(), second);
                 }
             } else {
                 constexpr int S = G::STAGES, A = S - 1;
@@ -367,11 +385,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
                     if (16 * wr >= rows)
                         continue;
                     if (D == 256 || wr_n == 2)
-                        work(j, j % S, kb, Width<1>());
+                        work(j, j % S, kb, Width<1>(), second);
                     else if (D == 128 && wr_n == 4)
-                        work(j, j % S, kb, Width<2>());
+                        work(j, j % S, kb, Width<2>(), second);
                     else
-                        work(j, j % S, kb, Width<KT / 8>());
+                        work(j, j % S, kb, Width<KT / 8>(), second);
                 }
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");

@@ -49,3 +49,34 @@ def test_items_in_a_row_with_values_that_are_not_finite(gdn, dtype, hq, hkv, d):
     q, out = run(gdn, c, new, hq)
     check(out, *attention_ref(c, q, new, d ** -0.5), dtype)
     assert gdn.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 2, 64, 70), (8, 1, 128, 5), (4, 1, 128, 100), (2, 1, 256, 40)])
+def test_largest_finite_values_stay_with_the_tokens_that_see_them(gdn, dtype, hq, hkv, d, n):
+    """V holds the type's largest and lowest value where only the chunk's last tokens see it.  Those tokens are compared in
+    fp32; in bf16 a sum before its division may pass the range."""
+    c = Cache([130 + n], dtype, hkv, d, 16, seed=d + n)
+    top = torch.finfo(TYPES[dtype]).max
+    see = [n - 1, n - 3]  # the first tokens that see them
+    for x, t in enumerate(see):
+        page, slot = place(c, 0, 130 + t)
+        c.v[0, page, :, slot, 7 + x] = top if x else -top
+    q, out = run(gdn, c, [n], hq)
+    ref, mag = attention_ref(c, q, [n], d ** -0.5)
+    upto = n if dtype == "f32" else n - 3
+    check(out[:upto], ref[:upto], mag[:upto], dtype)
+    assert torch.isfinite(ref).all() and gdn.get_device_error() == 0
+
+
+def test_fp32_keys_at_the_top_of_the_range(gdn):
+    """A key's largest value against a query's 2^-120: a score like any other."""
+    c = Cache([300], "f32", 1, 64, 16, seed=3)
+    top = torch.finfo(torch.float32).max
+    q = torch.randn(4, 4, 64, generator=torch.Generator().manual_seed(2))
+    q[:, :, 9] = 2.0 ** -120
+    for key, x in ((17, top), (230, -top), (298, top)):
+        page, slot = place(c, 0, key)
+        c.k[0, page, 0, slot, 9] = x
+    q, out = run(gdn, c, [4], 4, q=q)
+    check(out, *attention_ref(c, q, [4], 0.125), "f32")
