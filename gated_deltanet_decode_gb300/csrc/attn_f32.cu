@@ -22,8 +22,9 @@
 // and rounding to a head takes the largest finite values out of the range.  So
 // an item whose sums come out finite is done; otherwise a second pass takes the
 // elements of V that are not finite as zero, and the item's end adds them to
-// the rows that see them; it also splits with care for the range.  (Looking at
-// every tile as it lands cost decode up to 11 %.)
+// the rows that see them; it also splits with care for the range, so that an
+// infinite score is one.  (Looking at every tile as it lands cost decode up to
+// 11 %.)
 #include "attn_plan.cuh"
 
 #include <atomic>
@@ -98,14 +99,18 @@ template <int N> struct Width {
     static constexpr int value = N;
 };
 __device__ __forceinline__ bool odd(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; } // not finite
-// The second pass's: a head that rounding up would take out of the range (from 3.402e38 on) is cut short instead.
-__device__ __forceinline__ void split_any(float x, uint32_t &hi, uint32_t &lo)
+// The second pass's: a head that rounding up would take out of the range (from 3.402e38 on) is cut short instead, and a
+// value that is not finite has no tail; `fine` is the head, or zero in place of such a value.
+__device__ __forceinline__ void split_any(float x, uint32_t &hi, uint32_t &lo, uint32_t &fine)
 {
     split(x, hi, lo);
     if (odd(hi)) {
         hi = __float_as_uint(x) & 0xffffe000u;
         lo = __float_as_uint(x - __uint_as_float(hi));
     }
+    fine = hi;
+    if (odd(__float_as_uint(x)))
+        hi = isnan(x) ? 0x7fffffffu : __float_as_uint(x), lo = fine = 0;
 }
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -125,7 +130,9 @@ __device__ __forceinline__ void copy16(float *dst, const float *src, bool there)
 // 4), (g + 8, c + 4); B (k c, n g), (c + 4, g); D (g, 2c), (g, 2c + 1), (g + 8,
 // 2c), (g + 8, 2c + 1).  P V names key 2c as its k = c and key 2c + 1 as k = c +
 // 4, so the weights are an A fragment as they stand.  ANY: the operands may be
-// at the top of the range.
+// at the top of the range, and Q and K beyond it; then the products with tails
+// take the other side's finite heads, as infinity times a tail of zero or of
+// the other sign would be NaN.
 template <int D, int NT, bool ANY>
 __device__ __forceinline__ void tile_step(const float *q, const float *k, const float *v, int see0, int see8, float c2,
                                           float (&o)[D / 8][4], float &m0, float &m8, float &l0, float &l8)
@@ -155,22 +162,25 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const float *qp = q + g * LD + 8 * (k0 + ks) + c;
-            uint32_t ah[4], al[4];
+            uint32_t ah[4], al[4], af[4];
             const float qv[4] = {qp[0], qp[8 * LD], qp[4], qp[8 * LD + 4]};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                ANY ? split_any(qv[e], ah[e], al[e]) : split(qv[e], ah[e], al[e]);
+                if constexpr (ANY)
+                    split_any(qv[e], ah[e], al[e], af[e]);
+                else
+                    split(qv[e], ah[e], al[e]), af[e] = ah[e];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float *kp = k + (8 * n + g) * LD + 8 * (k0 + ks) + c;
-                uint32_t h0, h1, t0, t1;
+                uint32_t h0, h1, t0, t1, fine0, fine1;
                 if constexpr (ANY)
-                    split_any(kp[0], h0, t0), split_any(kp[4], h1, t1);
+                    split_any(kp[0], h0, t0, fine0), split_any(kp[4], h1, t1, fine1);
                 else
-                    split2(kp[0], kp[4], h0, t0, h1, t1);
+                    split2(kp[0], kp[4], h0, t0, h1, t1), fine0 = h0, fine1 = h1;
                 float(&d)[4] = t[n][ks % APART];
-                mma8(d, al, h0, h1);
-                mma8(d, ah, t0, t1);
+                mma8(d, al, fine0, fine1);
+                mma8(d, af, t0, t1);
                 mma8(d, ah, h0, h1);
             }
         }
@@ -219,10 +229,10 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            uint32_t h0, h1, t0, t1;
+            uint32_t h0, h1, t0, t1, fine0, fine1;
             const float v0 = vp[8 * n * LD + 8 * e], v1 = vp[8 * n * LD + 8 * e + LD];
-            if constexpr (ANY)
-                split_any(v0, h0, t0), split_any(v1, h1, t1);
+            if constexpr (ANY) // V's values are finite here
+                split_any(v0, h0, t0, fine0), split_any(v1, h1, t1, fine1);
             else
                 split2(v0, v1, h0, t0, h1, t1);
             mma8(d, al[n], h0, h1);

@@ -80,3 +80,30 @@ def test_fp32_keys_at_the_top_of_the_range(gdn):
         c.k[0, page, 0, slot, 9] = x
     q, out = run(gdn, c, [4], 4, q=q)
     check(out, *attention_ref(c, q, [4], 0.125), "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 2, 64, 70), (8, 1, 128, 5), (4, 1, 128, 100), (2, 1, 256, 40)])
+def test_infinite_keys_drop_out_or_leave_nothing(gdn, dtype, hq, hkv, d, n):
+    """One infinite element of K gives a score of minus infinity, a weight of zero, or of plus infinity, no result, by the
+    query's sign; tokens that do not see the key are as they are without it."""
+    c = Cache([130 + n], dtype, hkv, d, 16, seed=d + n + 1)
+    for t, x in ((n - 2, float("inf")), (n // 2, -float("inf"))):
+        page, slot = place(c, 0, 130 + t)
+        c.k[0, page, hkv - 1, slot, 11] = x
+    q, out = run(gdn, c, [n], hq)
+    ref, mag = attention_ref(c, q, [n], d ** -0.5)
+    assert torch.isnan(ref).any() and torch.isfinite(ref[n // 2:]).all(-1).any()
+    check(out, ref, mag, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 50])
+def test_an_infinite_query_leaves_the_other_heads_and_tokens_alone(gdn, dtype, n):
+    c = Cache([3000], dtype, 2, 128, 16, seed=n)
+    q = torch.randn(n, 8, 128, generator=torch.Generator().manual_seed(7)).to(TYPES[dtype])
+    q[n // 2, 5, 3] = float("inf")
+    q, out = run(gdn, c, [n], 8, q=q)
+    ref, mag = attention_ref(c, q, [n], 128 ** -0.5)
+    assert torch.isnan(ref[n // 2, 5]).all() and torch.isnan(ref).sum() == 128
+    check(out, ref, mag, dtype)
