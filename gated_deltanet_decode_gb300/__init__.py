@@ -710,7 +710,8 @@ class KVPagePool:
 
 class KVPageMoves:
     """Pages to copy, as kv_pages_fork and kv_pages_compact list them on the device: src[j] -> dst[j] for j < count[0]
-    (zeros past it).  `n` is the capacity: the forks, or the pool's pages.  `status` is 0 for every fork that was done."""
+    (zeros past it, up to the call's forks or pages).  `n` is the capacity: the most forks of a call, or the pool's pages.
+    `status` is 0 for every fork of the last call that was done; a compaction uses its room."""
 
     def __init__(self, n: int, device=None):
         device = torch.device(device if device is not None else "cuda")
@@ -720,8 +721,11 @@ class KVPageMoves:
         self.status = torch.zeros(n, dtype=torch.int32, device=device)
 
     def _pointers(self, n: int, dev: torch.device):
-        i32 = torch.int32
-        return (_arg(self.src, n, i32, dev, "moves"), _arg(self.dst, n, i32, dev, "moves"),
+        """Device pointers of the lists, of at least n entries, and of the count."""
+        i32, room = torch.int32, min(self.src.numel(), self.dst.numel(), self.status.numel())
+        if room < n:
+            raise ValueError(f"moves has room for {room} entries, {n} are needed")
+        return (_arg(self.src, self.src.numel(), i32, dev, "moves"), _arg(self.dst, self.dst.numel(), i32, dev, "moves"),
                 _arg(self.count, 1, i32, dev, "moves"))
 
 
@@ -887,7 +891,7 @@ def kv_pages_fork(table, seq_len, refs, src_rows, dst_rows, page_size: int, move
     _on(dev, _lib.load().kv_pages_fork,
         tab, trows, max_pages, _arg(seq_len, trows, i32, dev, "seq_len"), _arg(refs, pages, i32, dev, "refs"), pages,
         page_size, _arg(src_rows, n, i32, dev, "src_rows"), _arg(dst_rows, n, i32, dev, "dst_rows"), n,
-        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"))
+        *moves._pointers(n, dev), _arg(moves.status, moves.status.numel(), i32, dev, "moves"))
     return moves
 
 
@@ -910,7 +914,7 @@ def kv_pages_free(table, seq_len, refs, rows) -> None:
 def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.Tensor] = None,
                      refs_out: Optional[torch.Tensor] = None, remap: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Renumber the pages in use to the lowest numbers, in place or into table_out and refs_out; the copies are listed
-    in `moves` (of as many entries as the pool has pages), then kv_pages_copy(pool, moves).  Returns remap: each page's
+    in `moves` (with room for the pool's pages), then kv_pages_copy(pool, moves).  Returns remap: each page's
     new number, 0 for a free page."""
     dev, i32, n = table.device, torch.int32, refs.numel()
     tab, trows, max_pages = _table(table, dev)
@@ -920,7 +924,7 @@ def kv_pages_compact(table, refs, moves: KVPageMoves, table_out: Optional[torch.
         tab, trows, max_pages, refp, n,
         tab if table_out is None else _arg(table_out, trows * max_pages, i32, dev, "table_out"),
         refp if refs_out is None else _arg(refs_out, n, i32, dev, "refs_out"), _arg(remap, n, i32, dev, "remap"),
-        *moves._pointers(n, dev), _arg(moves.status, n, i32, dev, "moves"))
+        *moves._pointers(n, dev), _arg(moves.status, moves.status.numel(), i32, dev, "moves"))
     return remap
 
 

@@ -39,18 +39,20 @@ bool plain(const at::Tensor &t, at::ScalarType type, int device)
     return t.scalar_type() == type && t.is_cuda() && t.get_device() == device && t.is_contiguous();
 }
 
-// A contiguous tensor of n elements, or with `none` also None (a null pointer).
+enum Takes { kExactly, kOrNone, kOrMore };
+
+// A contiguous tensor of n elements; also None (a null pointer), or more elements, where that is taken.
 struct Arg {
     const void *p = nullptr;
     bool ok = false;
-    Arg(PyObject *o, int64_t n, at::ScalarType type, int device, bool none = false)
+    Arg(PyObject *o, int64_t n, at::ScalarType type, int device, Takes takes = kExactly)
     {
-        if (none && o == Py_None) {
+        if (takes == kOrNone && o == Py_None) {
             ok = true;
             return;
         }
         const at::Tensor *t = tensor(o);
-        if (t && t->numel() == n && plain(*t, type, device))
+        if (t && (t->numel() == n || (takes == kOrMore && t->numel() > n)) && plain(*t, type, device))
             p = t->const_data_ptr(), ok = true;
     }
     template <typename T> T *as() const { return static_cast<T *>(const_cast<void *>(p)); }
@@ -117,7 +119,7 @@ PyObject *prologue(PyObject *, PyObject *const *a, Py_ssize_t n)
         (a[4] != Py_None && (!rope || rope->dim() != 2 || !plain(*rope, at::kFloat, dev))))
         Py_RETURN_NONE;
     const Arg seq(a[6], table.rows, at::kInt, dev), cu(a[7], table.rows + 1, at::kInt, dev);
-    const Arg qn(a[9], pool.d, at::kFloat, dev, true), kn(a[10], pool.d, at::kFloat, dev, true);
+    const Arg qn(a[9], pool.d, at::kFloat, dev, kOrNone), kn(a[10], pool.d, at::kFloat, dev, kOrNone);
     const long layer = PyLong_AsLong(a[8]);
     const double eps = PyFloat_AsDouble(a[11]);
     const int interleaved = PyObject_IsTrue(a[12]);
@@ -126,7 +128,7 @@ PyObject *prologue(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_RETURN_NONE;
     }
     const int64_t size[3] = {q.tokens, q.heads, pool.d};
-    const Arg given(a[13], q.tokens * q.heads * pool.d, pool.type, dev, true);
+    const Arg given(a[13], q.tokens * q.heads * pool.d, pool.type, dev, kOrNone);
     if (!seq.ok || !cu.ok || !qn.ok || !kn.ok || !given.ok)
         Py_RETURN_NONE;
     at::Tensor made;
@@ -160,7 +162,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (!current(dev) || !q.ok || !table.ok || table.device != dev)
         Py_RETURN_NONE;
     const Arg seq(a[3], table.rows, at::kInt, dev), cu(a[4], table.rows + 1, at::kInt, dev);
-    const Arg given(a[7], q.tokens * q.heads * pool.d, pool.type, dev, true);
+    const Arg given(a[7], q.tokens * q.heads * pool.d, pool.type, dev, kOrNone);
     const long layer = PyLong_AsLong(a[5]);
     const double scale = PyFloat_AsDouble(a[6]);
     if (PyErr_Occurred()) {
@@ -211,8 +213,8 @@ PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
         Py_RETURN_NONE;
     const int dev = table.device;
     const int64_t rows = src->numel();
-    const Arg seq(a[1], table.rows, at::kInt, dev), dst(a[4], rows, at::kInt, dev), ms(a[6], rows, at::kInt, dev),
-        md(a[7], rows, at::kInt, dev), mc(a[8], 1, at::kInt, dev), st(a[9], rows, at::kInt, dev);
+    const Arg seq(a[1], table.rows, at::kInt, dev), dst(a[4], rows, at::kInt, dev), ms(a[6], rows, at::kInt, dev, kOrMore),
+        md(a[7], rows, at::kInt, dev, kOrMore), mc(a[8], 1, at::kInt, dev), st(a[9], rows, at::kInt, dev, kOrMore);
     const long page = PyLong_AsLong(a[5]);
     if (PyErr_Occurred()) {
         PyErr_Clear();
