@@ -303,9 +303,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     };
     auto wait = [&](unsigned long long &b, uint32_t parity) { return wait_at(bar(b), parity); };
     auto stage_addr = [&](int s) { return sbase + G::RING + s * G::SBYTES; };
-    // place of the item's K and V tiles in the ring's order: one tile at a time K0 K1 V0 K2 V1 ... (a single tile's
-    // steps look one key tile ahead), in pairs K0 V0 K1 V1 ...
-    auto k_place = [](bool pair, int j) { return pair ? 2 * j : j == 0 ? 0 : 2 * j - 1; };
+    // place of the item's V tiles in the ring's order: one tile at a time K0 K1 V0 K2 V1 ... (a single tile's steps look
+    // one key tile ahead), in pairs K0 V0 K1 V1 ...
     auto v_place = [](bool pair, int j, int n) { return pair ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
 
     if (warp < 4) {
