@@ -30,14 +30,19 @@
 // first half's product runs while the second half's are computed.
 //
 // Bound.  Decode streams the cache: 64 rows of 0.5 to 8 k (477 MB) take 95 us,
-// two of 180 to 210 k (763 MB) 123 us, 92 to 93 % of a plain copy's rate once
+// two of 180 to 210 k (763 MB) 124 us, 92 % of a plain copy's rate once
 // started; a start costs 5 us, the end with the joining 5.  A 2,048-token chunk
-// over 16 k (16 heads of 128) takes 227 us, 1,250 TFLOP/s: the products are at
+// over 16 k (16 heads of 128) takes 230 us, 1,240 TFLOP/s: the products are at
 // work for 60 % of it.  A group's first weights come about 1,150 clocks after
 // its scores, the other group's products cover 1,024, and the next scores wait
 // for the weights' product, as tensor memory is full.  (Key tiles of 64 leave
 // room for a second score tile, but N = 64 products take as long as N = 128
 // ones: 301 us.)
+//
+// The weights are rounded to bf16 for their product with V (the row's sum takes
+// them as they are): A and B of a product have one type, and a head and a tail
+// of every weight would take a second product with V a step.  Results are off
+// by 0.0022 of their norm instead of the 0.0017 of their own rounding.
 //
 // O is rescaled only when a row's maximum has grown by over 2^8 since the
 // value in use (kLazy): weights then stay below 2^8 and sums in fp32 lose

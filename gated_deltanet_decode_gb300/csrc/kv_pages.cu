@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kRowThreads) free_kernel(const PageTables t, c
 // Page p < L (L pages in use) that is free is a hole: its rank among the holes
 // is p minus the live pages before it.  A live page p >= L has rank (live
 // pages before p) - (live pages before L); there are as many of these as
-// holes, and equal ranks are matched.  Bound: the latency of three small
+// holes, and equal ranks are matched.  Bound: the latency of four small
 // launches; a CTA ranks kChunk pages, and takes the sums of the chunks before
 // its own from the first launch.  59 k pages take about 25 us with the tables.
 

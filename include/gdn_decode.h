@@ -478,7 +478,8 @@ int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int lay
  * kv_pages_reserve: gives row list_rows[i] the pages for tokens[i] tokens in
  * all; a row that has them keeps what it has.
  * kv_pages_fork: makes row dst_rows[i], which must hold no page, a copy of
- * row src_rows[i] (sources may repeat; none is a destination): full pages are
+ * row src_rows[i] (sources may repeat; none is a destination), which must hold
+ * a page in [1, num_pages) for every page of its length: full pages are
  * shared, and a partial last page is replaced by a free one.  The pages to
  * copy, (move_src[j], move_dst[j]) for j < *move_count, are then for
  * kv_pages_copy; the lists hold n entries, zero past the count.  A row is not
