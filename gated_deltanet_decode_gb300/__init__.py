@@ -10,6 +10,8 @@ decode path runs in the library's CUDA kernels.  The names follow the C ABI
   gdn_decode_step                gated delta rule per row and value head
   gdn_layer_decode               both in one kernel
   gdn_commit                     twin-slot commit (swap read/write slots)
+  linear_attention_decode, linear_attention_prefill   recurrent layers with a
+                                 decay for each head and no delta rule
   attn_prologue, paged_attention, kv_pages_*   the attention layers beside the
                                  GDN layers, over a paged cache (KVPagePool)
 
@@ -131,6 +133,8 @@ class GDNStatePool:
             self.counters = torch.zeros((nbytes + 3) // 4, dtype=torch.int32, device=tensor.device)
             _check(L.gdn_pool_attach_inplace_counters(h, _ptr(self.counters, "in-place counters"),
                                                       self.counters.numel() * 4))
+        self._fast = _lib.fast()  # the C++ binding and the pool as it takes it
+        self._p = self._fast.make_state(h.value, hk, hv, dk, dv, tensor.device.index) if self._fast else None
 
     @property
     def handle(self):
@@ -151,10 +155,12 @@ class GDNStatePool:
         h = getattr(self, "_h", None)
         if h is not None and h.value:
             try:
+                if getattr(self, "_p", None):
+                    self._fast.drop_state(self._p)
                 _lib.load().gdn_state_pool_destroy(h)
             except Exception:
                 pass
-            self._h = None
+            self._h = self._p = None
 
 
 class ConvStatePool:
@@ -943,3 +949,101 @@ def kv_pages_copy(pool: KVPagePool, moves: KVPageMoves) -> None:
 __all__ += ["rope_inv_freq", "rope_table", "KVPagePool", "KVPageMoves", "attn_prologue",
             "paged_attention", "paged_attention_workspace_bytes", "kv_pages_reserve", "kv_pages_fork", "kv_pages_free",
             "kv_pages_compact", "kv_pages_copy", "GDN_DEVERR_BAD_PAGE", "GDN_DEVERR_NO_PAGES"]
+
+
+# ---- linear attention with a decay for each head -----------------------------
+
+
+def _linear_args(q, k, v, log_decay, pool: GDNStatePool, out):
+    """What both forms check alike: the C ABI's arguments up to the pool's handle, the output and its pointer."""
+    dev, dt = pool.tensor.device, q.dtype
+    _dtype_code(dt)
+    T = q.shape[0]
+
+    def rows(x, heads, d, what):
+        shape, st = x.shape, x.stride()
+        if len(shape) != 3 or shape[0] != T or shape[1] != heads or shape[2] != d:
+            raise ValueError(f"{what} must be [{T}][{heads}][{d}], got {tuple(shape)}")
+        if T and ((st[2] != 1 and d > 1) or (st[1] != d and heads > 1)):
+            raise ValueError(f"{what}: the heads of a token must be dense")
+        return _ptr(x, what, dt, dev, False), st[0] if T > 1 else heads * d
+
+    args = (*rows(q, pool.hk, pool.dk, "q"), *rows(k, pool.hk, pool.dk, "k"), *rows(v, pool.hv, pool.dv, "v"))
+    if log_decay.dim() not in (1, 2):
+        raise ValueError("log_decay must be [hv] or [tokens][hv]")
+    per_token = log_decay.dim() == 2
+    decay = _arg(log_decay, pool.hv * (T if per_token else 1), torch.float32, dev, "log_decay")
+    if out is None:
+        out = torch.empty((T, pool.hv, pool.dv), dtype=dt, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, T * pool.hv * pool.dv, dt, dev, "out")
+    return (*args, decay, 1 if per_token else 0, pool.handle), out, op
+
+
+def _slots(read_slot, write_slot, rows: int, dev, keep_in_place: bool):
+    i32 = torch.int32
+    return (_arg(read_slot, rows, i32, dev, "read_slot"),
+            None if keep_in_place else _arg(write_slot, rows, i32, dev, "write_slot"))
+
+
+def linear_attention_decode(q, k, v, log_decay, pool: GDNStatePool, read_slot, write_slot=None,
+                            scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                            keep_in_place: bool = False) -> torch.Tensor:
+    """Linear attention with a decay for each head, one token a row: S' = exp(g) S + v k^T, o = scale S' q.
+
+    q, k [rows][hk][dk], v [rows][hv][dv] (views of a packed projection are fine); log_decay g is fp32, [hv] or
+    [rows][hv], at most 0 (what is above counts as 0).  The state goes from read_slot to write_slot (twin) or stays in
+    read_slot (keep_in_place).  scale defaults to dk^-1/2.  Returns o, [rows][hv][dv]."""
+    if scale is None:
+        scale = pool.dk ** -0.5
+    if pool._p:
+        r = pool._fast.linear_decode(q, k, v, log_decay, pool._p, read_slot, None if keep_in_place else write_slot, scale,
+                                     out, keep_in_place)
+        if r is not None:
+            return _made(r)
+    args, out, op = _linear_args(q, k, v, log_decay, pool, out)
+    rows, dev = q.shape[0], pool.tensor.device
+    _on(dev, _lib.load().linear_attention_decode, *args, *_slots(read_slot, write_slot, rows, dev, keep_in_place), scale, op,
+        rows, int(bool(keep_in_place)), _dtype_code(q.dtype))
+    return out
+
+
+def linear_attention_prefill_workspace_bytes(pool: GDNStatePool, nseq: int, total_tokens: int, dtype=torch.bfloat16) -> int:
+    """Bytes of the device workspace of linear_attention_prefill."""
+    return int(_lib.load().linear_attention_prefill_workspace_bytes(pool.handle, int(nseq), int(total_tokens),
+                                                                    _dtype_code(dtype)))
+
+
+def linear_attention_prefill(q, k, v, log_decay, pool: GDNStatePool, cu_seqlens, read_slot, write_slot=None,
+                             scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                             keep_in_place: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """linear_attention_decode's rule over packed sequences: sequence r is tokens cu_seqlens[r] .. cu_seqlens[r+1] of q, k
+    [T][hk][dk], v [T][hv][dv] and, where it is a number a token, log_decay [T][hv].
+
+    workspace is a uint8 tensor of linear_attention_prefill_workspace_bytes (allocated here when none is given).  Tokens
+    of no sequence are left alone.  Returns [T][hv][dv]."""
+    if scale is None:
+        scale = pool.dk ** -0.5
+    if pool._p:
+        r = pool._fast.linear_prefill(q, k, v, log_decay, pool._p, cu_seqlens, read_slot,
+                                      None if keep_in_place else write_slot, scale, out, keep_in_place, workspace)
+        if r is not None:
+            return _made(r)
+    args, out, op = _linear_args(q, k, v, log_decay, pool, out)
+    T, nseq, dev, code = q.shape[0], cu_seqlens.numel() - 1, pool.tensor.device, _dtype_code(q.dtype)
+    if nseq < 0:
+        raise ValueError("cu_seqlens needs nseq + 1 entries")
+    L = _lib.load()
+    if workspace is None:
+        nbytes = L.linear_attention_prefill_workspace_bytes(pool.handle, nseq, T, code)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, nbytes = _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size()
+    _on(dev, L.linear_attention_prefill, *args, _arg(cu_seqlens, nseq + 1, torch.int32, dev, "cu_seqlens"),
+        *_slots(read_slot, write_slot, nseq, dev, keep_in_place), scale, op, nseq, T, int(bool(keep_in_place)), wp, nbytes, code)
+    return out
+
+
+__all__ += ["linear_attention_decode", "linear_attention_prefill", "linear_attention_prefill_workspace_bytes"]

@@ -53,6 +53,7 @@ EXPORTS = [
     "kv_page_pool_create", "kv_page_pool_wrap", "kv_page_pool_destroy", "kv_page_pool_k", "kv_page_pool_v",
     "kv_page_pool_num_pages", "rope_table", "attn_prologue", "paged_attention_workspace_bytes", "paged_attention",
     "kv_pages_reserve", "kv_pages_fork", "kv_pages_free", "kv_pages_compact", "kv_pages_copy",
+    "linear_attention_decode", "linear_attention_prefill_workspace_bytes", "linear_attention_prefill",
 ]
 
 
@@ -121,6 +122,10 @@ _SIGS = {
     "kv_pages_free": (_I, [_P, _I, _I, _P, _P, _I, _P, _I, _P]),
     "kv_pages_compact": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "kv_pages_copy": (_I, [_P, _P, _P, _I, _P, _P]),
+    "linear_attention_decode": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _P, _P, _P, ctypes.c_float, _P, _I, _I, _I, _P]),
+    "linear_attention_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
+    "linear_attention_prefill": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _P, _P, _P, _P, ctypes.c_float, _P, _I, _I, _I, _P,
+                                      ctypes.c_size_t, _I, _P]),
 }
 
 _lock = threading.Lock()
@@ -144,7 +149,8 @@ def _load_fast(L):
         return None
     module.bind(*(ctypes.cast(getattr(L, f), _P).value for f in (
         "attn_prologue", "paged_attention_workspace_bytes", "paged_attention", "kv_pages_fork", "kv_pages_free",
-        "kv_pages_copy")))
+        "kv_pages_copy", "linear_attention_decode", "linear_attention_prefill_workspace_bytes",
+        "linear_attention_prefill")))
     return module
 
 

@@ -1,4 +1,4 @@
-// The Python binding's calls of the attention layers, in C++: the same checks
+// The Python binding's calls of the attention and linear attention layers, in C++: the same checks
 // and the same C ABI as the functions of the package, without a Python call for
 // every property of every tensor.  A decode step makes these calls per layer,
 // and each took 10 to 12 us of host time, as much as its kernels on the GPU.
@@ -25,11 +25,20 @@ decltype(&paged_attention) c_attention;
 decltype(&kv_pages_fork) c_fork;
 decltype(&kv_pages_free) c_free;
 decltype(&kv_pages_copy) c_copy;
+decltype(&linear_attention_decode) c_linear_decode;
+decltype(&linear_attention_prefill_workspace_bytes) c_linear_workspace;
+decltype(&linear_attention_prefill) c_linear_prefill;
 
 struct Pool {
     kv_page_pool *handle;
     int hkv, d, code, device;
     at::ScalarType type;
+};
+
+// a GDN state pool
+struct State {
+    gdn_pool *handle;
+    int hk, hv, dk, dv, device;
 };
 
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -63,15 +72,15 @@ struct Tokens {
     const void *p = nullptr;
     int64_t tokens = 0, heads = 0, stride = 0;
     bool ok = false;
-    Tokens(PyObject *o, const Pool &pool)
+    Tokens(PyObject *o, const Pool &pool) : Tokens(tensor(o), pool.d, pool.type, pool.device) {}
+    Tokens(const at::Tensor *t, int d, at::ScalarType type, int device)
     {
-        const at::Tensor *t = tensor(o);
-        if (!t || t->dim() != 3 || t->scalar_type() != pool.type || !t->is_cuda() || t->get_device() != pool.device)
+        if (!t || t->dim() != 3 || t->scalar_type() != type || !t->is_cuda() || t->get_device() != device)
             return;
         const auto size = t->sizes(), step = t->strides();
         tokens = size[0], heads = size[1];
-        stride = tokens > 1 ? step[0] : heads * pool.d;
-        ok = size[2] == pool.d && step[2] == 1 && (step[1] == pool.d || heads == 1);
+        stride = tokens > 1 ? step[0] : heads * d;
+        ok = size[2] == d && step[2] == 1 && (step[1] == d || heads == 1);
         p = t->const_data_ptr();
     }
 };
@@ -261,6 +270,139 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
                                   count.as<int32_t>(), stream_of(pool.device)));
 }
 
+// What the two linear attention calls have alike: q k v log_decay pool .. scale out in_place
+struct Linear {
+    at::ScalarType type;
+    Tokens q, k, v;
+    const float *decay = nullptr;
+    int per_token = 0, in_place = 0, code = 0;
+    double scale = 0;
+    void *out = nullptr;
+    at::Tensor made;
+    bool ok = false;
+    Linear(PyObject *const *a, const State &s, PyObject *scale_, PyObject *out_, PyObject *in_place_)
+        : type(tensor(a[0]) ? tensor(a[0])->scalar_type() : at::kInt), q(tensor(a[0]), s.dk, type, s.device),
+          k(tensor(a[1]), s.dk, type, s.device), v(tensor(a[2]), s.dv, type, s.device)
+    {
+        if ((type != at::kFloat && type != at::kBFloat16) || !current(s.device) || !q.ok || !k.ok || !v.ok || q.heads != s.hk ||
+            k.heads != s.hk || v.heads != s.hv || k.tokens != q.tokens || v.tokens != q.tokens)
+            return;
+        code = type == at::kBFloat16 ? GDN_BF16 : GDN_F32;
+        const at::Tensor *g = tensor(a[3]);
+        if (!g || (g->dim() != 1 && g->dim() != 2) || !plain(*g, at::kFloat, s.device) ||
+            g->numel() != (g->dim() == 2 ? q.tokens * s.hv : s.hv))
+            return;
+        per_token = g->dim() == 2;
+        decay = g->const_data_ptr<float>();
+        scale = PyFloat_AsDouble(scale_);
+        in_place = PyObject_IsTrue(in_place_);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return;
+        }
+        const Arg given(out_, q.tokens * s.hv * s.dv, type, s.device, kOrNone);
+        if (!given.ok)
+            return;
+        out = given.as<void>();
+        if (out_ == Py_None) {
+            const int64_t size[3] = {q.tokens, s.hv, s.dv};
+            made = cuda_empty(size, type, s.device);
+            out = made.mutable_data_ptr();
+        }
+        ok = true;
+    }
+    PyObject *result(int rc, PyObject *out_)
+    {
+        if (rc != GDN_OK)
+            return PyLong_FromLong(rc);
+        if (out_ == Py_None)
+            return THPVariable_Wrap(std::move(made));
+        Py_INCREF(out_);
+        return out_;
+    }
+};
+
+// q k v log_decay pool read_slot write_slot scale out in_place
+PyObject *linear_decode(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 10)
+        Py_RETURN_NONE;
+    const State &s = *static_cast<State *>(PyLong_AsVoidPtr(a[4]));
+    Linear x(a, s, a[7], a[8], a[9]);
+    if (!x.ok)
+        Py_RETURN_NONE;
+    const Arg read(a[5], x.q.tokens, at::kInt, s.device), write(a[6], x.q.tokens, at::kInt, s.device, kOrNone);
+    if (!read.ok || !write.ok)
+        Py_RETURN_NONE;
+    return x.result(c_linear_decode(x.q.p, x.q.stride, x.k.p, x.k.stride, x.v.p, x.v.stride, x.decay, x.per_token, s.handle,
+                                    read.as<int32_t>(), write.as<int32_t>(), (float)x.scale, x.out, (int)x.q.tokens, x.in_place,
+                                    x.code, stream_of(s.device)),
+                    a[8]);
+}
+
+// q k v log_decay pool cu_seqlens read_slot write_slot scale out in_place workspace
+PyObject *linear_prefill(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 12)
+        Py_RETURN_NONE;
+    const State &s = *static_cast<State *>(PyLong_AsVoidPtr(a[4]));
+    const at::Tensor *cu = tensor(a[5]);
+    if (!cu || !plain(*cu, at::kInt, s.device) || cu->numel() < 1)
+        Py_RETURN_NONE;
+    Linear x(a, s, a[8], a[9], a[10]);
+    const int64_t nseq = cu->numel() - 1;
+    const Arg read(a[6], nseq, at::kInt, s.device), write(a[7], nseq, at::kInt, s.device, kOrNone);
+    if (!x.ok || !read.ok || !write.ok)
+        Py_RETURN_NONE;
+    at::Tensor room;
+    void *work = nullptr;
+    size_t bytes = 0;
+    if (a[11] == Py_None) {
+        bytes = c_linear_workspace(s.handle, (int)nseq, (int)x.q.tokens, x.code);
+        if (bytes) {
+            const int64_t length = (int64_t)bytes;
+            room = cuda_empty(at::IntArrayRef(&length, 1), at::kByte, s.device);
+            work = room.mutable_data_ptr();
+        }
+    } else {
+        const at::Tensor *w = tensor(a[11]);
+        if (!w || !plain(*w, w->scalar_type(), s.device))
+            Py_RETURN_NONE;
+        work = w->mutable_data_ptr();
+        bytes = w->nbytes();
+    }
+    return x.result(c_linear_prefill(x.q.p, x.q.stride, x.k.p, x.k.stride, x.v.p, x.v.stride, x.decay, x.per_token, s.handle,
+                                     cu->const_data_ptr<int32_t>(), read.as<int32_t>(), write.as<int32_t>(), (float)x.scale, x.out,
+                                     (int)nseq, (int)x.q.tokens, x.in_place, work, bytes, x.code, stream_of(s.device)),
+                    a[9]);
+}
+
+// handle hk hv dk dv device -> the state pool as the calls above take it
+PyObject *make_state(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 6)
+        Py_RETURN_NONE;
+    State *p = new (std::nothrow) State;
+    if (!p)
+        return PyErr_NoMemory();
+    p->handle = static_cast<gdn_pool *>(PyLong_AsVoidPtr(a[0]));
+    int *const to[] = {&p->hk, &p->hv, &p->dk, &p->dv, &p->device};
+    for (int i = 0; i < 5; ++i)
+        *to[i] = (int)PyLong_AsLong(a[1 + i]);
+    if (PyErr_Occurred()) {
+        delete p;
+        return nullptr;
+    }
+    return PyLong_FromVoidPtr(p);
+}
+
+PyObject *drop_state(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n == 1)
+        delete static_cast<State *>(PyLong_AsVoidPtr(a[0]));
+    Py_RETURN_NONE;
+}
+
 // handle hkv d dtype_code device -> the pool as the calls above take it
 PyObject *make_pool(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -292,14 +434,17 @@ PyObject *drop_pool(PyObject *, PyObject *const *a, Py_ssize_t n)
 // the addresses of the C ABI's functions, in the order of the variables above
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    void **to[] = {reinterpret_cast<void **>(&c_prologue),  reinterpret_cast<void **>(&c_workspace),
-                   reinterpret_cast<void **>(&c_attention), reinterpret_cast<void **>(&c_fork),
-                   reinterpret_cast<void **>(&c_free),      reinterpret_cast<void **>(&c_copy)};
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "six addresses are needed");
+    void **to[] = {reinterpret_cast<void **>(&c_prologue),      reinterpret_cast<void **>(&c_workspace),
+                   reinterpret_cast<void **>(&c_attention),     reinterpret_cast<void **>(&c_fork),
+                   reinterpret_cast<void **>(&c_free),          reinterpret_cast<void **>(&c_copy),
+                   reinterpret_cast<void **>(&c_linear_decode), reinterpret_cast<void **>(&c_linear_workspace),
+                   reinterpret_cast<void **>(&c_linear_prefill)};
+    constexpr int count = sizeof(to) / sizeof(*to);
+    if (n != count) {
+        PyErr_Format(PyExc_TypeError, "%d addresses are needed", count);
         return nullptr;
     }
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < count; ++i)
         *to[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred())
         return nullptr;
@@ -323,6 +468,8 @@ PyMethodDef methods[] = {METHOD("bind", bind),           METHOD("make_pool", mak
                          METHOD("drop_pool", drop_pool), METHOD("attn_prologue", prologue),
                          METHOD("paged_attention", attention), METHOD("kv_pages_fork", fork_rows),
                          METHOD("kv_pages_free", free_rows),   METHOD("kv_pages_copy", copy_pages),
+                         METHOD("make_state", make_state),     METHOD("drop_state", drop_state),
+                         METHOD("linear_decode", linear_decode), METHOD("linear_prefill", linear_prefill),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -126,6 +126,25 @@ struct ConvPrefillArgs {
     int *err;
 };
 
+// Linear attention with a decay for each head: one token a row, or (with
+// cu_seqlens) packed sequences.
+struct LinearArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride; // elements a token
+    const float *log_decay;
+    long long decay_stride;                 // elements a token: hv, or 0 (a decay a head)
+    float *pool;
+    int num_slots;
+    const int32_t *cu_seqlens, *read_slot;
+    const int32_t *write_slot;              // NULL: in place
+    float scale;
+    void *out;
+    int rows, total_tokens, hk, hv, dk, dv; // rows: of the batch, or sequences
+    int most;                               // tokens of the longest sequence that the serial kernel takes
+    int *err;
+    void *work;                             // the chunked kernels'
+};
+
 // One layer of a page pool, for a kernel.
 struct PageView {
     void *k, *v; // the layer's [num_pages][hkv][page_size][d]
@@ -186,6 +205,11 @@ cudaError_t launch_gdn_prefill_chunked(const PrefillArgs &a, int dtype, cudaStre
 cudaError_t launch_gdn_prefill_chunked_tc(const PrefillArgs &a, cudaStream_t s);
 // Bytes of the workspace the bf16 chunked prefill needs (0 for no sequence).
 size_t prefill_chunked_workspace_bytes(int nseq, int total_tokens, int hv);
+
+// Linear attention: one token a row, and packed sequences token after token
+// (those of up to a.most tokens).
+cudaError_t launch_linear_decode(const LinearArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_linear_serial(const LinearArgs &a, int dtype, cudaStream_t s);
 
 // Attention layers over a page pool.
 cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table,

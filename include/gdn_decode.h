@@ -384,6 +384,40 @@ int gdn_layer_decode_noalloc(const void *x, conv_pool *cp, const void *w, const 
  * device ("mstar PR #1139", "What changed": commit swaps them). */
 int gdn_commit(int32_t *read_slot, int32_t *write_slot, int rows, void *stream);
 
+/* ---- linear attention with a decay for each head ------------------------ *
+ * The recurrent layers of a hybrid decoder that keep no delta rule, over the
+ * same state pools, slots and twin slots:
+ *   S' = exp(g) S + v k^T,   o = scale S' q         per (row, value head)
+ * with S [dv][dk] fp32 and value head h on qk head h / (hv / hk).  The pages
+ * describe the gated delta rule only; the slots' handling is theirs (padding
+ * rows, twin and in place, bad rows), the formula and kernels are not.
+ *   q, k [T][hk][dk], v [T][hv][dv]: token strides in elements (a token's
+ *   heads are dense), addresses and strides multiples of 16 bytes
+ *   log_decay g, fp32: [hv] (the same for every token), or with
+ *   decay_per_token [T][hv]; a value above 0 counts as 0, -inf forgets all
+ *   out [T][hv][dv], dense, 16-byte aligned
+ * All of it is device memory.  Arithmetic is fp32, rounded once into out;
+ * scale must be finite.
+ *
+ * linear_attention_decode: one token a row, T = rows.
+ *
+ * linear_attention_prefill: sequence r is tokens cu_seqlens[r] ..
+ * cu_seqlens[r+1]; its state starts from read_slot[r] and ends in
+ * write_slot[r] (twin) or read_slot[r] (in place).  An empty twin sequence
+ * moves its state unchanged.  Tokens of no sequence are left alone; a sequence
+ * whose range is outside [0, total_tokens] is a bad row.  Bad and padding
+ * sequences' outputs are zero.  Slots of one call must not overlap. */
+int linear_attention_decode(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const float *log_decay, int decay_per_token, gdn_pool *pool,
+                            const int32_t *read_slot, const int32_t *write_slot, float scale, void *out, int rows,
+                            int keep_in_place, int dtype, void *stream);
+size_t linear_attention_prefill_workspace_bytes(const gdn_pool *pool, int nseq, int total_tokens, int dtype);
+int linear_attention_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, const float *log_decay, int decay_per_token, gdn_pool *pool,
+                             const int32_t *cu_seqlens, const int32_t *read_slot, const int32_t *write_slot, float scale,
+                             void *out, int nseq, int total_tokens, int keep_in_place, void *workspace,
+                             size_t workspace_bytes, int dtype, void *stream);
+
 /* ---- attention layers over a paged cache -------------------------------- *
  * The layers of a hybrid decoder that are not GDN layers attend over a cache
  * of keys and values.  The pages name their work ("mstar PR #1139", "What
