@@ -868,6 +868,65 @@ def paged_attention(q, pool: KVPagePool, table, seq_len, cu_seqlens, layer: int 
     return out
 
 
+def kv_pages_shared(table, seq_len, cu_seqlens, bounds, page_size: int, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """What the rows of each group share, for paged_attention_shared: group g is rows bounds[g] .. bounds[g+1].  Returns
+    [rows][2] int32: the group's first live row, and the leading pages that all live rows of the group have alike, before
+    their new tokens."""
+    f = _lib.fast()
+    if f:
+        r = f.kv_pages_shared(table, seq_len, cu_seqlens, bounds, page_size, out)
+        if r is not None:
+            return _made(r)
+    dev, i32 = table.device, torch.int32
+    tab, rows, max_pages = _table(table, dev)
+    if out is None:
+        out = torch.empty((rows, 2), dtype=i32, device=dev)
+    _on(dev, _lib.load().kv_pages_shared,
+        tab, rows, max_pages, _arg(seq_len, rows, i32, dev, "seq_len"), _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"),
+        _arg(bounds, bounds.numel(), i32, dev, "bounds"), bounds.numel() - 1, page_size, _arg(out, 2 * rows, i32, dev, "out"))
+    return out
+
+
+def paged_attention_shared_workspace_bytes(pool: KVPagePool, hq: int, rows: int, total_tokens: int) -> int:
+    """Bytes of the device workspace of paged_attention_shared."""
+    return int(_lib.load().paged_attention_shared_workspace_bytes(pool._h, int(hq), int(rows), int(total_tokens)))
+
+
+def paged_attention_shared(q, pool: KVPagePool, table, seq_len, cu_seqlens, bounds, prefix, layer: int = 0,
+                           scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention with the pages that a group's rows share read once for all of them, for rows that were forked.
+
+    bounds [groups + 1] and prefix [rows][2] are kv_pages_shared's (which a step calls once, for all of its layers)."""
+    if scale is None:
+        scale = pool.d ** -0.5
+    if pool._p:
+        r = pool._fast.paged_attention_shared(q, pool._p, table, seq_len, cu_seqlens, layer, scale, out, workspace, bounds, prefix)
+        if r is not None:
+            return _made(r)
+    dev, d, i32 = pool.device, pool.d, torch.int32
+    T, hq = q.shape[:2]
+    tab, rows, max_pages = _table(table, dev)
+    qp, qs = _token_rows(q, T, hq, pool, "q")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=pool.dtype, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, T * hq * d, pool.dtype, dev, "out")
+    L = _lib.load()
+    if workspace is None:
+        nbytes = L.paged_attention_shared_workspace_bytes(pool._h, hq, rows, T)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, nbytes = _ptr(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size()
+    _on(dev, L.paged_attention_shared,
+        qp, qs, pool._h, layer, tab, max_pages, _arg(seq_len, rows, i32, dev, "seq_len"),
+        _arg(cu_seqlens, rows + 1, i32, dev, "cu_seqlens"), _arg(bounds, bounds.numel(), i32, dev, "bounds"), bounds.numel() - 1,
+        _arg(prefix, 2 * rows, i32, dev, "prefix"), scale, op, hq, rows, T, wp, nbytes, pool._code)
+    return out
+
+
 def kv_pages_reserve(table, refs, rows, tokens, page_size: int, status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Give row rows[i] of the table the pages for tokens[i] tokens in all.  Returns status (0 where done)."""
     dev, n, i32 = table.device, rows.numel(), torch.int32
@@ -948,7 +1007,8 @@ def kv_pages_copy(pool: KVPagePool, moves: KVPageMoves) -> None:
 
 __all__ += ["rope_inv_freq", "rope_table", "KVPagePool", "KVPageMoves", "attn_prologue",
             "paged_attention", "paged_attention_workspace_bytes", "kv_pages_reserve", "kv_pages_fork", "kv_pages_free",
-            "kv_pages_compact", "kv_pages_copy", "GDN_DEVERR_BAD_PAGE", "GDN_DEVERR_NO_PAGES"]
+            "kv_pages_compact", "kv_pages_copy", "kv_pages_shared", "paged_attention_shared",
+            "paged_attention_shared_workspace_bytes", "GDN_DEVERR_BAD_PAGE", "GDN_DEVERR_NO_PAGES"]
 
 
 # ---- linear attention with a decay for each head -----------------------------

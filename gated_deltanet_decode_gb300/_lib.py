@@ -54,6 +54,7 @@ EXPORTS = [
     "kv_page_pool_num_pages", "rope_table", "attn_prologue", "paged_attention_workspace_bytes", "paged_attention",
     "kv_pages_reserve", "kv_pages_fork", "kv_pages_free", "kv_pages_compact", "kv_pages_copy",
     "linear_attention_decode", "linear_attention_prefill_workspace_bytes", "linear_attention_prefill",
+    "kv_pages_shared", "paged_attention_shared_workspace_bytes", "paged_attention_shared",
 ]
 
 
@@ -126,6 +127,10 @@ _SIGS = {
     "linear_attention_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
     "linear_attention_prefill": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _P, _P, _P, _P, ctypes.c_float, _P, _I, _I, _I, _P,
                                       ctypes.c_size_t, _I, _P]),
+    "kv_pages_shared": (_I, [_P, _I, _I, _P, _P, _P, _I, _I, _P, _P]),
+    "paged_attention_shared_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
+    "paged_attention_shared": (_I, [_P, _L, _P, _I, _P, _I, _P, _P, _P, _I, _P, ctypes.c_float, _P, _I, _I, _I, _P,
+                                    ctypes.c_size_t, _I, _P]),
 }
 
 _lock = threading.Lock()
@@ -150,7 +155,7 @@ def _load_fast(L):
     module.bind(*(ctypes.cast(getattr(L, f), _P).value for f in (
         "attn_prologue", "paged_attention_workspace_bytes", "paged_attention", "kv_pages_fork", "kv_pages_free",
         "kv_pages_copy", "linear_attention_decode", "linear_attention_prefill_workspace_bytes",
-        "linear_attention_prefill")))
+        "linear_attention_prefill", "kv_pages_shared", "paged_attention_shared_workspace_bytes", "paged_attention_shared")))
     return module
 
 

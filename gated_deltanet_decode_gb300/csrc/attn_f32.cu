@@ -29,6 +29,7 @@
 #include "attn_plan.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_ptx.cuh"
 
@@ -71,10 +72,10 @@ template <int D> struct Cost32 {
     }
 };
 
-struct Ctrl32 {
+template <typename V> struct Ctrl32 {
     long long scan[kThreads / 32];
-    Found found;
-    Item item;
+    FoundOf<V> found;
+    typename V::ItemT item;
     int more, broken, dirty;
     float2 ml[8 * 16]; // (m, l) by (share, row): 128 pairs in every form
 };
@@ -245,12 +246,16 @@ __device__ __forceinline__ void tile_step(const float *q, const float *k, const 
     }
 }
 
-template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(const WorkArgs p)
+template <int D, bool SH>
+__global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(const typename Kind<SH>::Args p)
 {
     typedef Geo32<D> G;
+    typedef typename std::conditional<SH, Shared, Plain>::type View;
+    typedef typename Kind<SH>::ItemT ItemT;
+    typedef Walk<Cost32<D>, View, typename Kind<SH>::Args> WalkT;
     constexpr int KT = G::KT, LD = G::LD;
     extern __shared__ __align__(16) float sm[];
-    __shared__ Ctrl32 ctl;
+    __shared__ Ctrl32<View> ctl;
     float *const Q = sm;
     const AttentionArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -258,13 +263,13 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
     const float c2 = a.scale * 1.44269504088896341f;
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Run run = plan_run<kThreads, KT, Cost32<D>>(p, p.tq, ctl.scan, ctl.found);
-    zero_dead<float, D, kThreads>(p, tid);
-    Walk<Cost32<D>> walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
+    const RunOf<View> run = plan_run<kThreads, KT, Cost32<D>, View>(p, p.tq, ctl.scan, ctl.found);
+    zero_dead<float, D, kThreads, View>(p, tid);
+    WalkT walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
     for (;;) {
         __syncthreads();
         if (warp == 0) {
-            Item next;
+            ItemT next;
             const bool more = walk.next(next);
             if (lane == 0) {
                 ctl.item = next;
@@ -274,9 +279,11 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         __syncthreads();
         if (!ctl.more)
             break;
-        const Item it = ctl.item;
-        const int32_t *const table = a.c.table + (size_t)it.row * a.c.max_pages;
-        const int kvh = it.head / p.groups, rows = it.ntok * p.g, end = it.see + it.ntok - 1;
+        const ItemT it = ctl.item;
+        const int32_t *const table = item_table(a.c, it);
+        const int step = see_step(it);
+        const bool partial = it.part != -1;
+        const int kvh = it.head / p.groups, rows = it.ntok * p.g, end = it.see + (it.ntok - 1) * step;
         const bool few = rows <= G::FEW;
         float *const ring = sm + (few ? G::FEW : G::M) * LD;
         const int wr_n = few ? G::WRS : G::blocks(rows), wk_n = 8 / wr_n, wr = warp % wr_n, wk = warp / wr_n; // row block, share
@@ -336,7 +343,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
             }
         };
         const int r0 = 16 * wr + g, r8 = r0 + 8;
-        const int s0 = r0 < rows ? it.see + r0 / p.g : 0, s8 = r8 < rows ? it.see + r8 / p.g : 0; // keys the rows see
+        const int s0 = r0 < rows ? it.see + r0 / p.g * step : 0, s8 = r8 < rows ? it.see + r8 / p.g * step : 0; // keys the rows see
         float o[D / 8][4], m0, m8, l0, l8;
         // this warp's step on tile j, on keys kb .. of it
         auto work = [&](int j, int stage, int kb, auto nt, auto again) {
@@ -423,15 +430,16 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
             for (int x = 0; x < 2; ++x) {
                 const int row = x ? r8 : r0, t = row / p.g;
                 const bool bad = (x ? s8 : s0) > ctl.broken;
-                const float m = x ? m8 : m0, l = x ? l8 : l0, i = it.part >= 0 ? 1.f : 1.f / l;
-                float *const to = it.part >= 0 ? p.part_o + ((size_t)it.part * p.rows_max + row) * D
-                                               : static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + it.head * p.g + (row - t * p.g)) * D;
+                const float m = x ? m8 : m0, l = x ? l8 : l0, i = partial ? 1.f : 1.f / l;
+                const int head = it.head * p.g + (row - t * p.g);
+                const size_t prow = part_row(p, it, it.tok + t, head, row);
+                float *const to = partial ? p.part_o + prow * D : static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + head) * D;
                 if (row < rows) {
-                    if (it.part >= 0 && c == 0)
-                        p.part_ml[(size_t)it.part * p.rows_max + row] = make_float2(bad ? NaN : m, l);
+                    if (partial && c == 0)
+                        p.part_ml[prow] = make_float2(bad ? NaN : m, l);
 #pragma unroll
                     for (int e = 0; e < D / 8; ++e)
-                        *reinterpret_cast<float2 *>(to + 8 * e + 2 * c) = it.part < 0 && bad ? make_float2(0.f, 0.f)
+                        *reinterpret_cast<float2 *>(to + 8 * e + 2 * c) = !partial && bad ? make_float2(0.f, 0.f)
                                                                                              : make_float2(o[e][2 * x] * i, o[e][2 * x + 1] * i);
                 }
             }
@@ -450,7 +458,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
         }
         __syncthreads();
         for (int x = tid; x < rows * (D / 4); x += kThreads) {
-            const int row = x / (D / 4), col = 4 * (x - row * (D / 4)), t = row / p.g, see = it.see + t;
+            const int row = x / (D / 4), col = 4 * (x - row * (D / 4)), t = row / p.g, see = it.see + t * step;
             const bool bad = see > ctl.broken;
             float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
             for (int w = 0; w < wk_n; ++w)
@@ -472,14 +480,15 @@ template <int D> __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) a
                             y[e] += v[e];
                 }
             }
-            if (it.part >= 0) {
-                *reinterpret_cast<float4 *>(p.part_o + ((size_t)it.part * p.rows_max + row) * D + col) =
-                    make_float4(y[0], y[1], y[2], y[3]);
+            const int head = it.head * p.g + (row - t * p.g);
+            if (partial) {
+                const size_t prow = part_row(p, it, it.tok + t, head, row);
+                *reinterpret_cast<float4 *>(p.part_o + prow * D + col) = make_float4(y[0], y[1], y[2], y[3]);
                 if (col == 0)
-                    p.part_ml[(size_t)it.part * p.rows_max + row] = make_float2(bad ? NaN : m, l);
+                    p.part_ml[prow] = make_float2(bad ? NaN : m, l);
             } else {
                 const float i = 1.f / l;
-                float *const out = static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + it.head * p.g + (row - t * p.g)) * D + col;
+                float *const out = static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + head) * D + col;
                 *reinterpret_cast<float4 *>(out) =
                     bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[0] * i, y[1] * i, y[2] * i, y[3] * i);
             }
@@ -493,10 +502,10 @@ int slot_rows32(int m, int g, int total_tokens)
     return (total_tokens < tq ? total_tokens : tq) * g;
 }
 
-template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
+// The kernel's shared memory, once a device.
+template <int D, bool SH> cudaError_t configure()
 {
-    typedef Geo32<D> G;
-    static_assert(G::FLOATS * 4 + sizeof(Ctrl32) <= 232448, "shared memory");
+    static_assert(Geo32<D>::FLOATS * 4 + sizeof(Ctrl32<Shared>) <= 232448, "shared memory");
     static std::atomic<unsigned long long> configured{0}; // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -504,12 +513,21 @@ template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
         return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::FLOATS * 4);
+        e = cudaFuncSetAttribute(attn_f32_kernel<D, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo32<D>::FLOATS * 4);
         if (e != cudaSuccess)
             return e;
         configured.fetch_or(bit, std::memory_order_release);
     }
-    WorkArgs p;
+    return cudaSuccess;
+}
+
+template <int D> cudaError_t go(const AttentionArgs &a, const SharedPrefix *f, cudaStream_t s)
+{
+    typedef Geo32<D> G;
+    cudaError_t e = f ? configure<D, true>() : configure<D, false>();
+    if (e != cudaSuccess)
+        return e;
+    SharedArgs p;
     p.a = a;
     p.g = group_heads(a.hq, a.pages.hkv, G::M);
     p.groups = a.hq / a.pages.hkv / p.g;
@@ -517,30 +535,35 @@ template <int D> cudaError_t go(const AttentionArgs &a, cudaStream_t s)
     p.runs = kSms * G::PER_SM;
     p.rows_max = slot_rows32(G::M, p.g, a.c.total_tokens);
     p.second = 0;
+    const dim3 grid(p.runs), block(kThreads);
+    if (f) {
+        shared_layout(p, *f);
+        e = launch_pdl(attn_f32_kernel<D, true>, grid, block, (size_t)G::FLOATS * 4, s, p);
+        return e == cudaSuccess ? launch_join<float, D>(p, s) : e;
+    }
     work_layout(p);
-    e = launch_pdl(attn_f32_kernel<D>, dim3(p.runs), dim3(kThreads), (size_t)G::FLOATS * 4, s, p);
-    if (e != cudaSuccess)
-        return e;
-    return launch_combine<float, D>(p, s);
+    e = launch_pdl(attn_f32_kernel<D, false>, grid, block, (size_t)G::FLOATS * 4, s, static_cast<const WorkArgs &>(p));
+    return e == cudaSuccess ? launch_combine<float, D>(p, s) : e;
 }
 
 } // namespace
 
-size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens)
+size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens, bool shared)
 {
     const int m = d == 256 ? Geo32<256>::M : Geo32<128>::M; // 64 as 128
-    return work_bytes(d, kSms * (d == 64 ? Geo32<64>::PER_SM : 1), slot_rows32(m, group_heads(hq, hkv, m), total_tokens));
+    const int g = group_heads(hq, hkv, m), rows = slot_rows32(m, g, total_tokens), runs = kSms * (d == 64 ? Geo32<64>::PER_SM : 1);
+    return shared ? shared_bytes(d, hq, hq / g, total_tokens, runs, rows) : work_bytes(d, runs, rows);
 }
 
-cudaError_t launch_paged_attention_f32(const AttentionArgs &a, cudaStream_t s)
+cudaError_t launch_paged_attention_f32(const AttentionArgs &a, const SharedPrefix *f, cudaStream_t s)
 {
     switch (a.pages.d) {
     case 64:
-        return go<64>(a, s);
+        return go<64>(a, f, s);
     case 128:
-        return go<128>(a, s);
+        return go<128>(a, f, s);
     default:
-        return go<256>(a, s);
+        return go<256>(a, f, s);
     }
 }
 

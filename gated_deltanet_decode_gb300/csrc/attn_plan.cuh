@@ -25,6 +25,16 @@ struct Item {
     int part;                 // workspace slot of a cut item, or -1
 };
 
+// Attention over shared prefixes (see Shared below) has two kinds of items:
+// the shared keys of a group of rows, for all their tokens, and a row's own
+// keys behind them.
+struct SharedItem : Item {
+    int skip; // pages of the row's table before the item's keys
+    int step; // 1, or 0 where every token sees all keys (shared ones)
+    int kind; // 1: shared keys
+};
+constexpr int kDense = -2; // SharedItem::part: the item's first part, at its tokens' place
+
 // One cut item, for the combining kernel: written by the run that holds the
 // item's second part.
 struct Cut {
@@ -49,6 +59,28 @@ struct WorkArgs {
     float *part_o;     // [2 runs][rows_max][D]
     float2 *part_ml;
     Cut *cuts;         // [runs]
+};
+
+// The same with groups of rows that share their first pages.
+//   part_o, part_ml: [2 kinds][tokens][hq], every item's first part (the one
+//                    with its first key) at its tokens' and heads' place, then
+//                    [runs][rows_max], the part of an item that began before
+//                    the run
+struct SharedArgs : WorkArgs {
+    const int32_t *bounds; // [ngroups + 1] rows of the groups
+    const int2 *prefix;    // [rows] (row whose pages they are, pages), alike within a group
+    int ngroups;
+    size_t dense;          // rows of part_o before the runs' slots
+    int4 *rec;             // [2 kinds][tokens][head groups]: first token of the item, its first run, further runs (-1: a dead
+                           // token), whether shared keys go with them
+};
+template <bool SH> struct Kind {
+    typedef Item ItemT;
+    typedef WorkArgs Args;
+};
+template <> struct Kind<true> {
+    typedef SharedItem ItemT;
+    typedef SharedArgs Args;
 };
 
 // The workspace: cuts, then (m, l) and O of the cut items' parts.
@@ -102,19 +134,72 @@ __device__ __forceinline__ Row row_of(const CacheRows &c, int page_size, int r)
     }
     return x;
 }
+
+// The rows that the plan divides: a call's rows, or with shared prefixes first
+// the groups (their tokens over the shared keys, which all of them see), then
+// the rows (over their own keys).
+struct SharedRow : Row {
+    int row, skip, step, kind; // as in SharedItem
+};
+struct Plain {
+    typedef Row RowT;
+    typedef Item ItemT;
+    static __device__ __forceinline__ int count(const WorkArgs &p) { return p.a.c.rows; }
+    static __device__ __forceinline__ Row get(const WorkArgs &p, int r) { return row_of(p.a.c, p.a.pages.page_size, r); }
+    static __device__ __forceinline__ int step(const Row &) { return 1; }
+};
+struct Shared {
+    typedef SharedRow RowT;
+    typedef SharedItem ItemT;
+    static __device__ __forceinline__ int count(const SharedArgs &p) { return p.ngroups + p.a.c.rows; }
+    static __device__ __forceinline__ int step(const SharedRow &x) { return x.step; }
+    static __device__ SharedRow get(const SharedArgs &p, int i)
+    {
+        const CacheRows &c = p.a.c;
+        const int ps = p.a.pages.page_size;
+        SharedRow x = {};
+        if (i < p.ngroups) {
+            const int r0 = p.bounds[i], r1 = p.bounds[i + 1];
+            x.bad = r0 < 0 || r1 < r0 || r1 > c.rows;
+            if (x.bad || r0 == r1)
+                return x;
+            const int2 f = p.prefix[r0];
+            const int b = c.cu_seqlens[r0], e = c.cu_seqlens[r1];
+            if (f.y == 0)
+                return x;
+            x.bad = f.x < 0 || f.x >= c.rows || f.y < 0 || f.y > c.max_pages || b < 0 || e < b || e > c.total_tokens;
+            x.live = !x.bad && e > b;
+            if (x.live)
+                x.b = b, x.n = e - b, x.len = f.y * ps, x.row = f.x, x.kind = 1;
+            return x;
+        }
+        const int r = i - p.ngroups, pages = p.prefix[r].y;
+        static_cast<Row &>(x) = row_of(c, ps, r);
+        x.row = r, x.step = 1;
+        if (x.live) { // its own keys begin behind the shared pages, which lie before its new tokens
+            x.bad = pages < 0 || pages > c.max_pages || (long long)pages * ps > x.len - x.n;
+            x.live = !x.bad;
+            if (x.live)
+                x.skip = pages, x.len -= pages * ps;
+        }
+        return x;
+    }
+};
+
 // Key tiles of the row's item t (mt tokens an item).
-__device__ __forceinline__ int item_tiles(const Row &x, int t, int mt, int kt)
+template <typename V> __device__ __forceinline__ int item_tiles(const typename V::RowT &x, int t, int mt, int kt)
 {
     const int last = min(x.n, (t + 1) * mt);
-    return (x.len - x.n + last + kt - 1) / kt;
+    return (x.len - (x.n - last) * V::step(x) + kt - 1) / kt;
 }
 __device__ __forceinline__ int items_of(const Row &x, int mt) { return (x.n + mt - 1) / mt; }
-template <typename Cost> __device__ long long head_units(const Row &x, int mt, int kt, int g) // of one key head
+template <typename Cost, typename V>
+__device__ long long head_units(const typename V::RowT &x, int mt, int kt, int g) // of one key head
 {
     long long s = 0;
     const int n = items_of(x, mt);
     for (int t = 0; t < n; ++t)
-        s += item_tiles(x, t, mt, kt) * (long long)Cost::of(min(mt, x.n - t * mt) * g);
+        s += item_tiles<V>(x, t, mt, kt) * (long long)Cost::of(min(mt, x.n - t * mt) * g);
     return s;
 }
 
@@ -149,34 +234,34 @@ __device__ __forceinline__ long long scan64(long long v, long long *part, int wa
 // so that every run between an item's first and last has a part of it.  Called
 // by the whole CTA; `part` is a long long a warp, and `found` the place where
 // one thread leaves the row.
-struct Run {
+template <typename V> struct RunOf {
     long long share, u0, u1, base;
-    long long per; // units a head of the row it begins in
+    long long per;           // units a head of the row it begins in
     int row;
-    Row first;     // that row
+    typename V::RowT first;  // that row
 };
-struct Found { // shared memory
+template <typename V> struct FoundOf { // shared memory
     long long base, per;
     int row;
-    Row first;
+    typename V::RowT first;
 };
-template <int THREADS, int KT, typename Cost> __device__ Run plan_run(const WorkArgs &p, int mt, long long *part, Found &found)
+template <int THREADS, int KT, typename Cost, typename V, typename Args>
+__device__ RunOf<V> plan_run(const Args &p, int mt, long long *part, FoundOf<V> &found)
 {
-    const CacheRows &c = p.a.c;
-    const int ps = p.a.pages.page_size, heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
-    Row x{0, 0, 0, false, false};
+    const int count = V::count(p), heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
+    typename V::RowT x = {};
     long long per = 0;
     auto cost_of = [&](int r) -> long long {
-        if (r >= c.rows)
+        if (r >= count)
             return 0;
-        x = row_of(c, ps, r);
-        per = x.live ? head_units<Cost>(x, mt, KT, p.g) : 0;
+        x = V::get(p, r);
+        per = x.live ? head_units<Cost, V>(x, mt, KT, p.g) : 0;
         return per * heads;
     };
     int dearest = 1; // tile of this thread's rows
-    Run run;
+    RunOf<V> run;
     long long total = 0, cost = 0, before = 0, sum;
-    for (int b = 0; b < c.rows; b += THREADS) {
+    for (int b = 0; b < count; b += THREADS) {
         cost = cost_of(b + tid);
         if (cost > 0)
             dearest = max(dearest, Cost::of(min(x.n, mt) * p.g));
@@ -192,12 +277,12 @@ template <int THREADS, int KT, typename Cost> __device__ Run plan_run(const Work
         run.share = tile;
     run.u0 = run.share * blockIdx.x;
     run.u1 = min(total, run.u0 + run.share);
-    if (c.rows <= THREADS) { // the one pass has it
+    if (count <= THREADS) { // the one pass has it
         if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
             found = {before, per, tid, x};
     } else {
         long long seen = 0;
-        for (int b = 0; b < c.rows && seen <= run.u0 && run.u0 < total; b += THREADS) {
+        for (int b = 0; b < count && seen <= run.u0 && run.u0 < total; b += THREADS) {
             cost = cost_of(b + tid);
             before = seen + scan64(cost, part, THREADS / 32, sum);
             if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
@@ -215,17 +300,23 @@ template <int THREADS, int KT, typename Cost> __device__ Run plan_run(const Work
 
 // Zeros for the outputs of tokens that no live row has, by THREADS threads (tid)
 // of all CTAs together.
-template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkArgs &p, int tid)
+template <typename T, int D, int THREADS, typename V, typename Args> __device__ void zero_dead(const Args &p, int tid)
 {
+    constexpr bool SH = sizeof(Args) != sizeof(WorkArgs);
     const CacheRows &c = p.a.c;
     const size_t vecs = (size_t)p.a.hq * D * sizeof(T) / 16; // a token's
     uint4 *const out = static_cast<uint4 *>(p.a.out);
     auto zero = [&](int t0, int t1) {
         for (size_t i = (size_t)t0 * vecs + tid; i < (size_t)t1 * vecs; i += THREADS)
             out[i] = make_uint4(0, 0, 0, 0);
+        if constexpr (SH) { // nothing to be joined
+            const size_t heads = (size_t)p.a.pages.hkv * p.groups;
+            for (size_t i = t0 * heads + tid; i < t1 * heads; i += THREADS)
+                p.rec[i] = make_int4(0, 0, -1, 0);
+        }
     };
     for (int r = blockIdx.x; r < c.rows; r += gridDim.x) {
-        const Row x = row_of(c, p.a.pages.page_size, r);
+        const auto x = V::get(p, V::count(p) - c.rows + r);
         if (!x.live && x.n > 0)
             zero(x.b, x.b + x.n);
     }
@@ -241,23 +332,27 @@ template <typename T, int D, int THREADS> __device__ void zero_dead(const WorkAr
 }
 
 // The items of a run, in order, by one warp.
-template <typename Cost> struct Walk {
-    const WorkArgs &p;
-    const Run &run;
+template <typename Cost, typename V, typename Args> struct Walk {
+    typedef typename V::RowT RowT;
+    typedef typename V::ItemT ItemT;
+    const Args &p;
+    const RunOf<V> &run;
     int mt, kt, heads, lane;
     long long u;     // where the next tile begins
     int r, win;      // row; rows win .. win + 31 are in the lanes
-    Row mine, x;     // a lane's row; the current one
+    RowT mine, x;    // a lane's row; the current one
     int items, h, t, ja;
     bool in_row;
 
-    __device__ Walk(const WorkArgs &p_, const Run &run_, int mt_, int kt_)
+    __device__ Walk(const Args &p_, const RunOf<V> &run_, int mt_, int kt_)
         : p(p_), run(run_), mt(mt_), kt(kt_), heads(p_.a.pages.hkv * p_.groups), lane(threadIdx.x & 31), u(run_.u0),
           r(run_.row), win(run_.row), in_row(false)
     {
-        if (lane == 0)
-            p.cuts[blockIdx.x].parts = 0;
-        __syncwarp();
+        if constexpr (!SH) {
+            if (lane == 0)
+                p.cuts[blockIdx.x].parts = 0;
+            __syncwarp();
+        }
         fetch(); // the next rows' lengths, while the first row's items are handed out
         if (u < run.u1) {
             enter(run.first);
@@ -265,17 +360,18 @@ template <typename Cost> struct Walk {
             for (; rem >= run.per; ++h)
                 rem -= run.per;
             for (;; ++t) {
-                const long long units = item_tiles(x, t, mt, kt) * (long long)unit();
+                const long long units = item_tiles<V>(x, t, mt, kt) * (long long)unit();
                 if (rem < units)
                     break;
                 rem -= units;
             }
             ja = (int)((rem + unit() - 1) / unit());
             u += (long long)ja * unit() - rem; // a tile that began before u0 is the run's before
-            if (ja == item_tiles(x, t, mt, kt))
+            if (ja == item_tiles<V>(x, t, mt, kt))
                 done();
         }
     }
+    static constexpr bool SH = sizeof(Args) != sizeof(WorkArgs);
     __device__ int unit() const { return Cost::of(min(mt, x.n - t * mt) * p.g); }
     __device__ void done() // with item t
     {
@@ -286,7 +382,7 @@ template <typename Cost> struct Walk {
                 in_row = false, ++r;
         }
     }
-    __device__ void enter(const Row &row)
+    __device__ void enter(const RowT &row)
     {
         x = row;
         in_row = true;
@@ -296,12 +392,12 @@ template <typename Cost> struct Walk {
     __device__ void fetch()
     {
         win = r;
-        mine = Row{0, 0, 0, false, false};
-        if (u < run.u1 && win + lane < p.a.c.rows)
-            mine = row_of(p.a.c, p.a.pages.page_size, win + lane);
+        mine = RowT{};
+        if (u < run.u1 && win + lane < V::count(p))
+            mine = V::get(p, win + lane);
     }
     // The next item; false at the run's end.  Lane 0 lists a cut.
-    __device__ bool next(Item &it)
+    __device__ bool next(ItemT &it)
     {
         if (u >= run.u1)
             return false;
@@ -312,27 +408,67 @@ template <typename Cost> struct Walk {
             x.n = __shfl_sync(0xffffffffu, mine.n, r - win);
             x.len = __shfl_sync(0xffffffffu, mine.len, r - win);
             x.live = true, x.bad = false;
+            if constexpr (SH) {
+                x.row = __shfl_sync(0xffffffffu, mine.row, r - win);
+                x.skip = __shfl_sync(0xffffffffu, mine.skip, r - win);
+                x.step = __shfl_sync(0xffffffffu, mine.step, r - win);
+                x.kind = __shfl_sync(0xffffffffu, mine.kind, r - win);
+            }
             if (!__shfl_sync(0xffffffffu, (int)mine.live, r - win)) {
-                if (++r >= p.a.c.rows)
+                if (++r >= V::count(p))
                     return false;
                 continue;
             }
             enter(x);
         }
-        const int J = item_tiles(x, t, mt, kt);
+        const int J = item_tiles<V>(x, t, mt, kt);
         const int w = unit(), jb = (int)min((long long)J, ja + (run.u1 - u + w - 1) / w);
         const int t0 = t * mt, ntok = min(mt, x.n - t0);
-        it = {x.b + t0, ntok, h, r, x.len - x.n + t0 + 1, ja, jb,
-              ja > 0 || jb < J ? 2 * (int)blockIdx.x + (ja > 0 ? 0 : 1) : -1};
-        // the run that holds an item's second part lists it for the combining kernel
+        const bool cut = ja > 0 || jb < J;
         const long long start = u - (long long)ja * w;
-        if (lane == 0 && ja > 0 && start >= run.u0 - run.share)
-            p.cuts[blockIdx.x] = {2 + (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x, x.b + t0, ntok, h};
+        if constexpr (SH) {
+            static_cast<Item &>(it) = {x.b + t0, ntok, h, x.row, x.len - (x.n - t0 - 1) * x.step, ja, jb,
+                                       ja > 0 ? (int)blockIdx.x : cut || x.kind || x.skip > 0 ? kDense : -1};
+            it.skip = x.skip, it.step = x.step, it.kind = x.kind;
+            if (ja == 0) { // the item's first part says where the others are
+                const int more = (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x;
+                for (int i = lane; i < ntok; i += 32)
+                    p.rec[((size_t)x.kind * p.a.c.total_tokens + x.b + t0 + i) * heads + h] =
+                        make_int4(x.b + t0, (int)blockIdx.x, more, x.skip > 0);
+            }
+        } else {
+            it = {x.b + t0, ntok, h, r, x.len - x.n + t0 + 1, ja, jb, cut ? 2 * (int)blockIdx.x + (ja > 0 ? 0 : 1) : -1};
+            // the run that holds an item's second part lists it for the combining kernel
+            if (lane == 0 && ja > 0 && start >= run.u0 - run.share)
+                p.cuts[blockIdx.x] = {2 + (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x, x.b + t0, ntok, h};
+        }
         u += (long long)(jb - ja) * w;
         done();
         return true;
     }
 };
+
+// Row of part_o and part_ml that a row (token `tok` of all, head `head` of all;
+// `row` of the item's tiles) of a partial item writes.
+__device__ __forceinline__ size_t part_row(const WorkArgs &p, const Item &it, int, int, int row)
+{
+    return (size_t)max(it.part, 0) * p.rows_max + row;
+}
+__device__ __forceinline__ size_t part_row(const SharedArgs &p, const SharedItem &it, int tok, int head, int row)
+{
+    return it.part == kDense ? ((size_t)it.kind * p.a.c.total_tokens + tok) * p.a.hq + head
+                             : p.dense + (size_t)max(it.part, 0) * p.rows_max + row;
+}
+__device__ __forceinline__ int see_step(const Item &) { return 1; }
+__device__ __forceinline__ int see_step(const SharedItem &it) { return it.step; }
+__device__ __forceinline__ const int32_t *item_table(const CacheRows &c, const Item &it)
+{
+    return c.table + (size_t)it.row * c.max_pages;
+}
+__device__ __forceinline__ const int32_t *item_table(const CacheRows &c, const SharedItem &it)
+{
+    return c.table + (size_t)it.row * c.max_pages + it.skip;
+}
 
 // Joins the parts of R rows of the cut that run w listed, by one warp.
 template <typename T, int D, int R> __device__ __forceinline__ void combine_rows(const WorkArgs &p, const Cut &c, int w, int row0, int rows)
@@ -451,6 +587,109 @@ template <typename T, int D> cudaError_t launch_combine(const WorkArgs &p, cudaS
 {
     const int blocks = p.rows_max <= 64 ? (p.rows_max + 3) / 4 : (p.rows_max + 15) / 16;
     return launch_pdl(attn_combine_kernel<T, D>, dim3(p.runs, blocks), dim3(128), 0, s, p);
+}
+
+// Joins what a token's head has of its own and of the shared keys: a warp a
+// (token, head), parts in the order own, shared, each in the order of its keys.
+// Bound, as above, by the latency of three loads in a row: the items' records,
+// a part's (m, l) a lane, and the parts' O, eight at a time.
+template <typename T, int D> __global__ void __launch_bounds__(128) attn_join_kernel(const SharedArgs p)
+{
+    wait_prior_grid();
+    const int lane = threadIdx.x & 31, hq = p.a.hq, heads = p.a.pages.hkv * p.groups;
+    const long long i = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (i >= (long long)p.a.c.total_tokens * hq)
+        return;
+    const int tok = (int)(i / hq), head = (int)(i - (long long)tok * hq), h = head / p.g;
+    int4 own = p.rec[(size_t)tok * heads + h], all = p.rec[((size_t)p.a.c.total_tokens + tok) * heads + h];
+    if (own.z < 0 || (own.z == 0 && !own.w))
+        return; // a dead token, or the item has written the output
+    // (a token that no row has, by tables that are wrong, has no record: whatever is read as one stays within the workspace)
+    auto within = [&](int4 &x) {
+        x.y = min(max(x.y, 0), p.runs - 1);
+        x.z = min(max(x.z, 0), p.runs - 1 - x.y);
+        const int in = min(max(tok - x.x, 0), p.second ? 2 * p.tq - 1 : p.tq - 1), tile = p.second && in >= p.tq;
+        x.x = min(tile * p.second + (in - tile * p.tq) * p.g + (head - h * p.g), p.rows_max - 1); // row of the item's tiles
+    };
+    within(own), within(all);
+    const int no = 1 + own.z, parts = no + (own.w ? 1 + all.z : 0);
+    auto slot = [&](int j) -> size_t {
+        const int4 &x = j < no ? own : all;
+        const int k = j < no ? j : j - no;
+        return k == 0 ? (size_t)((j < no ? 0 : (long long)p.a.c.total_tokens * hq) + i) : p.dense + (size_t)(x.y + k) * p.rows_max + x.x;
+    };
+    constexpr int V = D / 32 < 4 ? D / 32 : 4, N = D / (32 * V); // a lane's columns: N runs of V
+    const float k2 = p.a.scale * 1.44269504088896341f;
+    float m = -INFINITY, l = 0.f, x[N][V] = {};
+    bool bad = false;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        const float2 ml = i0 + lane < parts ? p.part_ml[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
+        bad |= __any_sync(0xffffffffu, ml.x != ml.x);
+        float top = fmaxf(m, ml.x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float old = m == -INFINITY ? 0.f : ex2((m - top) * k2), f = ml.x == -INFINITY ? 0.f : ex2((ml.x - top) * k2);
+        m = top;
+        float sum = ml.y * f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = fmaf(l, old, sum);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                x[n][e] *= old;
+        const int here = min(32, parts - i0);
+#pragma unroll 8
+        for (int j = 0; j < here; ++j) {
+            const float fj = __shfl_sync(0xffffffffu, f, j);
+            const float *const o = p.part_o + slot(i0 + j) * D + V * lane;
+            float y[N][V];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if constexpr (V == 4)
+                    *reinterpret_cast<float4 *>(y[n]) = *reinterpret_cast<const float4 *>(o + 32 * V * n);
+                else
+                    *reinterpret_cast<float2 *>(y[n]) = *reinterpret_cast<const float2 *>(o + 32 * V * n);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < V; ++e) // (what a value that is not finite gave stays; a part without weight is finite)
+                    x[n][e] = fmaf(y[n][e], fj, x[n][e]);
+        }
+    }
+    T *const out = static_cast<T *>(p.a.out) + i * D + V * lane;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            out[32 * V * n + e] = from_f<T>(bad ? 0.f : x[n][e] * inv);
+}
+
+// The workspace with shared prefixes: the records, then (m, l) and O.
+inline size_t shared_bytes(int d, int hq, int heads, int tokens, int runs, int rows_max)
+{
+    const size_t rows = 2 * (size_t)tokens * hq + (size_t)runs * rows_max;
+    return 2 * sizeof(int4) * (size_t)tokens * heads + ((rows + 1) & ~(size_t)1) * sizeof(float2) + rows * sizeof(float) * d;
+}
+inline void shared_layout(SharedArgs &p, const SharedPrefix &f)
+{
+    const size_t tokens = p.a.c.total_tokens;
+    p.bounds = f.bounds, p.prefix = reinterpret_cast<const int2 *>(f.prefix), p.ngroups = f.groups;
+    p.cuts = nullptr;
+    p.dense = 2 * tokens * p.a.hq;
+    const size_t rows = p.dense + (size_t)p.runs * p.rows_max;
+    p.rec = static_cast<int4 *>(p.a.work);
+    p.part_ml = reinterpret_cast<float2 *>(p.rec + 2 * tokens * p.a.pages.hkv * p.groups);
+    p.part_o = reinterpret_cast<float *>(p.part_ml + ((rows + 1) & ~(size_t)1));
+}
+template <typename T, int D> cudaError_t launch_join(const SharedArgs &p, cudaStream_t s)
+{
+    const long long warps = (long long)p.a.c.total_tokens * p.a.hq;
+    return launch_pdl(attn_join_kernel<T, D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, p);
 }
 
 } // namespace

@@ -53,6 +53,7 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_plan.cuh"
 #include "gdn_device.cuh"
@@ -89,17 +90,17 @@ template <int D> struct Geo {
 };
 
 // The control block in shared memory, after Q and the ring.
-struct Ctrl {
+template <typename V> struct CtrlOf {
     unsigned long long full[12], empty[12];    // ring
     unsigned long long qfull[2], qempty[2];
     unsigned long long sready[2], pready[2][2], odone[2];
     unsigned long long ifull[kQueue], iempty[kQueue];
     unsigned long long drain; // the last products
     unsigned long long merge; // the two softmax groups, at the end of a single tile's item
-    Item item[kQueue];
+    typename V::ItemT item[kQueue];
     int valid[kMeta];       // good rows of a key tile, by the tile's count
     long long scan[13];
-    Found found;            // this run's first row, by the plan
+    FoundOf<V> found;       // this run's first row, by the plan
     uint32_t tmem;
     float ml[2][128][2];    // (m, l) of the two groups' rows, for the merge
     int bad[2];             // first key that could not be read, by group
@@ -108,7 +109,7 @@ struct Ctrl {
     // is in item q + 2 then, whose scores come after weights that every warp hands over in item q + 1, or after a meeting.
     int dirty[2];
 };
-static_assert(sizeof(Ctrl) <= 3 * 1024, "control block");
+static_assert(sizeof(CtrlOf<Plain>) <= 3 * 1024 && sizeof(CtrlOf<Shared>) <= 3 * 1024, "control block");
 
 // ---- tensor core and copy wrappers ----
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart
@@ -246,11 +247,14 @@ __device__ __forceinline__ void tst(uint32_t a, const uint32_t (&r)[32])
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool SH>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
-    attn_tc_kernel(const WorkArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+    attn_tc_kernel(const typename Kind<SH>::Args p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
     typedef Geo<D> G;
+    typedef typename std::conditional<SH, Shared, Plain>::type View;
+    typedef CtrlOf<View> Ctrl;
+    typedef typename Kind<SH>::ItemT ItemT;
     constexpr int KT = G::KT;
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctrl &ctl = *reinterpret_cast<Ctrl *>(smem + G::CTRL);
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const Run run = plan_run<G::THREADS, KT, EvenCost>(p, mt, ctl.scan, ctl.found);
+    const RunOf<View> run = plan_run<G::THREADS, KT, EvenCost, View>(p, mt, ctl.scan, ctl.found);
     bool alive = true; // false once a bounded wait ran out
     auto wait_at = [&](uint32_t b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
         if (!__all_sync(0xffffffffu, mbar_try(b, parity)) && alive && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
@@ -317,8 +321,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 3) {
             // ---- the walk: this run's items, in order
-            Walk<EvenCost> walk(p, run, mt, KT);
-            Item it;
+            Walk<EvenCost, View, typename Kind<SH>::Args> walk(p, run, mt, KT);
+            ItemT it;
             for (int q = 0; alive; ++q) {
                 const bool more = walk.next(it);
                 const int slot = q % kQueue;
@@ -343,15 +347,15 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 const int slot = q % kQueue;
                 if (!wait(ctl.ifull[slot], (q / kQueue) & 1))
                     break;
-                const Item it = ctl.item[slot];
+                const ItemT it = ctl.item[slot];
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(ctl.iempty[slot]));
                 if (it.ntok == 0)
                     break;
-                const int32_t *const table = a.c.table + (size_t)it.row * a.c.max_pages;
+                const int32_t *const table = item_table(a.c, it);
                 const int kvh = it.head / p.groups;
-                const int end = it.see + it.ntok - 1;     // keys the item's last token sees
+                const int end = it.see + (it.ntok - 1) * see_step(it); // keys the item's last token sees
                 const int pages = (end + ps - 1) >> a.pages.page_shift;
                 const bool pair = G::NO == 2 && it.ntok > p.tq;
                 const int n = it.jb - it.ja;
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 const int slot = q % kQueue;
                 if (!wait(ctl.ifull[slot], (q / kQueue) & 1))
                     break;
-                const Item it = ctl.item[slot];
+                const ItemT it = ctl.item[slot];
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(ctl.iempty[slot]));
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
         if constexpr (G::NO == 2)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ---- softmax: a thread a row; first, zeros where no live row writes
-        zero_dead<bf16, D, 128 * G::NO>(p, tid - 128);
+        zero_dead<bf16, D, 128 * G::NO, View>(p, tid - 128);
         const int grp = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // 32 tensor-memory lanes a warp
         const float c = a.scale * 1.44269504088896341f;    // weights are 2^(c (s - m))
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             const int slot = q % kQueue;
             if (!wait(ctl.ifull[slot], (q / kQueue) & 1))
                 break;
-            const Item it = ctl.item[slot];
+            const ItemT it = ctl.item[slot];
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar(ctl.iempty[slot]));
@@ -608,8 +612,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             const int n = it.jb - it.ja, steps = pair ? 2 * n : n;
             const int tt = tok + (pair ? grp * p.tq : 0);            // this row's token in the item
             const bool mine = tok < p.tq && tt < it.ntok;
-            const int see = mine ? it.see + tt : 0;                  // keys this row sees
-            const int end = it.see + it.ntok - 1;
+            const int see = mine ? it.see + tt * see_step(it) : 0;   // keys this row sees
+            const int end = it.see + (it.ntok - 1) * see_step(it);
             const bool idle = __all_sync(0xffffffffu, !mine);
             float m = -INFINITY, l = 0.f;
             int broken = 0x7fffffff;
@@ -781,11 +785,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             if (!idle) {
                 const int o = pair ? grp : 0;
                 const int k0 = G::NO == 2 && !pair ? grp * (D / 2) : 0, k1 = G::NO == 2 && !pair ? k0 + D / 2 : D;
-                const float inv = it.part >= 0 ? 1.f : 1.f / l;
-                const int prow = row + (pair ? grp * 128 : 0);
-                float *const po = p.part_o + ((size_t)max(it.part, 0) * p.rows_max + prow) * D;
-                if (it.part >= 0 && mine && k0 == 0)
-                    p.part_ml[(size_t)it.part * p.rows_max + prow] = make_float2(bad ? NaN : m, l);
+                const bool partial = it.part != -1;
+                const float inv = partial ? 1.f : 1.f / l;
+                const size_t prow = part_row(p, it, it.tok + tt, it.head * p.g + (row - tok * p.g), row + (pair ? grp * 128 : 0));
+                float *const po = p.part_o + prow * D;
+                if (partial && mine && k0 == 0)
+                    p.part_ml[prow] = make_float2(bad ? NaN : m, l);
 #pragma unroll 1
                 for (int k = k0; k < k1; k += 32) {
                     uint32_t r[32];
@@ -803,7 +808,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     if (dirty && !bad) {
                         // the elements that the tiles lost, from the cache itself
                         for (int key = max(it.see, it.ja * KT); key < min(see, it.jb * KT); ++key) {
-                            const int page = a.c.table[(size_t)it.row * a.c.max_pages + (key >> a.pages.page_shift)];
+                            const int page = item_table(a.c, it)[key >> a.pages.page_shift];
                             const bf16 *const v = static_cast<const bf16 *>(a.pages.v) +
                                                   (((size_t)page * hkv + it.head / p.groups) * ps + (key & (ps - 1))) * D + k;
 #pragma unroll 1
@@ -814,7 +819,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                             }
                         }
                     }
-                    if (mine && it.part >= 0) {
+                    if (mine && partial) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             *reinterpret_cast<float4 *>(po + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
@@ -884,10 +889,10 @@ int slot_rows(int d, int g, int total_tokens)
     return 128 + one; // a pair of tiles, the second's rows from 128 on
 }
 
-template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s)
+// The kernel's shared memory, once a device.
+template <int D, bool SH> cudaError_t configure()
 {
-    typedef Geo<D> G;
-    static_assert(G::TOTAL <= 232448, "shared memory");
+    static_assert(Geo<D>::TOTAL <= 232448, "shared memory");
     static std::atomic<unsigned long long> configured{0}; // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -895,12 +900,21 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
         return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::TOTAL);
+        e = cudaFuncSetAttribute(attn_tc_kernel<D, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::TOTAL);
         if (e != cudaSuccess)
             return e;
         configured.fetch_or(bit, std::memory_order_release);
     }
-    WorkArgs p;
+    return cudaSuccess;
+}
+
+template <int D> cudaError_t go(const AttentionArgs &a, const SharedPrefix *f, kv_page_pool &pool, cudaStream_t s)
+{
+    typedef Geo<D> G;
+    cudaError_t e = f ? configure<D, true>() : configure<D, false>();
+    if (e != cudaSuccess)
+        return e;
+    SharedArgs p;
     p.a = a;
     p.g = group_heads(a.hq, a.pages.hkv, 128);
     p.groups = a.hq / a.pages.hkv / p.g;
@@ -908,7 +922,6 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
     p.runs = kSms; // one CTA an SM: its tensor memory is taken whole
     p.rows_max = slot_rows(D, p.g, a.c.total_tokens);
     p.second = G::NO == 2 ? 128 : 0;
-    work_layout(p);
     {
         const std::lock_guard<std::mutex> lk(pool.map_mutex);
         const int box = pool.page_size < G::KT ? pool.page_size : G::KT;
@@ -918,28 +931,34 @@ template <int D> cudaError_t go(const AttentionArgs &a, kv_page_pool &pool, cuda
             pool.mapped = true;
         }
     }
-    e = launch_pdl(attn_tc_kernel<D>, dim3(p.runs), dim3(G::THREADS), (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
-    if (e != cudaSuccess)
-        return e;
-    return launch_combine<bf16, D>(p, s);
+    const dim3 grid(p.runs), block(G::THREADS);
+    if (f) {
+        shared_layout(p, *f);
+        e = launch_pdl(attn_tc_kernel<D, true>, grid, block, (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
+        return e == cudaSuccess ? launch_join<bf16, D>(p, s) : e;
+    }
+    work_layout(p);
+    e = launch_pdl(attn_tc_kernel<D, false>, grid, block, (size_t)G::TOTAL, s, static_cast<const WorkArgs &>(p), pool.kmap, pool.vmap);
+    return e == cudaSuccess ? launch_combine<bf16, D>(p, s) : e;
 }
 
 } // namespace
 
-size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens)
+size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens, bool shared)
 {
-    return work_bytes(d, kSms, slot_rows(d, group_heads(hq, hkv, 128), total_tokens));
+    const int g = group_heads(hq, hkv, 128), rows = slot_rows(d, g, total_tokens);
+    return shared ? shared_bytes(d, hq, hq / g, total_tokens, kSms, rows) : work_bytes(d, kSms, rows);
 }
 
-cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s)
+cudaError_t launch_paged_attention_tc(const AttentionArgs &a, const SharedPrefix *f, kv_page_pool &pool, cudaStream_t s)
 {
     switch (a.pages.d) {
     case 64:
-        return go<64>(a, pool, s);
+        return go<64>(a, f, pool, s);
     case 128:
-        return go<128>(a, pool, s);
+        return go<128>(a, f, pool, s);
     default:
-        return go<256>(a, pool, s);
+        return go<256>(a, f, pool, s);
     }
 }
 

@@ -28,6 +28,9 @@ decltype(&kv_pages_copy) c_copy;
 decltype(&linear_attention_decode) c_linear_decode;
 decltype(&linear_attention_prefill_workspace_bytes) c_linear_workspace;
 decltype(&linear_attention_prefill) c_linear_prefill;
+decltype(&kv_pages_shared) c_shared;
+decltype(&paged_attention_shared_workspace_bytes) c_shared_workspace;
+decltype(&paged_attention_shared) c_attention_shared;
 
 struct Pool {
     kv_page_pool *handle;
@@ -159,10 +162,10 @@ PyObject *prologue(PyObject *, PyObject *const *a, Py_ssize_t n)
     return a[13];
 }
 
-// q pool table seq_len cu_seqlens layer scale out workspace
+// q pool table seq_len cu_seqlens layer scale out workspace; with shared prefixes also bounds prefix
 PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 9)
+    if (n != 9 && n != 11)
         Py_RETURN_NONE;
     const Pool &pool = *pool_of(a[1]);
     const int dev = pool.device;
@@ -180,6 +183,13 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     }
     if (!seq.ok || !cu.ok || !given.ok)
         Py_RETURN_NONE;
+    const at::Tensor *bounds = nullptr, *prefix = nullptr;
+    if (n == 11) {
+        bounds = tensor(a[9]), prefix = tensor(a[10]);
+        if (!bounds || !prefix || !plain(*bounds, at::kInt, dev) || bounds->numel() < 1 || !plain(*prefix, at::kInt, dev) ||
+            prefix->numel() != 2 * (int64_t)table.rows)
+            Py_RETURN_NONE;
+    }
     const int64_t size[3] = {q.tokens, q.heads, pool.d};
     at::Tensor made, room;
     void *out = given.as<void>(), *work = nullptr;
@@ -189,7 +199,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         out = made.mutable_data_ptr();
     }
     if (a[8] == Py_None) {
-        bytes = c_workspace(pool.handle, (int)q.heads, table.rows, (int)q.tokens);
+        bytes = (bounds ? c_shared_workspace : c_workspace)(pool.handle, (int)q.heads, table.rows, (int)q.tokens);
         const int64_t length = (int64_t)bytes;
         room = cuda_empty(at::IntArrayRef(&length, 1), at::kByte, dev);
         work = room.mutable_data_ptr();
@@ -200,15 +210,55 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         work = w->mutable_data_ptr();
         bytes = w->nbytes();
     }
-    const int rc = c_attention(q.p, q.stride, pool.handle, (int)layer, table.p, table.width, seq.as<int32_t>(), cu.as<int32_t>(),
-                    (float)scale, out, (int)q.heads, table.rows, (int)q.tokens, work, bytes, pool.code,
-                    stream_of(dev));
+    const int rc = bounds ? c_attention_shared(q.p, q.stride, pool.handle, (int)layer, table.p, table.width, seq.as<int32_t>(),
+                                               cu.as<int32_t>(), bounds->const_data_ptr<int32_t>(), (int)bounds->numel() - 1,
+                                               prefix->const_data_ptr<int32_t>(), (float)scale, out, (int)q.heads, table.rows,
+                                               (int)q.tokens, work, bytes, pool.code, stream_of(dev))
+                          : c_attention(q.p, q.stride, pool.handle, (int)layer, table.p, table.width, seq.as<int32_t>(),
+                                        cu.as<int32_t>(), (float)scale, out, (int)q.heads, table.rows, (int)q.tokens, work, bytes,
+                                        pool.code, stream_of(dev));
     if (rc != GDN_OK)
         return PyLong_FromLong(rc);
     if (a[7] == Py_None)
         return THPVariable_Wrap(std::move(made));
     Py_INCREF(a[7]);
     return a[7];
+}
+
+// table seq_len cu_seqlens bounds page_size out
+PyObject *shared_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 6)
+        Py_RETURN_NONE;
+    const Table table(a[0]);
+    const at::Tensor *bounds = tensor(a[3]);
+    if (!table.ok || !current(table.device) || !bounds || !plain(*bounds, at::kInt, table.device) || bounds->numel() < 1)
+        Py_RETURN_NONE;
+    const int dev = table.device;
+    const Arg seq(a[1], table.rows, at::kInt, dev), cu(a[2], table.rows + 1, at::kInt, dev),
+        given(a[5], 2 * (int64_t)table.rows, at::kInt, dev, kOrNone);
+    const long page = PyLong_AsLong(a[4]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    if (!seq.ok || !cu.ok || !given.ok)
+        Py_RETURN_NONE;
+    at::Tensor made;
+    int32_t *out = given.as<int32_t>();
+    if (a[5] == Py_None) {
+        const int64_t size[2] = {table.rows, 2};
+        made = cuda_empty(size, at::kInt, dev);
+        out = made.mutable_data_ptr<int32_t>();
+    }
+    const int rc = c_shared(table.p, table.rows, table.width, seq.as<int32_t>(), cu.as<int32_t>(), bounds->const_data_ptr<int32_t>(),
+                            (int)bounds->numel() - 1, (int)page, out, stream_of(dev));
+    if (rc != GDN_OK)
+        return PyLong_FromLong(rc);
+    if (a[5] == Py_None)
+        return THPVariable_Wrap(std::move(made));
+    Py_INCREF(a[5]);
+    return a[5];
 }
 
 // table seq_len refs src_rows dst_rows page_size move_src move_dst move_count status
@@ -438,7 +488,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
                    reinterpret_cast<void **>(&c_attention),     reinterpret_cast<void **>(&c_fork),
                    reinterpret_cast<void **>(&c_free),          reinterpret_cast<void **>(&c_copy),
                    reinterpret_cast<void **>(&c_linear_decode), reinterpret_cast<void **>(&c_linear_workspace),
-                   reinterpret_cast<void **>(&c_linear_prefill)};
+                   reinterpret_cast<void **>(&c_linear_prefill), reinterpret_cast<void **>(&c_shared),
+                   reinterpret_cast<void **>(&c_shared_workspace), reinterpret_cast<void **>(&c_attention_shared)};
     constexpr int count = sizeof(to) / sizeof(*to);
     if (n != count) {
         PyErr_Format(PyExc_TypeError, "%d addresses are needed", count);
@@ -470,6 +521,7 @@ PyMethodDef methods[] = {METHOD("bind", bind),           METHOD("make_pool", mak
                          METHOD("kv_pages_free", free_rows),   METHOD("kv_pages_copy", copy_pages),
                          METHOD("make_state", make_state),     METHOD("drop_state", drop_state),
                          METHOD("linear_decode", linear_decode), METHOD("linear_prefill", linear_prefill),
+                         METHOD("kv_pages_shared", shared_pages), METHOD("paged_attention_shared", attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

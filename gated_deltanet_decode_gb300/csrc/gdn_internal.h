@@ -184,6 +184,12 @@ struct AttentionArgs {
     int *err;
 };
 
+// Groups of rows that share their first pages (paged_attention_shared).
+struct SharedPrefix {
+    const int32_t *bounds, *prefix; // [groups + 1], [rows][2]
+    int groups;
+};
+
 struct PageTables {
     int32_t *table;
     int table_rows, max_pages;
@@ -215,11 +221,13 @@ cudaError_t launch_linear_serial(const LinearArgs &a, int dtype, cudaStream_t s)
 cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table,
                               cudaStream_t s);
 cudaError_t launch_attn_prologue(const PrologueArgs &a, int dtype, cudaStream_t s);
-// paged_attention: bf16 (attn_tc.cu) and fp32 (attn_f32.cu)
-size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens);
-size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens);
-cudaError_t launch_paged_attention_tc(const AttentionArgs &a, kv_page_pool &pool, cudaStream_t s);
-cudaError_t launch_paged_attention_f32(const AttentionArgs &a, cudaStream_t s);
+// paged_attention and, with f, paged_attention_shared: bf16 (attn_tc.cu) and fp32 (attn_f32.cu)
+size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens, bool shared);
+size_t attention_f32_workspace_bytes(int d, int hq, int hkv, int total_tokens, bool shared);
+cudaError_t launch_paged_attention_tc(const AttentionArgs &a, const SharedPrefix *f, kv_page_pool &pool, cudaStream_t s);
+cudaError_t launch_paged_attention_f32(const AttentionArgs &a, const SharedPrefix *f, cudaStream_t s);
+cudaError_t launch_pages_shared(const CacheRows &c, const int32_t *bounds, int groups, int page_size, int32_t *prefix,
+                                int *err, cudaStream_t s);
 cudaError_t launch_pages_reserve(const PageTables &t, const int32_t *list_rows, const int32_t *tokens, int n,
                                  int32_t *status, cudaStream_t s);
 cudaError_t launch_pages_fork(const PageTables &t, const int32_t *src_rows, const int32_t *dst_rows, int n,

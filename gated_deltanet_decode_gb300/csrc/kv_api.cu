@@ -101,6 +101,46 @@ int check_tables(const int32_t *table, int table_rows, int max_pages, const int3
 
 int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? api_ok() : api_cuda_fail(e, what); }
 
+size_t workspace_bytes_of(const kv_page_pool *pool, int hq, int rows, int total_tokens, bool shared)
+{
+    if (!pool || hq < 1 || hq % pool->hkv != 0 || rows < 1 || total_tokens < 1)
+        return 0;
+    return pool->dtype == GDN_BF16 ? gdn::attention_tc_workspace_bytes(pool->d, hq, pool->hkv, total_tokens, shared)
+                                   : gdn::attention_f32_workspace_bytes(pool->d, hq, pool->hkv, total_tokens, shared);
+}
+
+// paged_attention (f NULL) and paged_attention_shared
+int attention(const void *q, int64_t q_stride, kv_page_pool *pool, int layer, const int32_t *table, int max_pages,
+              const int32_t *seq_len, const int32_t *cu_seqlens, const gdn::SharedPrefix *f, float scale, void *out, int hq,
+              int rows, int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream, const char *what)
+{
+    int rc = check_rows(pool, layer, table, max_pages, seq_len, cu_seqlens, hq, rows, total_tokens, dtype);
+    if (rc)
+        return rc;
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return api_fail(GDN_EINVAL, "scale must be positive and finite");
+    if (total_tokens == 0)
+        return api_ok();
+    if ((rc = check_stride("q", q, q_stride, hq, pool->d, dtype)))
+        return rc;
+    if (!out || !aligned16(out))
+        return api_fail(GDN_EINVAL, "out must be non-NULL and 16-byte aligned");
+    const size_t need = workspace_bytes_of(pool, hq, rows, total_tokens, f != nullptr);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return api_fail(GDN_EINVAL, "workspace must be 16-byte aligned and hold %zu bytes (given %zu)", need,
+                        workspace ? workspace_bytes : (size_t)0);
+    gdn::AttentionArgs a = {};
+    if ((rc = api_error_word(&a.err)))
+        return rc;
+    a.q = q, a.q_stride = q_stride;
+    a.pages = view(pool, layer);
+    a.c = {table, seq_len, cu_seqlens, max_pages, rows, total_tokens};
+    a.scale = scale, a.out = out, a.hq = hq, a.work = workspace;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launched(dtype == GDN_BF16 ? gdn::launch_paged_attention_tc(a, f, *pool, s) : gdn::launch_paged_attention_f32(a, f, s),
+                    what);
+}
+
 } // namespace
 
 extern "C" {
@@ -240,41 +280,64 @@ int attn_prologue(const void *q, int64_t q_stride, const void *k, int64_t k_stri
 
 size_t paged_attention_workspace_bytes(const kv_page_pool *pool, int hq, int rows, int total_tokens)
 {
-    if (!pool || hq < 1 || hq % pool->hkv != 0 || rows < 1 || total_tokens < 1)
-        return 0;
-    return pool->dtype == GDN_BF16 ? gdn::attention_tc_workspace_bytes(pool->d, hq, pool->hkv, total_tokens)
-                                   : gdn::attention_f32_workspace_bytes(pool->d, hq, pool->hkv, total_tokens);
+    return workspace_bytes_of(pool, hq, rows, total_tokens, false);
 }
 
 int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int layer, const int32_t *table,
                     int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens, float scale, void *out, int hq,
                     int rows, int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream)
 {
-    int rc = check_rows(pool, layer, table, max_pages, seq_len, cu_seqlens, hq, rows, total_tokens, dtype);
+    return attention(q, q_stride, pool, layer, table, max_pages, seq_len, cu_seqlens, nullptr, scale, out, hq, rows,
+                     total_tokens, workspace, workspace_bytes, dtype, stream, "paged_attention launch");
+}
+
+size_t paged_attention_shared_workspace_bytes(const kv_page_pool *pool, int hq, int rows, int total_tokens)
+{
+    return workspace_bytes_of(pool, hq, rows, total_tokens, true);
+}
+
+int paged_attention_shared(const void *q, int64_t q_stride, kv_page_pool *pool, int layer, const int32_t *table,
+                           int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens, const int32_t *bounds,
+                           int groups, const int32_t *prefix, float scale, void *out, int hq, int rows,
+                           int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream)
+{
+    if (groups < 0 || groups > rows)
+        return api_fail(GDN_EINVAL, "groups=%d outside [0, rows=%d]", groups, rows);
+    if (total_tokens > 0 && (!bounds || !prefix))
+        return api_fail(GDN_EINVAL, "bounds and prefix must be non-NULL");
+    if (reinterpret_cast<uintptr_t>(prefix) & 7u)
+        return api_fail(GDN_EINVAL, "prefix must be 8-byte aligned");
+    const gdn::SharedPrefix f = {bounds, prefix, groups};
+    return attention(q, q_stride, pool, layer, table, max_pages, seq_len, cu_seqlens, &f, scale, out, hq, rows,
+                     total_tokens, workspace, workspace_bytes, dtype, stream, "paged_attention_shared launch");
+}
+
+int kv_pages_shared(const int32_t *table, int rows, int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens,
+                    const int32_t *bounds, int groups, int page_size, int32_t *prefix, void *stream)
+{
+    if (rows < 0 || max_pages < 1)
+        return api_fail(GDN_EINVAL, "rows=%d max_pages=%d", rows, max_pages);
+    if (!page_size_ok(page_size))
+        return api_fail(GDN_EUNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", page_size);
+    if ((long long)max_pages * page_size > kMaxTokens)
+        return api_fail(GDN_EUNSUPPORTED, "max_pages=%d pages hold over 2^30 tokens", max_pages);
+    if (groups < 0 || groups > rows)
+        return api_fail(GDN_EINVAL, "groups=%d outside [0, rows=%d]", groups, rows);
+    if (rows == 0)
+        return api_ok();
+    if (groups == 0)
+        return api_fail(GDN_EINVAL, "groups=0 with rows=%d", rows);
+    if (!table || !seq_len || !cu_seqlens || !bounds || !prefix)
+        return api_fail(GDN_EINVAL, "table, seq_len, cu_seqlens, bounds and prefix must be non-NULL");
+    if (reinterpret_cast<uintptr_t>(prefix) & 7u)
+        return api_fail(GDN_EINVAL, "prefix must be 8-byte aligned");
+    int *err = nullptr;
+    int rc = api_error_word(&err);
     if (rc)
         return rc;
-    if (!(scale > 0.f) || !std::isfinite(scale))
-        return api_fail(GDN_EINVAL, "scale must be positive and finite");
-    if (total_tokens == 0)
-        return api_ok();
-    if ((rc = check_stride("q", q, q_stride, hq, pool->d, dtype)))
-        return rc;
-    if (!out || !aligned16(out))
-        return api_fail(GDN_EINVAL, "out must be non-NULL and 16-byte aligned");
-    const size_t need = paged_attention_workspace_bytes(pool, hq, rows, total_tokens);
-    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
-        return api_fail(GDN_EINVAL, "workspace must be 16-byte aligned and hold %zu bytes (given %zu)", need,
-                        workspace ? workspace_bytes : (size_t)0);
-    gdn::AttentionArgs a = {};
-    if ((rc = api_error_word(&a.err)))
-        return rc;
-    a.q = q, a.q_stride = q_stride;
-    a.pages = view(pool, layer);
-    a.c = {table, seq_len, cu_seqlens, max_pages, rows, total_tokens};
-    a.scale = scale, a.out = out, a.hq = hq, a.work = workspace;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launched(dtype == GDN_BF16 ? gdn::launch_paged_attention_tc(a, *pool, s) : gdn::launch_paged_attention_f32(a, s),
-                    "paged_attention launch");
+    const gdn::CacheRows c = {table, seq_len, cu_seqlens, max_pages, rows, 0};
+    return launched(gdn::launch_pages_shared(c, bounds, groups, page_size, prefix, err, static_cast<cudaStream_t>(stream)),
+                    "kv_pages_shared launch");
 }
 
 // ---- pages ----------------------------------------------------------------------------

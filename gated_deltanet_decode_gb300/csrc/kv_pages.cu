@@ -1,10 +1,12 @@
 // Pages of cache rows (sm_103a): reserving, forking and freeing them,
-// compacting a pool, and copying page contents.
+// compacting a pool, copying page contents, and finding what rows share.
 //
 // The reference counts are the only record of what is free, so every
 // allocation ranks the free pages (refs == 0, page 0 apart) in ascending order
 // and hands rank r to the r-th page asked for: the result depends on the
 // tables alone, never on timing.
+#include <cooperative_groups.h>
+
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
 
@@ -507,7 +509,108 @@ int sm_count()
     return n;
 }
 
+// The pages that the rows of a group share: a cluster of CTAs a group.  Every
+// CTA looks over the group's lengths (the first live row leads, and no row's
+// new tokens may lie in a shared page); then the warps of the cluster compare
+// the live rows' entries with the leader's, kSpan of them at a time, and leave
+// out what lies behind the first difference found so far.  Bound: latency, of
+// four or five loads in a row; the entries themselves are few.
+constexpr int kSpan = 256;
+
+__global__ void __launch_bounds__(kRowThreads) shared_kernel(const CacheRows c, const int32_t *bounds, int groups, int page_shift,
+                                                             int2 *prefix, int *err)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ int lead, live, limit; // this CTA's, then the cluster's in its first CTA
+    const int tid = threadIdx.x, lane = tid & 31, warps = kRowThreads / 32, size = cluster.num_blocks(), rank = cluster.block_rank();
+    const int g = blockIdx.x / size;
+    wait_prior_grid();
+    const int b0 = bounds[g], b1 = bounds[g + 1];
+    const int r0 = min(max(b0, 0), c.rows), r1 = min(max(b1, r0), c.rows);
+    if (tid == 0) {
+        lead = r1, live = 0, limit = c.max_pages;
+        if (rank == 0 && (r0 != b0 || r1 != b1 || (g == 0 && b0 != 0) || (g == groups - 1 && b1 != c.rows)))
+            report(err, GDN_DEVERR_BAD_PAGE);
+    }
+    __syncthreads();
+    auto before = [&](int r) { // tokens before the new ones, or -1
+        const int n = c.seq_len[r], fresh = c.cu_seqlens[r + 1] - c.cu_seqlens[r];
+        return n > 0 && fresh > 0 && n >= fresh ? n - fresh : -1;
+    };
+    for (int r = r0 + tid; r < r1; r += kRowThreads) {
+        const int n = before(r);
+        if (n >= 0) {
+            atomicMin(&lead, r);
+            atomicAdd(&live, 1);
+            atomicMin(&limit, n >> page_shift);
+        }
+    }
+    __syncthreads();
+    const int first = lead < r1 ? lead : r0;
+    const int most = live > 1 ? limit : 0; // (the same in every CTA)
+    __syncthreads();
+    if (tid == 0)
+        limit = most;
+    cluster.sync();
+    int *const found = cluster.map_shared_rank(&limit, 0);
+    const int32_t *const model = c.table + (size_t)first * c.max_pages;
+    const int spans = (most + kSpan - 1) / kSpan;
+    const long long units = (long long)spans * (r1 - r0);
+    for (long long u = (long long)rank * warps + tid / 32; u < units; u += (long long)size * warps) {
+        const int span = (int)(u / (r1 - r0)), r = r0 + (int)(u - (long long)span * (r1 - r0)), at = span * kSpan + lane;
+        if (r == first || span * kSpan >= *reinterpret_cast<volatile int *>(&limit) || before(r) < 0)
+            continue;
+        const int32_t *const row = c.table + (size_t)r * c.max_pages;
+        int differs = most;
+#pragma unroll
+        for (int k = kSpan / 32 - 1; k >= 0; --k) {
+            const int i = at + 32 * k;
+            if (i < most && row[i] != model[i])
+                differs = i;
+        }
+        differs = __reduce_min_sync(0xffffffffu, differs);
+        if (lane == 0 && differs < most) {
+            atomicMin(&limit, differs);
+            if (rank != 0)
+                atomicMin(found, differs);
+        }
+    }
+    cluster.sync();
+    const int2 answer = make_int2(first, *reinterpret_cast<volatile int *>(found));
+    for (int r = r0 + rank * kRowThreads + tid; r < r1; r += size * kRowThreads)
+        prefix[r] = answer;
+    if (g == 0 && rank == 0) // rows of no group, by bounds that are wrong
+        for (int r = tid; r < r0; r += kRowThreads)
+            prefix[r] = make_int2(r, 0);
+    if (g == groups - 1 && rank == 0)
+        for (int r = r1 + tid; r < c.rows; r += kRowThreads)
+            prefix[r] = make_int2(r, 0);
+    cluster.sync(); // the first CTA's memory is read by the others
+}
+
 } // namespace
+
+cudaError_t launch_pages_shared(const CacheRows &c, const int32_t *bounds, int groups, int page_size, int32_t *prefix, int *err,
+                                cudaStream_t s)
+{
+    constexpr unsigned kCluster = 8;
+    int shift = 0;
+    while ((1 << shift) < page_size)
+        ++shift;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)groups * kCluster);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, shared_kernel, c, bounds, groups, shift, reinterpret_cast<int2 *>(prefix), err);
+}
 
 cudaError_t launch_pages_reserve(const PageTables &t, const int32_t *list_rows, const int32_t *tokens, int n,
                                  int32_t *status, cudaStream_t s)

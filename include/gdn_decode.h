@@ -502,6 +502,35 @@ int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int lay
                     int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens, float scale, void *out, int hq,
                     int rows, int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream);
 
+/* Rows that share their first pages, as forks of one prompt do, read the keys
+ * and values there once for all of them.  Groups are neighbouring rows: group
+ * g is rows bounds[g] .. bounds[g+1] (bounds [groups+1] int32, non-decreasing,
+ * from 0 to rows; a row that shares nothing is a group of its own).
+ *
+ * kv_pages_shared: prefix [rows][2] int32, 8-byte aligned, gets for every row
+ * its group's first live row, and how many leading pages all live rows of the
+ * group share: pages with the same entries in their tables that hold none of
+ * their new tokens.  A row is live when seq_len[r] is at least its new tokens,
+ * of which it has one or more.  A group with fewer than two live rows shares
+ * none (and its first row stands in where none is live).  Bounds that are
+ * wrong set GDN_DEVERR_BAD_PAGE, and rows of no group get (r, 0).
+ *
+ * paged_attention_shared: paged_attention, with each group's shared pages read
+ * once.  prefix is what kv_pages_shared gives for the same table, lengths and
+ * bounds (another is fine that names, alike for every row of a group, a row
+ * and a number of its pages that all of the group's live rows begin with).  A
+ * row whose pages before its new tokens are fewer than prefix[r][1] gives
+ * zeros, with GDN_DEVERR_BAD_PAGE; the outputs of a group whose bounds or
+ * prefix are wrong mean nothing, with the same code.  The workspace is
+ * paged_attention_shared_workspace_bytes. */
+int kv_pages_shared(const int32_t *table, int rows, int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens,
+                    const int32_t *bounds, int groups, int page_size, int32_t *prefix, void *stream);
+size_t paged_attention_shared_workspace_bytes(const kv_page_pool *pool, int hq, int rows, int total_tokens);
+int paged_attention_shared(const void *q, int64_t q_stride, kv_page_pool *pool, int layer, const int32_t *table,
+                           int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens, const int32_t *bounds,
+                           int groups, const int32_t *prefix, float scale, void *out, int hq, int rows,
+                           int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream);
+
 /* Pages of rows, on the device.  Free pages are taken lowest first, for the
  * listed rows in order.  `list_rows` (n of them) are distinct row numbers
  * below table_rows; n is at most GDN_MAX_PAGE_ROWS.  status[i] is 0 where
