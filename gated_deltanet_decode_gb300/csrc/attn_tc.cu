@@ -47,11 +47,7 @@
 // O is rescaled only when a row's maximum has grown by over 2^8 since the
 // value in use (kLazy): weights then stay below 2^8 and sums in fp32 lose
 // nothing.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <atomic>
-#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -59,11 +55,11 @@
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
 #include "gdn_ptx.cuh"
+#include "tc_ops.cuh"
 
 namespace gdn {
 namespace {
 
-typedef __nv_bfloat16 bf16;
 
 constexpr int kQueue = 4;   // items in flight between the walking warp and the others
 constexpr int kMeta = 16;   // key tiles whose valid-row count is kept; over a ring's tiles
@@ -111,83 +107,11 @@ template <typename V> struct CtrlOf {
 };
 static_assert(sizeof(CtrlOf<Plain>) <= 3 * 1024 && sizeof(CtrlOf<Shared>) <= 3 * 1024, "control block");
 
-// ---- tensor core and copy wrappers ----
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-// MN-major, 128-byte swizzle: 64-element columns `lead` bytes apart, 8-key groups 1024 bytes apart
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead)
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-// D fp32, A and B bf16, M = 128, N = n; b_mn: B is MN-major
-__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn)
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-           ((uint32_t)(128 >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
-                 : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
-                 : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool elect() // one lane of a converged warp
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-    return ok != 0;
-}
-__device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void smem_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-                 "%4}], [%5];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(d)
-        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-    return *reinterpret_cast<float2 *>(&d);
-}
-// Two bf16: whether both are finite; with zeros in the place of those that are not.
-__device__ __forceinline__ bool finite2(uint32_t w)
-{
-    return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
-}
-__device__ __forceinline__ uint32_t drop2(uint32_t w)
-{
-    if ((w & 0x7f80u) == 0x7f80u)
-        w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u)
-        w &= 0xffffu;
-    return w;
 }
 // x[at] += y without indexing the registers
 __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
@@ -197,54 +121,6 @@ __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
         if (e == at)
             x[e] += y;
 }
-
-#define R4(r, i) "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3])
-#define R16(r, i) R4(r, i), R4(r, i + 4), R4(r, i + 8), R4(r, i + 12)
-#define I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
-#define I16(r, i) I4(r, i), I4(r, i + 4), I4(r, i + 8), I4(r, i + 12)
-// 128, 64, 32 consecutive columns of this thread's lane
-__device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[128])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
-                 "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
-                 "%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-                 "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,"
-                 "%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,"
-                 "%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,"
-                 "%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127"
-                 "}, [%128];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : R16(r, 0), R16(r, 16), R16(r, 32), R16(r, 48), R16(r, 64), R16(r, 80), R16(r, 96), R16(r, 112)
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[64])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-                 "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,"
-                 "%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : R16(r, 0), R16(r, 16), R16(r, 32), R16(r, 48)
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-                 "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : R16(r, 0), R16(r, 16)
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void tst(uint32_t a, const uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-                 I16(r, 0), I16(r, 16)
-                 : "memory");
-}
-__device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 template <int D, bool SH>
@@ -852,20 +728,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
 }
 
 // ---- host ----
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
 // a pool's K or V as [layers x pages x heads][page_size][d], boxes of 64 d x `box` keys
 bool encode_pages(CUtensorMap *m, void *base, const kv_page_pool &v, int box)
 {

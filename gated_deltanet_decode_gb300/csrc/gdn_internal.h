@@ -216,6 +216,10 @@ size_t prefill_chunked_workspace_bytes(int nseq, int total_tokens, int hv);
 // (those of up to a.most tokens).
 cudaError_t launch_linear_decode(const LinearArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_linear_serial(const LinearArgs &a, int dtype, cudaStream_t s);
+// Packed sequences in chunks (bf16): every one, the short ones by the serial kernel.
+bool linear_chunked_supported(int dk, int dv, int dtype);
+size_t linear_chunked_workspace_bytes(int nseq, int tokens, int hv, int dk, int dv);
+cudaError_t launch_linear_chunked(LinearArgs a, cudaStream_t s);
 
 // Attention layers over a page pool.
 cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table,
