@@ -16,13 +16,19 @@
 // some tens of its steps.
 //
 // linear_chunk_kernel: persistent, one CTA an SM.  Warp 0 brings Q, K and V by
-// tensor copies into four tiles that change roles (a chunk's V takes the tile
-// that was free, K the last Q's, Q the last V's), so that each copy runs a chunk
-// ahead as soon as its tile is read; warp 1 issues the products, warp 2 forms
-// the decays, warp 3 walks the items.  Eight warps compute, a thread a row and
-// half of its columns: Q K^T to weights (bf16, over the scores in tensor
-// memory), V times its weights, the outputs, and the state, which stays in their
-// registers.
+// tensor copies (two tiles of K and of V, one of Q, which is done with early),
+// warp 1 issues the products, warp 2 forms the decays and sends the outputs
+// off, warp 3 walks the items.  Of sixteen computing warps eight weigh V, 32
+// tokens at a time into two places in turn, and eight turn Q K^T into weights
+// (bf16, in the scores' place in tensor memory) and write the outputs, through
+// V's tile; the state is in the registers of all, a thread a row and a quarter
+// of its columns.
+//
+// Shared memory's 128 bytes a clock bound the chunk kernel's first forms: a 128 x
+// 128 x 16 product with both operands there takes all of them.  So weighted V
+// goes to tensor memory, transposed as it is read (a thread a column of V), and
+// only K comes from shared memory; the outputs' two parts are summed in one
+// place, the state's part being multiplied by its tokens' decays there.
 //
 // Precision.  The state is to be right to fp32, and its products' operands are
 // bf16: e^{G_C - G_j} v_j is cut into three bf16 values that make it up exactly
@@ -43,9 +49,11 @@ namespace gdn {
 namespace {
 
 constexpr int kC = 128;        // tokens a chunk
-constexpr int kThreads = 384;  // 4 warps of their own and 8 that compute
+constexpr int kComp = 16;      // warps that compute: a thread a row and a quarter of its columns
+constexpr int kThreads = 32 * (4 + kComp);
+constexpr int kRun = 32;       // tokens whose weighted V is written and taken at a time
 constexpr int kQueue = 4;      // items in flight between the walking warp and the others
-constexpr int kReaders = 11;   // warps 0, 1, 2 and the computing ones
+constexpr int kReaders = 3 + kComp; // warps 0, 1, 2 and the computing ones
 constexpr int kSerial = 32;    // tokens up to which a sequence is the serial kernel's
 constexpr int kSms = 152;
 
@@ -143,48 +151,70 @@ struct alignas(16) Decays {
     float rhi[4], rlo[4];     // R
     float all;                // e^{G_C}
 };
+// A number in two floats, and the sum of two such (Knuth's two-sum; fp64 takes
+// this part longer: 128 sums in doubles were 11,000 clocks, more than all else).
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    const float s = a.h + b.h, x = s - a.h, e = ((a.h - (s - x)) + (b.h - x)) + (a.l + b.l);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ Two shuffle(Two a, int from) { return {__shfl_sync(0xffffffffu, a.h, from), __shfl_sync(0xffffffffu, a.l, from)}; }
+__device__ __forceinline__ float minus(Two a, Two b) { return (a.h - b.h) + (a.l - b.l); }
+
+// Four tokens' log decays a lane, zero past the end
+__device__ __forceinline__ void load_decays(const LinearArgs &a, int tok, int n, int head, float (&x)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int j = 4 * (threadIdx.x & 31) + e;
+        x[e] = j < n ? a.log_decay[(long long)(tok + j) * a.decay_stride + head] : 0.f;
+    }
+}
 // FULL: all of it, else w and `all`
-template <bool FULL, typename Tab>
-__device__ __forceinline__ void form_decays(const LinearArgs &a, int tok, int n, int head, Tab &t)
+template <bool FULL, typename Tab> __device__ __forceinline__ void form_decays(const float (&in)[4], Tab &t)
 {
     const int lane = threadIdx.x & 31;
-    double g[4];
-    double sum = 0;
+    Two g[4], upto = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int j = 4 * lane + e;
-        float x = j < n ? a.log_decay[(long long)(tok + j) * a.decay_stride + head] : 0.f;
-        x = x > 0.f ? 0.f : x < -110.f ? -110.f : x; // (a NaN stays)
-        sum += (double)x * 1.4426950408889634;
-        g[e] = sum;
+        const float x = in[e] > 0.f ? 0.f : in[e] < -110.f ? -110.f : in[e]; // (a NaN stays)
+        constexpr float L = 1.44269504f, M = 1.92596303e-8f;                  // log2 e in two floats
+        const float h = x * L;
+        upto = upto + Two{h, fmaf(x, L, -h) + x * M};
+        g[e] = upto;
     }
-    double upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, upto, o);
+        const Two x = shuffle(upto, lane < o ? lane : lane - o);
         if (lane >= o)
-            upto += x;
+            upto = upto + x;
     }
-    const double before = upto - sum, all = __shfl_sync(0xffffffffu, upto, 31);
-    const double block = __shfl_sync(0xffffffffu, upto, lane | 7);
+    const Two all = shuffle(upto, 31), block = shuffle(upto, lane | 7);
+    Two before = shuffle(upto, lane == 0 ? 0 : lane - 1);
+    if (lane == 0)
+        before = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int j = 4 * lane + e;
-        const double G = before + g[e];
-        t.w[j] = exp2f((float)(all - G));
+        const Two G = before + g[e];
+        t.w[j] = exp2f(minus(all, G));
         if constexpr (FULL) {
-            t.hi[j] = (float)G;
-            t.lo[j] = (float)(G - (double)(float)G);
-            t.c[j] = exp2f((float)(block - G));
+            t.hi[j] = G.h;
+            t.lo[j] = G.l;
+            t.c[j] = exp2f(minus(block, G));
         }
     }
     if constexpr (FULL)
         if ((lane & 7) == 7) {
-            t.rhi[lane >> 3] = (float)block;
-            t.rlo[lane >> 3] = (float)(block - (double)(float)block);
+            t.rhi[lane >> 3] = block.h;
+            t.rlo[lane >> 3] = block.l;
         }
     if (lane == 0)
-        t.all = exp2f((float)all);
+        t.all = exp2f(all.h + all.l);
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -193,40 +223,53 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Whether one of eight bf16 is not finite
-__device__ __forceinline__ bool odd8(uint4 z)
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y)
 {
-    const uint32_t m = 0x7f807f80u, c = 0x00800080u;
-    return ((((z.x & m) + c) | ((z.y & m) + c) | ((z.z & m) + c) | ((z.w & m) + c)) & 0x80008000u) != 0;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 // Two floats, each cut into three bf16 values that make it up: heads, middles, tails as pairs.
-__device__ __forceinline__ void cut3(float x, float y, uint32_t &h, uint32_t &m, uint32_t &l)
+__device__ __forceinline__ void cut3(float2 x, uint32_t &h, uint32_t &m, uint32_t &l)
 {
-    const uint32_t xh = __float_as_uint(x), yh = __float_as_uint(y);
-    h = __byte_perm(xh, yh, 0x7632);
-    const float x1 = x - __uint_as_float(xh & 0xffff0000u), y1 = y - __uint_as_float(yh & 0xffff0000u);
-    const uint32_t xm = __float_as_uint(x1), ym = __float_as_uint(y1);
-    m = __byte_perm(xm, ym, 0x7632);
-    const float x2 = x1 - __uint_as_float(xm & 0xffff0000u), y2 = y1 - __uint_as_float(ym & 0xffff0000u);
-    l = __byte_perm(__float_as_uint(x2), __float_as_uint(y2), 0x7632);
+    auto rest = [](float2 v, uint32_t &pair) { // takes off the upper halves
+        const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+        pair = __byte_perm(a, b, 0x7632);
+        return fma2(make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)), make_float2(-1.f, -1.f), v);
+    };
+    const float2 y = rest(x, h), z = rest(y, m);
+    l = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
 }
-// 16 bytes of V times a weight, cut in three
-__device__ __forceinline__ void weigh(uint4 z, float w, unsigned char *to, int term)
+// Sixteen tokens of a column of V (a tile's byte `at`: its column, its first token) times their weights, cut in three, to
+// tensor memory, eight columns at `to` and every `term` on; a token's weight in `w`.  x gets V's values, for a look at them.
+__device__ __forceinline__ void read_column(const unsigned char *smem, uint32_t at, float (&x)[16])
 {
-    uint4 h, m, l;
-    const uint32_t in[4] = {z.x, z.y, z.z, z.w};
-    uint32_t o[3][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 x = mul2(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), make_float2(w, w));
-        cut3(x.x, x.y, o[0][e], o[1][e], o[2][e]);
+    for (int e = 0; e < 16; ++e) // (16-byte pieces of a row lie at their number ^ the row's)
+        x[e] = __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short *>(smem + (at ^ ((e & 7) << 4)) + e * 128) << 16);
+}
+__device__ __forceinline__ void weigh_column(const float (&x)[16], const float *w, uint32_t to, int term)
+{
+    uint32_t h[8], m[8], l[8];
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(w + e);
+        cut3(mul2(make_float2(x[e], x[e + 1]), make_float2(f.x, f.y)), h[e / 2], m[e / 2], l[e / 2]);
+        cut3(mul2(make_float2(x[e + 2], x[e + 3]), make_float2(f.z, f.w)), h[e / 2 + 1], m[e / 2 + 1], l[e / 2 + 1]);
     }
-    h = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-    m = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-    l = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
-    *reinterpret_cast<uint4 *>(to) = h;
-    *reinterpret_cast<uint4 *>(to + term) = m;
-    *reinterpret_cast<uint4 *>(to + 2 * term) = l;
+    tst(to, h);
+    tst(to + term, m);
+    tst(to + 2 * term, l);
+}
+// What of a column is not finite becomes zero in V's tile (and the values stay as they are); the first such token.
+__device__ __noinline__ int clear_column(unsigned char *smem, uint32_t at, int tok)
+{
+    int first = kC;
+    for (int e = 15; e >= 0; --e) {
+        unsigned short *const v = reinterpret_cast<unsigned short *>(smem + (at ^ ((e & 7) << 4)) + e * 128);
+        if ((*v & 0x7f80) == 0x7f80)
+            *v = 0, first = tok + e;
+    }
+    return first;
 }
 
 template <int DK, int DV> struct CGeo {
@@ -234,17 +277,16 @@ template <int DK, int DV> struct CGeo {
     static constexpr int TILE = kC * D * 2;           // a Q, K or V tile, as 64-column blocks of kC rows
     static constexpr int BLOCK = kC * 128;            // one such block
     static constexpr int KBYTES = kC * DK * 2, VBYTES = kC * DV * 2;
-    static constexpr int TERM = 64 * DV * 2;          // a third of weighted V for half of a chunk
-    static constexpr int WBYTES = (DV == 64 ? 4 : 3) * TERM; // (products take 128 rows of it: with dv = 64 the next term's, unused)
     static constexpr int SBYTES = DV * DK * 2;        // the state in bf16
+    static constexpr int WK = DK / 4;                 // a thread's columns of the state
 };
 
 // What both kernels wait for each other with.
 struct Bars {
     unsigned long long ifull[kQueue], iempty[kQueue];
     unsigned long long gfull[2], gempty[2]; // decays
-    unsigned long long full[4], empty[4];   // tiles
-    unsigned long long wready[2], wdone[2]; // halves of weighted V: written; read by their products
+    unsigned long long full[6], empty[6];   // tiles
+    unsigned long long wready[2], wdone[2]; // places of weighted V: written; read by their products
     unsigned long long drain;
 };
 
@@ -258,7 +300,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
 // ---- the outputs, and the states at the sequences' ends ----
 template <int DK, int DV> struct ChunkCtrl {
     Bars b;
-    unsigned long long qk, pready, odone, dsdone, sready;
+    unsigned long long qk, qs, pready, odone, ofree, dsdone, sready, vseen;
     LItem item[kQueue];
     Decays tab[2];
     int badfrom[3][kC]; // by chunk: first token with a value that is not finite, by column
@@ -269,15 +311,15 @@ template <int DK, int DV> struct ChunkCtrl {
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const ChunkArgs p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap)
+                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap)
 {
     typedef CGeo<DK, DV> G;
     typedef ChunkCtrl<DK, DV> Ctrl;
-    constexpr int SAT = 4 * G::TILE, WAT = SAT + G::SBYTES, CAT = WAT + G::WBYTES;
+    constexpr int SAT = 5 * G::TILE, CAT = SAT + G::SBYTES;
     static_assert(CAT % 1024 == 0 && CAT + sizeof(Ctrl) <= 232448, "shared memory");
-    constexpr uint32_t CS = 0, CO1 = 128, CO2 = 256, CD = 384; // tensor memory: scores and weights, the chunk's own part, the
-                                                               // state's part, the chunk's sum
-    constexpr int HK = DK / 2, HV = DV / 2;
+    // tensor memory: scores and weights, outputs, the chunk's sum, two places of weighted V (three terms of 16 columns)
+    constexpr uint32_t CS = 0, CO = 128, CD = 256, CW = 384, PLACE = 48;
+    constexpr int WK = G::WK, HV = DV / 2;
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctrl &ctl = *reinterpret_cast<Ctrl *>(smem + CAT);
     const uint32_t sbase = sm_addr(smem);
@@ -297,18 +339,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&omap) : "memory");
     }
     if (tid == 32) {
         for (int i = 0; i < kQueue; ++i)
             mbar_init(bar(ctl.b.ifull[i]), 1), mbar_init(bar(ctl.b.iempty[i]), kReaders);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(ctl.b.gfull[i]), 1), mbar_init(bar(ctl.b.gempty[i]), 8);
-            mbar_init(bar(ctl.b.wready[i]), 8), mbar_init(bar(ctl.b.wdone[i]), 1);
+            mbar_init(bar(ctl.b.gfull[i]), 1), mbar_init(bar(ctl.b.gempty[i]), kComp);
+            mbar_init(bar(ctl.b.wready[i]), kComp / 2), mbar_init(bar(ctl.b.wdone[i]), 1);
         }
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 5; ++i)
             mbar_init(bar(ctl.b.full[i]), 1), mbar_init(bar(ctl.b.empty[i]), 1);
-        mbar_init(bar(ctl.qk), 1), mbar_init(bar(ctl.pready), 8), mbar_init(bar(ctl.odone), 1);
-        mbar_init(bar(ctl.dsdone), 1), mbar_init(bar(ctl.sready), 8), mbar_init(bar(ctl.b.drain), 1);
+        mbar_init(bar(ctl.qk), 1), mbar_init(bar(ctl.qs), 1), mbar_init(bar(ctl.pready), kComp / 2);
+        mbar_init(bar(ctl.odone), 1), mbar_init(bar(ctl.ofree), kComp / 2), mbar_init(bar(ctl.vseen), kComp / 2);
+        mbar_init(bar(ctl.dsdone), 1), mbar_init(bar(ctl.sready), kComp), mbar_init(bar(ctl.b.drain), 1);
         ctl.dirty[0] = ctl.dirty[1] = ctl.dirty[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -345,18 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(ctl.b.iempty[slot]);
         return it.n > 0;
     };
-    // the tiles' roles in the current chunk, and the phases of their barriers, a bit a tile
-    int tq = 0, tk = 1, tv = 2, tf = 3;
-    auto turn = [&] {
-        const int q = tv, k = tq, v = tf, f = tk;
-        tq = q, tk = k, tv = v, tf = f;
-    };
-    uint32_t phase = 0;
-    auto wait_tile = [&](int t) {
-        const uint32_t parity = (phase >> t) & 1;
-        phase ^= 1u << t;
-        return wait(ctl.b.full[t], parity);
-    };
+    // tiles: V of even and odd chunks, K of even and odd chunks, Q
+    constexpr int TQ = 4;
     auto tile = [&](int t) { return sbase + t * G::TILE; };
     unsigned ch = 0; // chunks done
     LItem it;
@@ -381,111 +415,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 0) {
         // ---- Q, K and V
-        uint32_t loaded = 0; // tiles that were asked for at least once
-        auto load = [&](int t, const CUtensorMap *map, int blocks, int head, int tok, int bytes) {
-            if (!wait(ctl.b.empty[t], ((phase >> t) & 1) ^ 1))
+        auto load = [&](int t, uint32_t use, const CUtensorMap *map, int blocks, int head, int tok, int bytes) {
+            if (!wait(ctl.b.empty[t], (use & 1) ^ 1))
                 return false;
-            phase ^= 1u << t;
-            loaded |= 1u << t;
             if (lane == 0)
                 load_tile(tile(t), map, blocks, head, tok, bar(ctl.b.full[t]), bytes);
             __syncwarp();
             return true;
         };
+        unsigned asked[3] = {0, 0, 0}; // copies of V, K and Q
         for (int q = 0; take(q, it); ++q) {
             const int hk = it.head / (a.hv / a.hk);
-            for (int t = 0; t < it.n && alive; t += kC, turn()) {
-                if (!load(tv, &vmap, DV / 64, it.head, it.tok + t, G::VBYTES) || !load(tk, &kmap, DK / 64, hk, it.tok + t, G::KBYTES) ||
-                    !load(tq, &qmap, DK / 64, hk, it.tok + t, G::KBYTES))
+            for (int t = 0; t < it.n && alive; t += kC, ++ch) {
+                if (!load(2 + (ch & 1), ch >> 1, &kmap, DK / 64, hk, it.tok + t, G::KBYTES))
                     break;
+                ++asked[1];
+                if (!load(ch & 1, ch >> 1, &vmap, DV / 64, it.head, it.tok + t, G::VBYTES))
+                    break;
+                ++asked[0];
+                if (!load(TQ, ch, &qmap, DK / 64, hk, it.tok + t, G::KBYTES))
+                    break;
+                ++asked[2];
             }
             if (!alive)
                 break;
         }
         // the last copies land before the CTA leaves, whoever still waits for them
-        for (int t = 0; t < 4; ++t)
-            if (loaded >> t & 1)
-                mbar_wait(bar(ctl.b.full[t]), ((phase >> t) & 1) ^ 1);
+        for (int x = 0; x < 2; ++x)
+            for (unsigned c = asked[x] > 2 ? asked[x] - 2 : 0; c < asked[x]; ++c)
+                mbar_wait(bar(ctl.b.full[2 * x + (c & 1)]), (c >> 1) & 1);
+        if (asked[2])
+            mbar_wait(bar(ctl.b.full[TQ]), (asked[2] - 1) & 1);
     } else if (warp == 1) {
         // ---- the products, issued by one elected lane of the whole warp's walk
         const bool leader = elect();
-        auto scores = [&] { // Q K^T of the current tiles
-            if (!wait_tile(tq) || !wait_tile(tk))
+        auto sum = [&](int run) { // of a run's weighted V and K
+            if (!wait(ctl.b.wready[run & 1], run >> 1))
                 return false;
             after_sync();
             if (leader) {
-                const uint64_t qd = desc_k(tile(tq)), kd = desc_k(tile(tk));
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint64_t at = ((k >> 2) * G::BLOCK + (k & 3) * 32) >> 4;
-                    mma_ss(tmem + CS, qd + at, kd + at, idesc(kC, false), k > 0);
-                }
-                commit(bar(ctl.qk));
-            }
-            return true;
-        };
-        auto sum = [&](int half) { // of the chunk's weighted V and K, tokens 64 half ..
-            if (leader) {
-                const uint64_t kd = desc_mn(tile(tk) + half * 64 * 128, G::BLOCK);
-                const uint64_t wd = desc_mn(sbase + WAT, 64 * 128);
+                const uint64_t kd = desc_mn(tile(2 + (ch & 1)) + run * kRun * 128, G::BLOCK);
 #pragma unroll
                 for (int x = 2; x >= 0; --x) // the small terms first
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(tmem + CD, wd + ((x * G::TERM + k * 2048) >> 4), kd + (k * 2048 >> 4), idesc(DK, true, true),
-                               half > 0 || x < 2 || k > 0);
+                    for (int k = 0; k < kRun / 16; ++k)
+                        mma_ts(tmem + CD, tmem + CW + PLACE * (run & 1) + 16 * x + 8 * k, kd + (k * 2048 >> 4), idesc(DK, true),
+                               run > 0 || x < 2 || k > 0);
+                commit(bar(ctl.b.wdone[run & 1]));
             }
-        };
-        auto own = [&](int half) { // the weights times V
-            if (leader) {
-                const uint64_t vd = desc_mn(tile(tv) + half * 64 * 128, G::BLOCK);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ts(tmem + CO1, tmem + CS + 64 * half + 8 * k, vd + (k * 2048 >> 4), idesc(DV, true), half > 0 || k > 0);
-            }
+            return true;
         };
         for (int q = 0; take(q, it); ++q) {
             for (int t = 0; t < it.n && alive; t += kC, ++ch) {
-                const uint32_t par = ch & 1;
-                if (t == 0 && !scores())
+                const uint32_t par = ch & 1, par2 = (ch >> 1) & 1;
+                const int tv = ch & 1, tk = 2 + (ch & 1);
+                const uint64_t qd = desc_k(tile(TQ));
+                if (!wait(ctl.b.full[TQ], par) || !wait(ctl.b.full[tk], par2))
                     break;
-                if (!wait(ctl.sready, par))
+                after_sync();
+                if (leader) { // Q K^T
+                    const uint64_t kd = desc_k(tile(tk));
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k) {
+                        const uint64_t at = ((k >> 2) * G::BLOCK + (k & 3) * 32) >> 4;
+                        mma_ss(tmem + CS, qd + at, kd + at, idesc(kC, false), k > 0);
+                    }
+                    commit(bar(ctl.qk));
+                }
+                if (!wait(ctl.sready, par)) // the state is written, the sum before is read
+                    break;
+                if (!sum(0) || !sum(1) || !wait(ctl.ofree, par ^ 1)) // the outputs before are read
                     break;
                 after_sync();
                 if (leader) { // the state times q
-                    const uint64_t qd = desc_k(tile(tq)), sd = desc_k(sbase + SAT);
+                    const uint64_t sd = desc_k(sbase + SAT);
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k)
-                        mma_ss(tmem + CO2, qd + (((k >> 2) * G::BLOCK + (k & 3) * 32) >> 4),
+                        mma_ss(tmem + CO, qd + (((k >> 2) * G::BLOCK + (k & 3) * 32) >> 4),
                                sd + (((k >> 2) * DV * 128 + (k & 3) * 32) >> 4), idesc(DV, false), k > 0);
-                    commit(bar(ctl.b.empty[tq]));
+                    commit(bar(ctl.qs));
+                    commit(bar(ctl.b.empty[TQ]));
                 }
-                if (!wait(ctl.b.wready[0], par) || !wait_tile(tv))
+                if (!sum(2) || !sum(3))
                     break;
-                after_sync();
-                sum(0);
-                if (leader)
-                    commit(bar(ctl.b.wdone[0]));
-                if (!wait(ctl.pready, par))
-                    break;
-                after_sync();
-                own(0);
-                if (!wait(ctl.b.wready[1], par))
-                    break;
-                after_sync();
-                own(1);
-                if (leader) {
-                    commit(bar(ctl.odone));
-                    commit(bar(ctl.b.empty[tv]));
-                }
-                sum(1);
                 if (leader) {
                     commit(bar(ctl.dsdone));
                     commit(bar(ctl.b.empty[tk]));
                 }
-                turn();
-                if (t + kC < it.n && !scores())
+                if (!wait(ctl.pready, par) || !wait(ctl.b.full[tv], par2))
                     break;
+                after_sync();
+                if (leader) { // and the weights times V
+                    const uint64_t vd = desc_mn(tile(tv), G::BLOCK);
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_ts(tmem + CO, tmem + CS + 64 * (k >> 2) + 8 * (k & 3), vd + (k * 2048 >> 4), idesc(DV, true), true);
+                    commit(bar(ctl.odone));
+                }
             }
             if (!alive)
                 break;
@@ -497,223 +523,290 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait(bar(ctl.b.drain), 0);
     } else if (warp == 2) {
+        // ---- the decays, and whole chunks of outputs from V's tile; the tile is then free
+        int to[2] = {0, 0}, head[2] = {0, 0}; // of the last two chunks: first token (-1: no store), head
+        auto send = [&](unsigned c) {
+            const int t = c & 1, tok = t ? to[1] : to[0], h = t ? head[1] : head[0];
+            if (lane == 0) {
+                if (tok >= 0) {
+                    for (int x = 0; x < DV / 64; ++x)
+                        tma3_store(&omap, tile(t) + x * G::BLOCK, 64 * x, h, tok);
+                    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+                mbar_arrive(bar(ctl.b.empty[t]));
+            }
+            __syncwarp();
+        };
         for (int q = 0; take(q, it); ++q) {
+            float x[4], next[4];
+            load_decays(a, it.tok, it.n, it.head, next);
             for (int t = 0; t < it.n && alive; t += kC, ++ch) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = next[e];
+                load_decays(a, it.tok + t + kC, it.n - t - kC, it.head, next); // the next chunk's, under way meanwhile
                 if (!wait(ctl.b.gempty[ch & 1], ((ch >> 1) & 1) ^ 1))
                     break;
-                form_decays<true>(a, it.tok + t, min(kC, it.n - t), it.head, ctl.tab[ch & 1]);
+                if (ch >= 2)
+                    send(ch);
+                const int tok = it.n - t >= kC ? it.tok + t : -1;
+                if (ch & 1)
+                    to[1] = tok, head[1] = it.head;
+                else
+                    to[0] = tok, head[0] = it.head;
+                form_decays<true>(x, ctl.tab[ch & 1]);
                 arrive(ctl.b.gfull[ch & 1]);
             }
             if (!alive)
                 break;
         }
+        for (unsigned c = ch > 2 ? ch : 2; c < ch + 2 && alive; ++c) // the last two
+            if (wait(ctl.b.gempty[c & 1], ((c >> 1) & 1) ^ 1))
+                send(c);
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
-        const int w4 = warp & 3, hb = (warp - 4) >> 2, row = 32 * w4 + lane, ct = tid - 128; // 0 .. 255
+        const int w4 = warp & 3, quarter = (warp - 4) >> 2, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)w4 << 21;
-        const bool has = row < DV; // whether this thread keeps a part of the state: row `row`, columns hb HK ..
-        float s[HK];
+        const bool has = row < DV; // whether this thread keeps a part of the state: row `row`, columns quarter WK ..
+        float s[WK];
         auto write_state = [&] { // in bf16, for the products
             if (has) {
 #pragma unroll
-                for (int k = 0; k < HK; k += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(s[k + 2 * e], s[k + 2 * e + 1]);
-                        w[e] = *reinterpret_cast<const uint32_t *>(&h2);
-                    }
-                    const int col = hb * HK + k;
+                for (int k = 0; k < WK; k += 8) {
+                    const int col = quarter * WK + k;
                     *reinterpret_cast<uint4 *>(smem + SAT + (col >> 6) * DV * 128 + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                        make_uint4(bf16_pair(s[k], s[k + 1]), bf16_pair(s[k + 2], s[k + 3]), bf16_pair(s[k + 4], s[k + 5]),
+                                   bf16_pair(s[k + 6], s[k + 7]));
                 }
             }
             smem_to_async();
             before_sync();
             arrive(ctl.sready);
         };
-        for (int q = 0; take(q, it); ++q) {
-            const size_t head = (size_t)it.head * DV * DK, slot = (size_t)a.hv * DV * DK, mine = (size_t)row * DK + hb * HK;
-            {
-                const float *const from = it.from < 0 ? a.pool + slot * it.rs + head + mine : p.state + slot * it.from + head + mine;
+        auto begin = [&] { // an item: its state
+            const size_t slot = (size_t)a.hv * DV * DK, mine = (size_t)it.head * DV * DK + (size_t)row * DK + quarter * WK;
+            const float *const from = it.from < 0 ? a.pool + slot * it.rs + mine : p.state + slot * it.from + mine;
 #pragma unroll
-                for (int k = 0; k < HK; k += 4) {
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (has)
-                        x = *reinterpret_cast<const float4 *>(from + k);
-                    s[k] = x.x, s[k + 1] = x.y, s[k + 2] = x.z, s[k + 3] = x.w;
-                }
+            for (int k = 0; k < WK; k += 4) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (has)
+                    x = *reinterpret_cast<const float4 *>(from + k);
+                s[k] = x.x, s[k + 1] = x.y, s[k + 2] = x.z, s[k + 3] = x.w;
             }
             write_state();
-            for (int t = 0; t < it.n && alive; t += kC, ++ch, turn()) {
-                const uint32_t par = ch & 1;
-                const int n = min(kC, it.n - t), buf = ch % 3;
-                const Decays &tab = ctl.tab[ch & 1];
-                if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait_tile(tv))
-                    break;
-                // (the phase of K's barrier is followed, and waited for where its rows past the end are cleared)
-                const uint32_t kpar = (phase >> tk) & 1;
-                phase ^= 1u << tk;
-                phase ^= 1u << tq;
-                if (n < kC && !wait(ctl.b.full[tk], kpar))
-                    break;
-                // V times its weights, cut in three.  Rows past the end become zeros, in K and V too, and so do the elements of
-                // V that are not finite, which the weights of zero of earlier tokens would not hide: the outputs from such an
-                // element on are set at the end, and the sum takes it as it is.
-                auto weights = [&](int half) {
+        };
+        auto update = [&](int t) { // the state, with the sum of the chunk at token t of the item
+            const float all = ctl.tab[ch & 1].all;
+            if (!wait(ctl.dsdone, ch & 1))
+                return false;
+            after_sync();
+            {
+                uint32_t r[WK];
+                tld(tmem + lanes + CD + quarter * WK, r);
 #pragma unroll
-                    for (int i = 0; i < DV / 32; ++i) {
-                        const int x = i * 256 + ct, r = x / (DV / 8), c = x % (DV / 8), tok = half * 64 + r;
-                        const uint32_t swz = ((c & 7) ^ (r & 7)) << 4;
-                        uint4 *const at = reinterpret_cast<uint4 *>(smem + tv * G::TILE + (c >> 3) * G::BLOCK + tok * 128 + swz);
-                        uint4 z = *at;
-                        if (tok >= n) {
-                            z = make_uint4(0, 0, 0, 0);
-                            *at = z;
-                        } else if (odd8(z)) {
-                            uint4 y = z;
-                            y.x = drop2(z.x), y.y = drop2(z.y), y.z = drop2(z.z), y.w = drop2(z.w);
-                            *at = y;
-                            const uint32_t in[4] = {z.x, z.y, z.z, z.w};
+                for (int e = 0; e < WK; ++e)
+                    s[e] = fmaf(s[e], all, __uint_as_float(r[e]));
+            }
+            if (t + kC < it.n) {
+                write_state();
+            } else {
+                if (it.last && has) {
+                    float *const to = a.pool + (size_t)a.hv * DV * DK * it.ws + (size_t)it.head * DV * DK + (size_t)row * DK + quarter * WK;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if ((in[e >> 1] >> (16 * (e & 1)) & 0x7f80u) == 0x7f80u)
-                                    atomicMin(&ctl.badfrom[buf][8 * c + e], tok);
-                            *reinterpret_cast<volatile int *>(&ctl.dirty[buf]) = 1;
+                    for (int k = 0; k < WK; k += 4)
+                        *reinterpret_cast<float4 *>(to + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
+                }
+                before_sync();
+            }
+            return true;
+        };
+        if (warp < 4 + kComp / 2) {
+            // ---- V times its weights, a thread a column of V and half of a run's tokens.  What lies past the end becomes zero,
+            // in K and V too, and so do the elements of V that are not finite, which the weights of zero of earlier tokens
+            // would not hide: the outputs from such an element on are set when they are written, and the sum takes it as it is.
+            const int half = (warp - 4) >> 2, ct = tid - 128;
+            for (int q = 0; take(q, it); ++q) {
+                begin();
+                for (int t = 0; t < it.n && alive; t += kC, ++ch) {
+                    const int n = min(kC, it.n - t), buf = ch % 3;
+                    const Decays &tab = ctl.tab[ch & 1];
+                    if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait(ctl.b.full[ch & 1], (ch >> 1) & 1))
+                        break;
+                    if (n < kC && !wait(ctl.b.full[2 + (ch & 1)], (ch >> 1) & 1))
+                        break;
+#pragma unroll 1
+                    for (int run = 0; run < kC / kRun; ++run) {
+                        const int tok = run * kRun + 16 * half;
+                        const uint32_t at = (ch & 1) * G::TILE + (row >> 6) * G::BLOCK + tok * 128 + ((row & 63) >> 3 << 4) + (row & 7) * 2;
+                        float x[16];
+                        bool wrote = false;
+                        if (has) {
+                            read_column(smem, at, x);
+                            if (tok + 16 > n) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (tok + e >= n) {
+                                        x[e] = 0.f;
+                                        *reinterpret_cast<unsigned short *>(smem + (at ^ ((e & 7) << 4)) + e * 128) = 0;
+                                    }
+                                wrote = true;
+                            }
+                            float z = 0.f; // stays zero unless a value is not finite
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                z = fmaf(x[e], 0.f, z);
+                            if (z != 0.f) {
+                                atomicMin(&ctl.badfrom[buf][row], clear_column(smem, at, tok));
+                                *reinterpret_cast<volatile int *>(&ctl.dirty[buf]) = 1;
+                                wrote = true;
+                            }
                         }
-                        weigh(z, tab.w[tok], smem + WAT + (c >> 3) * 64 * 128 + r * 128 + swz, G::TERM);
+                        if (n < run * kRun + kRun) {
+                            for (int i = ct; i < kRun * (DK / 8); i += 16 * kComp) {
+                                const int r = run * kRun + i / (DK / 8), c = i % (DK / 8);
+                                if (r >= n)
+                                    *reinterpret_cast<uint4 *>(smem + (2 + (ch & 1)) * G::TILE + (c >> 3) * G::BLOCK + r * 128 + ((c & 7) << 4)) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
+                            wrote = true;
+                        }
+                        if (wrote)
+                            smem_to_async();
+                        __syncwarp(); // what follows is for whole warps
+                        if (!wait(ctl.b.wdone[run & 1], (run >> 1) ^ 1)) // the products before are done with the place
+                            break;
+                        after_sync();
+                        if (w4 < DV / 32)
+                            weigh_column(x, &tab.w[tok], tmem + lanes + CW + PLACE * (run & 1) + 8 * half, 16);
+                        tst_wait();
+                        before_sync();
+                        arrive(ctl.b.wready[run & 1]);
                     }
-                    if (n < half * 64 + 64)
-                        for (int x = ct; x < 64 * (DK / 8); x += 256) {
-                            const int tok = half * 64 + x / (DK / 8), c = x % (DK / 8);
-                            if (tok >= n)
-                                *reinterpret_cast<uint4 *>(smem + tk * G::TILE + (c >> 3) * G::BLOCK + tok * 128 + ((c & 7) << 4)) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                    smem_to_async();
-                    arrive(ctl.b.wready[half]);
-                };
-                weights(0);
-                // the weights of the chunk's tokens
-                if (!wait(ctl.qk, par))
+                    arrive(ctl.vseen);
+                    if (!alive || !update(t))
+                        break;
+                    // nobody looks at the marks of the chunk before any more: the products of this one waited for its outputs
+                    const int old = (ch + 2) % 3;
+                    if (half == 0)
+                        ctl.badfrom[old][ct] = kC;
+                    if (ct == 0)
+                        ctl.dirty[old] = 0;
+                    arrive(ctl.b.gempty[ch & 1]);
+                }
+                if (!alive)
                     break;
-                after_sync();
-                const float gh = tab.hi[row], gl = tab.lo[row];
-                {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int jb = 2 * hb + y; // a block of 32 tokens
+            }
+        } else {
+            // ---- the weights of the chunk's tokens, a thread a row and half of its columns, and the outputs
+            const int hb = (warp - 4 - kComp / 2) >> 2;
+            for (int q = 0; take(q, it); ++q) {
+                begin();
+                for (int t = 0; t < it.n && alive; t += kC, ++ch) {
+                    const uint32_t par = ch & 1;
+                    const int n = min(kC, it.n - t), buf = ch % 3;
+                    const Decays &tab = ctl.tab[ch & 1];
+                    if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait(ctl.qk, par))
+                        break;
+                    after_sync();
+                    const float gh = tab.hi[row], gl = tab.lo[row];
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y) { // blocks of 32 x 32, each into half of its scores' place
+                        const int jb = 2 * hb + y;
+                        uint32_t w[16];
                         if (jb > w4) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                w[16 * y + e] = 0;
-                            continue;
-                        }
-                        uint32_t r[32];
-                        tld(tmem + lanes + CS + 32 * jb, r);
-                        if (jb < w4) { // e^{G_i - G_j} = e^{G_i - R} e^{R - G_j}, neither above one
-                            const float f = ex2((gh - tab.rhi[jb]) + (gl - tab.rlo[jb]));
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 c = *reinterpret_cast<const float4 *>(&tab.c[32 * jb + e]);
-                                const float2 f2 = make_float2(f, f);
-                                const float2 x = mul2(mul2(make_float2(c.x, c.y), f2), make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
-                                const float2 z = mul2(mul2(make_float2(c.z, c.w), f2), make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])));
-                                const __nv_bfloat162 a2 = __floats2bfloat162_rn(x.x, x.y), b2 = __floats2bfloat162_rn(z.x, z.y);
-                                w[16 * y + e / 2] = *reinterpret_cast<const uint32_t *>(&a2);
-                                w[16 * y + e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&b2);
-                            }
+                                w[e] = 0;
                         } else {
+                            uint32_t r[32];
+                            tld(tmem + lanes + CS + 32 * jb, r);
+                            if (jb < w4) { // e^{G_i - G_j} = e^{G_i - R} e^{R - G_j}, neither above one
+                                const float f = ex2((gh - tab.rhi[jb]) + (gl - tab.rlo[jb]));
+                                const float2 f2 = make_float2(f, f);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const int j = 32 * jb + e;
-                                const float2 h2 = *reinterpret_cast<const float2 *>(&tab.hi[j]), l2 = *reinterpret_cast<const float2 *>(&tab.lo[j]);
-                                const float x = e <= lane ? __uint_as_float(r[e]) * ex2((gh - h2.x) + (gl - l2.x)) : 0.f;
-                                const float z = e + 1 <= lane ? __uint_as_float(r[e + 1]) * ex2((gh - h2.y) + (gl - l2.y)) : 0.f;
-                                const __nv_bfloat162 a2 = __floats2bfloat162_rn(x, z);
-                                w[16 * y + e / 2] = *reinterpret_cast<const uint32_t *>(&a2);
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 c = *reinterpret_cast<const float4 *>(&tab.c[32 * jb + e]);
+                                    const float2 x = mul2(mul2(make_float2(c.x, c.y), f2), make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+                                    const float2 z = mul2(mul2(make_float2(c.z, c.w), f2), make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])));
+                                    w[e / 2] = bf16_pair(x.x, x.y);
+                                    w[e / 2 + 1] = bf16_pair(z.x, z.y);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const int j = 32 * jb + e;
+                                    const float2 h2 = *reinterpret_cast<const float2 *>(&tab.hi[j]), l2 = *reinterpret_cast<const float2 *>(&tab.lo[j]);
+                                    const float x = e <= lane ? __uint_as_float(r[e]) * ex2((gh - h2.x) + (gl - l2.x)) : 0.f;
+                                    const float z = e + 1 <= lane ? __uint_as_float(r[e + 1]) * ex2((gh - h2.y) + (gl - l2.y)) : 0.f;
+                                    w[e / 2] = bf16_pair(x, z);
+                                }
                             }
                         }
+                        tst(tmem + lanes + CS + 64 * hb + 16 * y, w); // (columns that this warp alone reads, and has read)
                     }
-                    tst(tmem + lanes + CS + 64 * hb, w);
+                    // the state's part of the outputs times the decays, in its place
+                    const float f = ex2(gh + gl);
+                    if (!wait(ctl.qs, par))
+                        break;
+                    after_sync();
+#pragma unroll 1
+                    for (int k = 0; k < HV; k += 32) {
+                        uint32_t x[32];
+                        tld(tmem + lanes + CO + hb * HV + k, x);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                        tst(tmem + lanes + CO + hb * HV + k, x);
+                    }
                     tst_wait();
                     before_sync();
                     arrive(ctl.pready);
-                }
-                if (!wait(ctl.b.wdone[0], par))
-                    break;
-                weights(1);
-                // every warp has been over V: what was found of it is there for all, and nobody looks at the chunk's before
-                if (!wait(ctl.b.wready[1], par))
-                    break;
-                if (ct < kC) {
-                    const int old = (ch + 2) % 3;
-                    ctl.badfrom[old][ct] = kC;
-                    if (ct == 0)
-                        ctl.dirty[old] = 0;
-                }
-                // ---- outputs
-                if (!wait(ctl.odone, par))
-                    break;
-                after_sync();
-                const bool dirty = *reinterpret_cast<volatile int *>(&ctl.dirty[buf]) != 0;
-                {
-                    const float f = ex2(gh + gl) * a.scale;
-                    bf16 *const out = static_cast<bf16 *>(a.out) + ((size_t)(it.tok + t + row) * a.hv + it.head) * DV + hb * HV;
-#pragma unroll
+                    if (!update(t))
+                        break;
+                    if (!wait(ctl.vseen, par) || !wait(ctl.odone, par)) // all of V was looked at, and read
+                        break;
+                    after_sync();
+                    const bool dirty = *reinterpret_cast<volatile int *>(&ctl.dirty[buf]) != 0;
+                    unsigned char *const mine = smem + (ch & 1) * G::TILE + ((hb * HV) >> 6) * G::BLOCK; // over V, laid out alike
+                    auto piece = [&](int r, int i) {
+                        return reinterpret_cast<uint4 *>(mine + r * 128 + (((((hb * HV) & 63) / 8 + i) ^ (r & 7)) << 4));
+                    };
+#pragma unroll 1
                     for (int k = 0; k < HV; k += 32) {
-                        uint32_t x[32], y[32];
-                        tld(tmem + lanes + CO1 + hb * HV + k, x);
-                        tld(tmem + lanes + CO2 + hb * HV + k, y);
+                        uint32_t x[32];
+                        tld(tmem + lanes + CO + hb * HV + k, x);
                         if (dirty) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (ctl.badfrom[buf][hb * HV + k + e] <= row)
                                     x[e] = 0x7fffffffu;
                         }
-                        if (row < n) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint32_t w[4];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
 #pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const float o0 = fmaf(__uint_as_float(y[e + 2 * z]), f, __uint_as_float(x[e + 2 * z]) * a.scale);
-                                    const float o1 = fmaf(__uint_as_float(y[e + 2 * z + 1]), f, __uint_as_float(x[e + 2 * z + 1]) * a.scale);
-                                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(o0, o1);
-                                    w[z] = *reinterpret_cast<const uint32_t *>(&h2);
-                                }
-                                *reinterpret_cast<uint4 *>(out + k + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            for (int z = 0; z < 4; ++z)
+                                w[z] = bf16_pair(__uint_as_float(x[8 * i + 2 * z]) * a.scale, __uint_as_float(x[8 * i + 2 * z + 1]) * a.scale);
+                            *piece(row, k / 8 + i) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        __syncwarp();
                     }
+                    before_sync();
+                    arrive(ctl.ofree);                    if (n < kC) { // the last tokens of a sequence: the rows that there are, by this warp itself
+                        constexpr int P = HV / 8; // pieces of a row
+                        bf16 *const out = static_cast<bf16 *>(a.out) + ((size_t)(it.tok + t) * a.hv + it.head) * DV + hb * HV;
+                        for (int i = lane; i < 32 * P; i += 32) {
+                            const int r = 32 * w4 + i / P;
+                            if (r < n)
+                                *reinterpret_cast<uint4 *>(out + (size_t)r * a.hv * DV + 8 * (i % P)) = *piece(r, i % P);
+                        }
+                    }
+                    smem_to_async();
+                    arrive(ctl.b.gempty[ch & 1]);
                 }
-                // ---- the state
-                const float all = tab.all;
-                if (!wait(ctl.dsdone, par))
+                if (!alive)
                     break;
-                after_sync();
-#pragma unroll
-                for (int k = 0; k < HK; k += 32) {
-                    uint32_t r[32];
-                    tld(tmem + lanes + CD + hb * HK + k, r);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        s[k + e] = fmaf(s[k + e], all, __uint_as_float(r[e]));
-                }
-                arrive(ctl.b.gempty[ch & 1]);
-                if (t + kC < it.n) {
-                    write_state();
-                } else if (it.last && has) {
-                    float *const to = a.pool + slot * it.ws + head + mine;
-#pragma unroll
-                    for (int k = 0; k < HK; k += 4)
-                        *reinterpret_cast<float4 *>(to + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
-                }
-                before_sync();
             }
-            if (!alive)
-                break;
         }
     }
     before_sync();
@@ -724,13 +817,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- the segments' own sums ----
-// As above without Q: two tiles of V and two of K in turn, the halves of the
-// weighted V each in a place of its own, two chunks' sums in tensor memory, so
-// that a chunk's products run beside the next one's weights.
+// As above without Q, all sixteen warps weighing V: three tiles of V and three
+// of K in turn, a place for each half of the weighted V, two chunks' sums in
+// tensor memory, so that a chunk's products run beside the next one's weights.
 template <int DK, int DV> struct SumCtrl {
     Bars b;
+    unsigned long long added[2]; // a chunk's sum is done, by chunk parity
     LItem item[kQueue];
-    struct {
+    struct alignas(16) {
         float w[kC];
         float all;
     } tab[2];
@@ -743,9 +837,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     typedef CGeo<DK, DV> G;
     typedef SumCtrl<DK, DV> Ctrl;
-    constexpr int WAT = 4 * G::TILE, CAT = WAT + 2 * G::WBYTES;
+    constexpr int STAGES = 3, CAT = 2 * STAGES * G::TILE;
     static_assert(CAT % 1024 == 0 && CAT + sizeof(Ctrl) <= 232448, "shared memory");
-    constexpr int HK = DK / 2;
+    constexpr uint32_t CW = 256, PLACE = 96; // tensor memory: two sums of 128 columns, two places of three terms of 32
+    constexpr int WK = G::WK;
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctrl &ctl = *reinterpret_cast<Ctrl *>(smem + CAT);
     const uint32_t sbase = sm_addr(smem);
@@ -758,18 +853,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(256) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 32) {
         for (int i = 0; i < kQueue; ++i)
             mbar_init(bar(ctl.b.ifull[i]), 1), mbar_init(bar(ctl.b.iempty[i]), kReaders);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(ctl.b.gfull[i]), 1), mbar_init(bar(ctl.b.gempty[i]), 8);
-            mbar_init(bar(ctl.b.wready[i]), 8), mbar_init(bar(ctl.b.wdone[i]), 1);
+            mbar_init(bar(ctl.b.gfull[i]), 1), mbar_init(bar(ctl.b.gempty[i]), kComp);
+            mbar_init(bar(ctl.b.wready[i]), kComp / 2), mbar_init(bar(ctl.b.wdone[i]), 1);
+            mbar_init(bar(ctl.added[i]), 1);
         }
-        for (int i = 0; i < 4; ++i) // V's tiles are read by the computing warps, K's by the products
-            mbar_init(bar(ctl.b.full[i]), 1), mbar_init(bar(ctl.b.empty[i]), i < 2 ? 8 : 1);
+        for (int i = 0; i < 2 * STAGES; ++i) // V's tiles are read by the computing warps, K's by the products
+            mbar_init(bar(ctl.b.full[i]), 1), mbar_init(bar(ctl.b.empty[i]), i < STAGES ? kComp : 1);
         mbar_init(bar(ctl.b.drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -804,6 +900,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto tile = [&](int t) { return sbase + t * G::TILE; };
     unsigned ch = 0; // chunks done
+    int st = 0;      // the chunk's tiles: V in st, K in STAGES + st, with the phase `turn` of their barriers
+    uint32_t turn = 0;
+    auto advance = [&] {
+        ++ch;
+        if (++st == STAGES)
+            st = 0, turn ^= 1;
+    };
     LItem it;
 
     if (warp == 3) {
@@ -828,13 +931,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned asked = 0; // chunks whose copies were asked for
         for (int q = 0; take(q, it); ++q) {
             const int hk = it.head / (a.hv / a.hk);
-            for (int t = 0; t < it.n && alive; t += kC, ++ch) {
-                const uint32_t free = ((ch >> 1) & 1) ^ 1;
-                if (!wait(ctl.b.empty[ch & 1], free) || !wait(ctl.b.empty[2 + (ch & 1)], free))
+            for (int t = 0; t < it.n && alive; t += kC, advance()) {
+                if (!wait(ctl.b.empty[st], turn ^ 1) || !wait(ctl.b.empty[STAGES + st], turn ^ 1))
                     break;
                 if (lane == 0) {
-                    load_tile(tile(ch & 1), &vmap, DV / 64, it.head, it.tok + t, bar(ctl.b.full[ch & 1]), G::VBYTES);
-                    load_tile(tile(2 + (ch & 1)), &kmap, DK / 64, hk, it.tok + t, bar(ctl.b.full[2 + (ch & 1)]), G::KBYTES);
+                    load_tile(tile(st), &vmap, DV / 64, it.head, it.tok + t, bar(ctl.b.full[st]), G::VBYTES);
+                    load_tile(tile(STAGES + st), &kmap, DK / 64, hk, it.tok + t, bar(ctl.b.full[STAGES + st]), G::KBYTES);
                 }
                 __syncwarp();
                 ++asked;
@@ -843,35 +945,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
         }
         // the last copies land before the CTA leaves, whoever still waits for them
-        for (unsigned i = asked > 2 ? asked - 2 : 0; i < asked; ++i) {
-            mbar_wait(bar(ctl.b.full[i & 1]), (i >> 1) & 1);
-            mbar_wait(bar(ctl.b.full[2 + (i & 1)]), (i >> 1) & 1);
+        for (unsigned i = asked > STAGES ? asked - STAGES : 0; i < asked; ++i) {
+            mbar_wait(bar(ctl.b.full[i % STAGES]), (i / STAGES) & 1);
+            mbar_wait(bar(ctl.b.full[STAGES + i % STAGES]), (i / STAGES) & 1);
         }
     } else if (warp == 1) {
         const bool leader = elect();
         for (int q = 0; take(q, it); ++q) {
-            for (int t = 0; t < it.n && alive; t += kC, ++ch) {
-                const int kt = 2 + (ch & 1);
-                if (!wait(ctl.b.full[kt], (ch >> 1) & 1))
+            for (int t = 0; t < it.n && alive; t += kC, advance()) {
+                // (both halves: every warp has then read the sum that was in this chunk's place)
+                if (!wait(ctl.b.full[STAGES + st], turn) || !wait(ctl.b.wready[0], ch & 1) || !wait(ctl.b.wready[1], ch & 1))
                     break;
+                after_sync();
+                if (leader) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!wait(ctl.b.wready[half], ch & 1))
-                        break;
-                    after_sync();
-                    if (leader) {
-                        const uint64_t kd = desc_mn(tile(kt) + half * 64 * 128, G::BLOCK);
-                        const uint64_t wd = desc_mn(sbase + WAT + half * G::WBYTES, 64 * 128);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint64_t kd = desc_mn(tile(STAGES + st) + half * 64 * 128, G::BLOCK);
 #pragma unroll
                         for (int x = 2; x >= 0; --x) // the small terms first
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_ss(tmem + 128 * (ch & 1), wd + ((x * G::TERM + k * 2048) >> 4), kd + (k * 2048 >> 4),
-                                       idesc(DK, true, true), half > 0 || x < 2 || k > 0);
+                                mma_ts(tmem + 128 * (ch & 1), tmem + CW + PLACE * half + 32 * x + 8 * k, kd + (k * 2048 >> 4),
+                                       idesc(DK, true), half > 0 || x < 2 || k > 0);
                         commit(bar(ctl.b.wdone[half]));
-                        if (half)
-                            commit(bar(ctl.b.empty[kt]));
                     }
+                    commit(bar(ctl.added[ch & 1]));
+                    commit(bar(ctl.b.empty[STAGES + st]));
                 }
             }
             if (!alive)
@@ -885,73 +984,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(ctl.b.drain), 0);
     } else if (warp == 2) {
         for (int q = 0; take(q, it); ++q) {
+            float x[4], next[4];
+            load_decays(a, it.tok, it.n, it.head, next);
             for (int t = 0; t < it.n && alive; t += kC, ++ch) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = next[e];
+                load_decays(a, it.tok + t + kC, it.n - t - kC, it.head, next); // the next chunk's, under way meanwhile
                 if (!wait(ctl.b.gempty[ch & 1], ((ch >> 1) & 1) ^ 1))
                     break;
-                form_decays<false>(a, it.tok + t, min(kC, it.n - t), it.head, ctl.tab[ch & 1]);
+                form_decays<false>(x, ctl.tab[ch & 1]);
                 arrive(ctl.b.gfull[ch & 1]);
             }
             if (!alive)
                 break;
         }
     } else {
-        const int w4 = warp & 3, hb = (warp - 4) >> 2, row = 32 * w4 + lane, ct = tid - 128; // 0 .. 255
+        const int w4 = warp & 3, quarter = (warp - 4) >> 2, row = 32 * w4 + lane;
+        const bool has = row < DV;
+        const int tok = 32 * quarter, half = quarter >> 1; // this warp's tokens of a chunk, and their place
         const uint32_t lanes = (uint32_t)w4 << 21;
-        float s[HK];
+        float s[WK];
         auto add = [&](unsigned c, float all) { // the sum of chunk c, which is done
             after_sync();
+            uint32_t r[WK];
+            tld(tmem + lanes + 128 * (c & 1) + quarter * WK, r);
 #pragma unroll
-            for (int k = 0; k < HK; k += 32) {
-                uint32_t r[32];
-                tld(tmem + lanes + 128 * (c & 1) + hb * HK + k, r);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    s[k + e] = fmaf(s[k + e], all, __uint_as_float(r[e]));
-            }
+            for (int e = 0; e < WK; ++e)
+                s[e] = fmaf(s[e], all, __uint_as_float(r[e]));
             before_sync();
         };
         for (int q = 0; take(q, it); ++q) {
             float total = 1.f, last = 0.f;
 #pragma unroll
-            for (int k = 0; k < HK; ++k)
+            for (int k = 0; k < WK; ++k)
                 s[k] = 0.f;
-            for (int t = 0; t < it.n && alive; t += kC, ++ch) { // (whole chunks: a segment with another behind it)
-                if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait(ctl.b.full[ch & 1], (ch >> 1) & 1))
+            for (int t = 0; t < it.n && alive; t += kC, advance()) { // (whole chunks: a segment with another behind it)
+                if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait(ctl.b.full[st], turn))
                     break;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!wait(ctl.b.wdone[half], (ch & 1) ^ 1)) // the chunk before is done with the place
-                        break;
-#pragma unroll
-                    for (int i = 0; i < DV / 32; ++i) {
-                        const int x = i * 256 + ct, r = x / (DV / 8), c = x % (DV / 8), tok = half * 64 + r;
-                        const uint32_t swz = ((c & 7) ^ (r & 7)) << 4;
-                        const uint4 z = *reinterpret_cast<const uint4 *>(smem + (ch & 1) * G::TILE + (c >> 3) * G::BLOCK + tok * 128 + swz);
-                        weigh(z, ctl.tab[ch & 1].w[tok], smem + WAT + half * G::WBYTES + (c >> 3) * 64 * 128 + r * 128 + swz, G::TERM);
-                    }
-                    smem_to_async();
-                    arrive(ctl.b.wready[half]);
-                }
-                if (!alive)
+                const uint32_t at = st * G::TILE + (row >> 6) * G::BLOCK + ((row & 63) >> 3 << 4) + (row & 7) * 2;
+                float x[16];
+                if (has)
+                    read_column(smem, at + tok * 128, x);
+                if (!wait(ctl.b.wdone[half], (ch & 1) ^ 1)) // the chunk before is done with the place
                     break;
+                after_sync();
+                const uint32_t to = tmem + lanes + CW + PLACE * half + (tok & 63) / 2;
+                if (w4 < DV / 32)
+                    weigh_column(x, &ctl.tab[ch & 1].w[tok], to, 32);
+                if (has)
+                    read_column(smem, at + (tok + 16) * 128, x);
+                if (w4 < DV / 32)
+                    weigh_column(x, &ctl.tab[ch & 1].w[tok + 16], to + 8, 32);
+                tst_wait();
+                before_sync();
+                arrive(ctl.b.wready[half]);
                 const float all = ctl.tab[ch & 1].all;
-                arrive(ctl.b.empty[ch & 1]);
+                arrive(ctl.b.empty[st]);
                 arrive(ctl.b.gempty[ch & 1]);
-                if (t > 0)
+                if (t > 0) {
+                    if (!wait(ctl.added[(ch - 1) & 1], ((ch - 1) >> 1) & 1))
+                        break;
                     add(ch - 1, last);
+                }
                 last = all;
                 total *= all;
             }
-            if (!alive || !wait(ctl.b.wdone[1], (ch - 1) & 1))
+            if (!alive || !wait(ctl.added[(ch - 1) & 1], ((ch - 1) >> 1) & 1))
                 break;
             add(ch - 1, last);
-            if (row < DV) {
-                float *const to = p.state + ((size_t)it.at * a.hv + it.head) * DV * DK + (size_t)row * DK + hb * HK;
+            if (has) {
+                float *const to = p.state + ((size_t)it.at * a.hv + it.head) * DV * DK + (size_t)row * DK + quarter * WK;
 #pragma unroll
-                for (int k = 0; k < HK; k += 4)
+                for (int k = 0; k < WK; k += 4)
                     *reinterpret_cast<float4 *>(to + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
             }
-            if (ct == 0)
+            if (tid == 128)
                 p.decay[(size_t)it.at * a.hv + it.head] = total;
         }
     }
@@ -959,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // The state after each segment but a sequence's last, from the segments' sums,
@@ -1000,7 +1108,8 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkArgs p)
 
 // ---- host ----
 // Chunks a segment, from what the host knows (the lengths are on the device; sequences are taken as equal): the fewest
-// rounds of CTAs, in chunks, where a segment costs one more to begin, and forming the sums half a chunk's time.
+// rounds of CTAs, in chunks, where a segment costs one more to begin, and forming the sums half a chunk's time.  Uncut,
+// sequences of up to twice their mean length and of four chunks stay whole: a short piece too many is a round too many.
 int segment_chunks(int nseq, int tokens, int hv)
 {
     const int m = (int)(((long long)tokens + (long long)nseq * kC - 1) / ((long long)nseq * kC)); // chunks a sequence
@@ -1011,9 +1120,9 @@ int segment_chunks(int nseq, int tokens, int hv)
         auto rounds = [&](long long n) { return (double)((n * nseq * hv + kSms - 1) / kSms); };
         const double cost = rounds(segs) * (len + 1) + (segs > 1 ? rounds(segs - 1) * (0.5 * len + 1) + 3 : 0);
         if (cost < least)
-            least = cost, best = len;
+            least = cost, best = segs > 1 ? len : 2 * m;
     }
-    return best;
+    return best < 4 ? 4 : best;
 }
 // Whether a sequence can have several segments
 bool divided(int tokens, int seg) { return tokens > (long long)seg * kC; }
@@ -1034,8 +1143,8 @@ bool encode_tokens(CUtensorMap *m, const void *base, int d, int heads, int token
 template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
 {
     typedef CGeo<DK, DV> G;
-    constexpr int CHUNK = 4 * G::TILE + G::SBYTES + G::WBYTES + (int)sizeof(ChunkCtrl<DK, DV>);
-    constexpr int SUM = 4 * G::TILE + 2 * G::WBYTES + (int)sizeof(SumCtrl<DK, DV>);
+    constexpr int CHUNK = 5 * G::TILE + G::SBYTES + (int)sizeof(ChunkCtrl<DK, DV>);
+    constexpr int SUM = 6 * G::TILE + (int)sizeof(SumCtrl<DK, DV>);
     static std::atomic<unsigned long long> configured{0}; // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1050,9 +1159,10 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
             return e;
         configured.fetch_or(bit, std::memory_order_release);
     }
-    CUtensorMap qmap, kmap, vmap;
+    CUtensorMap qmap, kmap, vmap, omap;
     if (!encode_tokens(&qmap, a.q, DK, a.hk, a.total_tokens, a.q_stride) || !encode_tokens(&kmap, a.k, DK, a.hk, a.total_tokens, a.k_stride) ||
-        !encode_tokens(&vmap, a.v, DV, a.hv, a.total_tokens, a.v_stride))
+        !encode_tokens(&vmap, a.v, DV, a.hv, a.total_tokens, a.v_stride) ||
+        !encode_tokens(&omap, a.out, DV, a.hv, a.total_tokens, (long long)a.hv * DV))
         return cudaErrorInvalidValue;
     ChunkArgs p;
     p.a = a;
@@ -1069,7 +1179,7 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
         if (e != cudaSuccess)
             return e;
     }
-    return launch_pdl(linear_chunk_kernel<DK, DV>, grid, dim3(kThreads), (size_t)CHUNK, s, p, qmap, kmap, vmap);
+    return launch_pdl(linear_chunk_kernel<DK, DV>, grid, dim3(kThreads), (size_t)CHUNK, s, p, qmap, kmap, vmap, omap);
 }
 
 } // namespace

@@ -68,6 +68,13 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ void tma3_store(const CUtensorMap *map, uint32_t src, int x, int y, int z) // into the thread's group
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
     unsigned long long d;
@@ -93,7 +100,7 @@ __device__ __forceinline__ uint32_t drop2(uint32_t w)
 #define R16(r, i) R4(r, i), R4(r, i + 4), R4(r, i + 8), R4(r, i + 12)
 #define I4(r, i) "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3])
 #define I16(r, i) I4(r, i), I4(r, i + 4), I4(r, i + 8), I4(r, i + 12)
-// 128, 64, 32 consecutive columns of this thread's lane
+// 128, 64, 32, 16 consecutive columns of this thread's lane
 __device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[128])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
@@ -126,6 +133,24 @@ __device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[32])
                  "tcgen05.wait::ld.sync.aligned;"
                  : R16(r, 0), R16(r, 16)
                  : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R16(r, 0)
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void tst(uint32_t a, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), I4(r, 0), I4(r, 4) : "memory");
+}
+__device__ __forceinline__ void tst(uint32_t a, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+                 I16(r, 0)
                  : "memory");
 }
 __device__ __forceinline__ void tst(uint32_t a, const uint32_t (&r)[32])
