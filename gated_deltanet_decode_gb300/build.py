@@ -19,10 +19,10 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgdn_decode.so")
 SOURCES = ["gdn_api.cu", "gdn_stream.cu", "gdn_conv.cu", "gdn_prefill.cu", "gdn_chunked.cu", "gdn_chunked_tc.cu",
            "kv_api.cu", "kv_pages.cu", "attn_prologue.cu", "attn_tc.cu", "attn_f32.cu",
-           "linear_api.cu", "linear_attn.cu", "linear_attn_tc.cu"]
+           "linear_api.cu", "linear_attn.cu", "linear_attn_tc.cu", "linear_attn_f32.cu"]
 HEADERS = [os.path.join(CSRC, "gdn_device.cuh"), os.path.join(CSRC, "gdn_ptx.cuh"),
            os.path.join(CSRC, "gdn_chunk_common.cuh"), os.path.join(CSRC, "attn_plan.cuh"),
-           os.path.join(CSRC, "tc_ops.cuh"),
+           os.path.join(CSRC, "tc_ops.cuh"), os.path.join(CSRC, "linear_plan.cuh"),
            os.path.join(CSRC, "gdn_internal.h"),
            os.path.join(ROOT, "include", "gdn_decode.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

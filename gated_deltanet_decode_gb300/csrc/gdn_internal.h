@@ -216,10 +216,12 @@ size_t prefill_chunked_workspace_bytes(int nseq, int total_tokens, int hv);
 // (those of up to a.most tokens).
 cudaError_t launch_linear_decode(const LinearArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_linear_serial(const LinearArgs &a, int dtype, cudaStream_t s);
-// Packed sequences in chunks (bf16): every one, the short ones by the serial kernel.
-bool linear_chunked_supported(int dk, int dv, int dtype);
-size_t linear_chunked_workspace_bytes(int nseq, int tokens, int hv, int dk, int dv);
-cudaError_t launch_linear_chunked(LinearArgs a, cudaStream_t s);
+// Packed sequences: the short ones by the serial kernel, the others in chunks, bf16 with dk and dv 64 or 128 on the
+// tensor cores (launch_linear_chunked), the rest in fp32 FMAs.
+size_t linear_prefill_workspace_bytes(const LinearArgs &a, int dtype);
+cudaError_t launch_linear_prefill(LinearArgs a, int dtype, cudaStream_t s);
+size_t linear_chunked_workspace_bytes(const LinearArgs &a);
+cudaError_t launch_linear_chunked(const LinearArgs &a, cudaStream_t s);
 
 // Attention layers over a page pool.
 cudaError_t launch_rope_table(const double *inv_freq, int rot, int positions, double mscale, float *table,

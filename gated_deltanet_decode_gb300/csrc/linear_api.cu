@@ -1,5 +1,5 @@
 // C ABI of linear attention with a decay for each head: argument checks.  The
-// kernels are in linear_attn.cu and linear_attn_tc.cu.
+// kernels are in linear_attn.cu, linear_attn_tc.cu and linear_attn_f32.cu.
 #include <cmath>
 
 #include "gdn_device.cuh"
@@ -89,9 +89,12 @@ int linear_attention_decode(const void *q, int64_t q_stride, const void *k, int6
 
 size_t linear_attention_prefill_workspace_bytes(const gdn_pool *pool, int nseq, int total_tokens, int dtype)
 {
-    if (!pool || nseq < 1 || total_tokens < 1 || !gdn::linear_chunked_supported(pool->dims.dk, pool->dims.dv, dtype))
+    if (!pool || nseq < 1 || total_tokens < 1 || (dtype != GDN_F32 && dtype != GDN_BF16))
         return 0;
-    return gdn::linear_chunked_workspace_bytes(nseq, total_tokens, pool->dims.hv, pool->dims.dk, pool->dims.dv);
+    gdn::LinearArgs a = {};
+    a.rows = nseq, a.total_tokens = total_tokens;
+    a.hk = pool->dims.hk, a.hv = pool->dims.hv, a.dk = pool->dims.dk, a.dv = pool->dims.dv;
+    return gdn::linear_prefill_workspace_bytes(a, dtype);
 }
 
 int linear_attention_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -118,11 +121,7 @@ int linear_attention_prefill(const void *q, int64_t q_stride, const void *k, int
     if ((rc = api_error_word(&a.err)))
         return rc;
     a.cu_seqlens = cu_seqlens, a.work = workspace;
-    a.most = 0x7fffffff;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = total_tokens > 0 && gdn::linear_chunked_supported(a.dk, a.dv, dtype)
-                              ? gdn::launch_linear_chunked(a, s)
-                              : gdn::launch_linear_serial(a, dtype, s);
+    const cudaError_t e = gdn::launch_linear_prefill(a, dtype, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "linear_attention_prefill launch");
 }
 

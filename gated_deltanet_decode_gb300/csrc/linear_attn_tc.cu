@@ -7,13 +7,8 @@
 // which regroups the recurrence token after token (linear_attn.cu); as a decay
 // is a number, the sums over j of different chunks do not depend on each other.
 //
-// Work.  A sequence's chunks are cut into segments of L, so that few sequences
-// still fill the GPU.  linear_sum_kernel forms every segment's own sum (all but
-// a sequence's last), linear_scan_kernel turns them into the states after each
-// segment, and linear_chunk_kernel goes through the segments, each from its
-// state.  Sequences of one segment need only the last.  Sequences of up to
-// kSerial tokens are the serial kernel's: a chunk's products take the time of
-// some tens of its steps.
+// Work: as linear_plan.cuh divides it, by linear_sum_kernel, linear_scan_kernel
+// and linear_chunk_kernel.
 //
 // linear_chunk_kernel: persistent, one CTA an SM.  Warp 0 brings Q, K and V by
 // tensor copies (two tiles of K and of V, one of Q, which is done with early),
@@ -43,6 +38,7 @@
 
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
+#include "linear_plan.cuh"
 #include "tc_ops.cuh"
 
 namespace gdn {
@@ -54,91 +50,6 @@ constexpr int kThreads = 32 * (4 + kComp);
 constexpr int kRun = 32;       // tokens whose weighted V is written and taken at a time
 constexpr int kQueue = 4;      // items in flight between the walking warp and the others
 constexpr int kReaders = 3 + kComp; // warps 0, 1, 2 and the computing ones
-constexpr int kSerial = 32;    // tokens up to which a sequence is the serial kernel's
-constexpr int kSms = 152;
-
-struct ChunkArgs {
-    LinearArgs a;
-    int seg;      // chunks a segment
-    float *state; // [segments][hv][dv][dk]: a segment's sum, then the state after it (a sequence's last: the state before all)
-    float *decay; // [segments][hv]: the segment's decay
-};
-
-// A segment of a sequence and head.
-struct LItem {
-    int tok, n, head; // first token, tokens (0: no more items), value head
-    int rs, ws;       // the sequence's slots
-    int at, from;     // places in the workspace: the segment's, and of the state before it (-1: read slot)
-    int last;         // of its sequence
-};
-
-// A sequence's segments: none where it is the serial kernel's, padding or bad.
-__device__ __forceinline__ int segments(const ChunkArgs &p, int r, int &b, int &n, int &rs, int &ws)
-{
-    b = p.a.cu_seqlens[r];
-    const int e = p.a.cu_seqlens[r + 1];
-    rs = p.a.read_slot[r], ws = p.a.write_slot ? p.a.write_slot[r] : rs;
-    n = 0;
-    if (classify_seq(rs, ws, p.a.write_slot == nullptr, nullptr, b, e, p.a.total_tokens, p.a.num_slots) != 1)
-        return 0;
-    n = e - b;
-    const int span = kC * p.seg;
-    return n > kSerial ? n / span + (n % span != 0) : 0;
-}
-// The workspace's places of a sequence's segments begin at its first token's
-// place over a segment's length and one a sequence before it, so no two meet.
-__device__ __forceinline__ int first_place(const ChunkArgs &p, int b, int r) { return b / (kC * p.seg) + r; }
-inline long long places(int nseq, int tokens, int seg) { return (long long)tokens / ((long long)kC * seg) + nseq + 1; }
-
-// The items of a CTA: number blockIdx.x and every gridDim.x-th on, heads of a
-// segment next to each other.  By one warp; SUM leaves out the last segments.
-template <bool SUM> struct ItemWalk {
-    const ChunkArgs &p;
-    const int lane;
-    long long i;     // the next item
-    long long done;  // items of the sequences before `row`
-    int row;         // the window's first sequence
-    int b, n, rs, ws, segs;
-    __device__ explicit ItemWalk(const ChunkArgs &p_) : p(p_), lane(threadIdx.x & 31), i(blockIdx.x), done(0), row(0) { look(); }
-    __device__ void look()
-    {
-        segs = 0;
-        if (row + lane < p.a.rows)
-            segs = segments(p, row + lane, b, n, rs, ws);
-        if (SUM && segs > 0)
-            --segs;
-    }
-    __device__ bool next(LItem &it)
-    {
-        for (; row < p.a.rows; row += 32, look()) {
-            int upto = segs;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o)
-                    upto += x;
-            }
-            const long long all = (long long)__shfl_sync(0xffffffffu, upto, 31) * p.a.hv;
-            if (i >= done + all) {
-                done += all;
-                continue;
-            }
-            const int s = (int)((i - done) / p.a.hv), h = (int)((i - done) - (long long)s * p.a.hv);
-            const int who = __ffs(__ballot_sync(0xffffffffu, upto > s)) - 1;
-            const int seg = s - __shfl_sync(0xffffffffu, upto - segs, who), span = kC * p.seg;
-            const int wb = __shfl_sync(0xffffffffu, b, who), wn = __shfl_sync(0xffffffffu, n, who);
-            const int count = __shfl_sync(0xffffffffu, segs, who) + (SUM ? 1 : 0);
-            it.tok = wb + seg * span, it.n = min(span, wn - seg * span), it.head = h;
-            it.rs = __shfl_sync(0xffffffffu, rs, who), it.ws = __shfl_sync(0xffffffffu, ws, who);
-            it.at = first_place(p, wb, row + who) + seg;
-            it.from = seg > 0 ? it.at - 1 : count > 1 ? it.at + count - 1 : -1;
-            it.last = seg == count - 1;
-            i += gridDim.x;
-            return true;
-        }
-        return false;
-    }
-};
 
 // Decays of a chunk, by warp 2.  In units of log2: -G is up to 2^15 for decays
 // that forget everything (a token's is cut off at e^-110, below half of the
@@ -151,20 +62,6 @@ struct alignas(16) Decays {
     float rhi[4], rlo[4];     // R
     float all;                // e^{G_C}
 };
-// A number in two floats, and the sum of two such (Knuth's two-sum; fp64 takes
-// this part longer: 128 sums in doubles were 11,000 clocks, more than all else).
-struct Two {
-    float h, l;
-};
-__device__ __forceinline__ Two operator+(Two a, Two b)
-{
-    const float s = a.h + b.h, x = s - a.h, e = ((a.h - (s - x)) + (b.h - x)) + (a.l + b.l);
-    const float h = s + e;
-    return {h, e - (h - s)};
-}
-__device__ __forceinline__ Two shuffle(Two a, int from) { return {__shfl_sync(0xffffffffu, a.h, from), __shfl_sync(0xffffffffu, a.l, from)}; }
-__device__ __forceinline__ float minus(Two a, Two b) { return (a.h - b.h) + (a.l - b.l); }
-
 // Four tokens' log decays a lane, zero past the end
 __device__ __forceinline__ void load_decays(const LinearArgs &a, int tok, int n, int head, float (&x)[4])
 {
@@ -182,9 +79,7 @@ template <bool FULL, typename Tab> __device__ __forceinline__ void form_decays(c
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float x = in[e] > 0.f ? 0.f : in[e] < -110.f ? -110.f : in[e]; // (a NaN stays)
-        constexpr float L = 1.44269504f, M = 1.92596303e-8f;                  // log2 e in two floats
-        const float h = x * L;
-        upto = upto + Two{h, fmaf(x, L, -h) + x * M};
+        upto = upto + log2_units(x);
         g[e] = upto;
     }
 #pragma unroll
@@ -217,12 +112,6 @@ template <bool FULL, typename Tab> __device__ __forceinline__ void form_decays(c
         t.all = exp2f(all.h + all.l);
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t bf16_pair(float x, float y)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -1070,42 +959,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// The state after each segment but a sequence's last, from the segments' sums,
-// in their places: a thread four floats of a (sequence, head).
-__global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkArgs p)
-{
-    wait_prior_grid();
-    const int floats = p.a.dv * p.a.dk, parts = floats / 1024;
-    const int part = blockIdx.x % parts, x = blockIdx.x / parts, h = x % p.a.hv, r = x / p.a.hv;
-    int b, n, rs, ws;
-    const int segs = segments(p, r, b, n, rs, ws);
-    if (segs < 2)
-        return;
-    const size_t slot = (size_t)p.a.hv * floats, mine = (size_t)h * floats + part * 1024 + 4 * threadIdx.x;
-    const size_t place = first_place(p, b, r);
-    float4 s = *reinterpret_cast<const float4 *>(p.a.pool + slot * rs + mine);
-    // (the first segment takes its state from the last one's place: in place, the slot is written by the last segment)
-    *reinterpret_cast<float4 *>(p.state + slot * (place + segs - 1) + mine) = s;
-    constexpr int U = 4; // segments under way
-    for (int i0 = 0; i0 < segs - 1; i0 += U) {
-        float4 y[U];
-        float f[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < segs - 1) {
-                y[u] = *reinterpret_cast<const float4 *>(p.state + slot * (place + i0 + u) + mine);
-                f[u] = p.decay[(place + i0 + u) * p.a.hv + h];
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < segs - 1) {
-                s.x = fmaf(s.x, f[u], y[u].x), s.y = fmaf(s.y, f[u], y[u].y);
-                s.z = fmaf(s.z, f[u], y[u].z), s.w = fmaf(s.w, f[u], y[u].w);
-                *reinterpret_cast<float4 *>(p.state + slot * (place + i0 + u) + mine) = s;
-            }
-    }
-}
-
 // ---- host ----
 // Chunks a segment, from what the host knows (the lengths are on the device; sequences are taken as equal): the fewest
 // rounds of CTAs, in chunks, where a segment costs one more to begin, and forming the sums half a chunk's time.  Uncut,
@@ -1124,9 +977,6 @@ int segment_chunks(int nseq, int tokens, int hv)
     }
     return best < 4 ? 4 : best;
 }
-// Whether a sequence can have several segments
-bool divided(int tokens, int seg) { return tokens > (long long)seg * kC; }
-
 // [tokens][heads][d] bf16, boxes of 64 d of one head x kC tokens
 bool encode_tokens(CUtensorMap *m, const void *base, int d, int heads, int tokens, long long stride)
 {
@@ -1166,16 +1016,16 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     ChunkArgs p;
     p.a = a;
-    p.seg = segment_chunks(a.rows, a.total_tokens, a.hv);
-    const long long most = places(a.rows, a.total_tokens, p.seg) * a.hv; // items
-    p.state = static_cast<float *>(a.work);
-    p.decay = p.state + (size_t)most * DV * DK;
+    p.span = kC * segment_chunks(a.rows, a.total_tokens, a.hv);
+    p.least = kSerial;
+    p.heads = a.hv;
+    chunk_layout(p);
+    const long long most = places(a.rows, a.total_tokens, p.span) * a.hv; // items
     const dim3 grid((unsigned)(most < kSms ? most : kSms));
-    if (divided(a.total_tokens, p.seg)) {
+    if (a.total_tokens > p.span) { // a sequence can have several segments
         e = launch_pdl(linear_sum_kernel<DK, DV>, grid, dim3(kThreads), (size_t)SUM, s, p, kmap, vmap);
-        if (e != cudaSuccess)
-            return e;
-        e = launch_pdl(linear_scan_kernel, dim3((unsigned)a.rows * a.hv * (DV * DK / 1024)), dim3(256), 0, s, p);
+        if (e == cudaSuccess)
+            e = launch_scan(p, s);
         if (e != cudaSuccess)
             return e;
     }
@@ -1184,24 +1034,14 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
 
 } // namespace
 
-bool linear_chunked_supported(int dk, int dv, int dtype)
+size_t linear_chunked_workspace_bytes(const LinearArgs &a)
 {
-    return dtype == GDN_BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
+    const int span = kC * segment_chunks(a.rows, a.total_tokens, a.hv);
+    return a.total_tokens > span ? chunk_bytes(a, span) : 0;
 }
 
-size_t linear_chunked_workspace_bytes(int nseq, int tokens, int hv, int dk, int dv)
+cudaError_t launch_linear_chunked(const LinearArgs &a, cudaStream_t s)
 {
-    const int seg = segment_chunks(nseq, tokens, hv);
-    return divided(tokens, seg) ? sizeof(float) * (size_t)places(nseq, tokens, seg) * hv * ((size_t)dv * dk + 1) : 0;
-}
-
-cudaError_t launch_linear_chunked(LinearArgs a, cudaStream_t s)
-{
-    // the short sequences, the padding and the bad ones
-    a.most = kSerial;
-    const cudaError_t e = launch_linear_serial(a, GDN_BF16, s);
-    if (e != cudaSuccess || a.total_tokens <= kSerial)
-        return e;
     if (a.dk == 128)
         return a.dv == 128 ? go<128, 128>(a, s) : go<128, 64>(a, s);
     return a.dv == 128 ? go<64, 128>(a, s) : go<64, 64>(a, s);
