@@ -160,9 +160,11 @@ template <typename T, int DK, int R> __global__ void __launch_bounds__(kThreads)
         if (cls != 1) {
             if (cls < 0 && tid == 0)
                 report(p.err, GDN_DEVERR_BAD_SLOT);
+            const int vecs = rows * (int)sizeof(T) / 16; // of a token
             if (b >= 0 && e <= p.total_tokens) // (its own tokens, when there are such)
-                for (long long i = tid; i < (long long)(e - b) * rows; i += kThreads)
-                    static_cast<T *>(p.out)[((b + i / rows) * p.hv + h) * p.dv + first + i % rows] = from_f<T>(0.f);
+                for (int t = b + tid / vecs; tid < kThreads / vecs * vecs && t < e; t += kThreads / vecs)
+                    reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + ((size_t)t * p.hv + h) * p.dv + first)[tid % vecs] =
+                        make_uint4(0, 0, 0, 0);
             continue;
         }
         const int n = e - b;
