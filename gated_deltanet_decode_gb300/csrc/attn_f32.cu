@@ -431,12 +431,11 @@ __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(co
                 const int row = x ? r8 : r0, t = row / p.g;
                 const bool bad = (x ? s8 : s0) > ctl.broken;
                 const float m = x ? m8 : m0, l = x ? l8 : l0, i = partial ? 1.f : 1.f / l;
-                const int head = it.head * p.g + (row - t * p.g);
-                const size_t prow = part_row(p, it, it.tok + t, head, row);
-                float *const to = partial ? p.part_o + prow * D : static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + head) * D;
+                float *const to = partial ? p.part_o + part_row(p, it, it.tok + t, it.head * p.g + (row - t * p.g), row) * D
+                                          : static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + it.head * p.g + (row - t * p.g)) * D;
                 if (row < rows) {
                     if (partial && c == 0)
-                        p.part_ml[prow] = make_float2(bad ? NaN : m, l);
+                        p.part_ml[part_row(p, it, it.tok + t, it.head * p.g + (row - t * p.g), row)] = make_float2(bad ? NaN : m, l);
 #pragma unroll
                     for (int e = 0; e < D / 8; ++e)
                         *reinterpret_cast<float2 *>(to + 8 * e + 2 * c) = !partial && bad ? make_float2(0.f, 0.f)
@@ -480,15 +479,14 @@ __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(co
                             y[e] += v[e];
                 }
             }
-            const int head = it.head * p.g + (row - t * p.g);
             if (partial) {
-                const size_t prow = part_row(p, it, it.tok + t, head, row);
+                const size_t prow = part_row(p, it, it.tok + t, it.head * p.g + (row - t * p.g), row);
                 *reinterpret_cast<float4 *>(p.part_o + prow * D + col) = make_float4(y[0], y[1], y[2], y[3]);
                 if (col == 0)
                     p.part_ml[prow] = make_float2(bad ? NaN : m, l);
             } else {
                 const float i = 1.f / l;
-                float *const out = static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + head) * D + col;
+                float *const out = static_cast<float *>(a.out) + ((size_t)(it.tok + t) * a.hq + it.head * p.g + (row - t * p.g)) * D + col;
                 *reinterpret_cast<float4 *>(out) =
                     bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[0] * i, y[1] * i, y[2] * i, y[3] * i);
             }

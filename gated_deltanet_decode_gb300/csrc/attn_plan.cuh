@@ -73,6 +73,7 @@ struct SharedArgs : WorkArgs {
     size_t dense;          // rows of part_o before the runs' slots
     int4 *rec;             // [2 kinds][tokens][head groups]: first token of the item, its first run, further runs (-1: a dead
                            // token), whether shared keys go with them
+    CUtensorMap qmap;      // bf16: Q
 };
 template <bool SH> struct Kind {
     typedef Item ItemT;
@@ -82,6 +83,10 @@ template <> struct Kind<true> {
     typedef SharedItem ItemT;
     typedef SharedArgs Args;
 };
+
+// Tokens an item at most, of kernels whose items have up to `tiles` tiles.
+__device__ __forceinline__ int item_tokens(const WorkArgs &p, int tiles) { return p.tq * tiles; }
+__device__ __forceinline__ int item_tokens(const SharedArgs &p, int) { return p.second ? 2 * p.tq : p.tq; }
 
 // The workspace: cuts, then (m, l) and O of the cut items' parts.
 inline size_t work_bytes(int d, int runs, int rows_max)
@@ -673,7 +678,7 @@ template <typename T, int D> __global__ void __launch_bounds__(128) attn_join_ke
 inline size_t shared_bytes(int d, int hq, int heads, int tokens, int runs, int rows_max)
 {
     const size_t rows = 2 * (size_t)tokens * hq + (size_t)runs * rows_max;
-    return 2 * sizeof(int4) * (size_t)tokens * heads + ((rows + 1) & ~(size_t)1) * sizeof(float2) + rows * sizeof(float) * d;
+    return ((2 * sizeof(int4) * (size_t)tokens * heads + rows * sizeof(float2) + 31) & ~(size_t)31) + 16 + rows * sizeof(float) * d;
 }
 inline void shared_layout(SharedArgs &p, const SharedPrefix &f)
 {
@@ -684,7 +689,7 @@ inline void shared_layout(SharedArgs &p, const SharedPrefix &f)
     const size_t rows = p.dense + (size_t)p.runs * p.rows_max;
     p.rec = static_cast<int4 *>(p.a.work);
     p.part_ml = reinterpret_cast<float2 *>(p.rec + 2 * tokens * p.a.pages.hkv * p.groups);
-    p.part_o = reinterpret_cast<float *>(p.part_ml + ((rows + 1) & ~(size_t)1));
+    p.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(p.part_ml + rows) + 31) & ~(uintptr_t)31); // (32-byte stores)
 }
 template <typename T, int D> cudaError_t launch_join(const SharedArgs &p, cudaStream_t s)
 {

@@ -64,6 +64,10 @@ namespace {
 constexpr int kQueue = 4;   // items in flight between the walking warp and the others
 constexpr int kMeta = 16;   // key tiles whose valid-row count is kept; over a ring's tiles
 constexpr float kLazy = 8.f;
+// With shared prefixes, rows of a Q tile from which it comes by a tensor copy, whole: one warp's 16-byte copies take 4 us
+// for 128 rows, and a group's item, cut into many parts, has its Q in each of them.  A row of its own few rows copies those.
+constexpr int kCopyRows = 16;
+constexpr int kPairTokens = 1024; // and rows of new tokens of a key head from which items are pairs of tiles
 constexpr int kTmemCols = 512;
 
 template <int D> struct Geo {
@@ -113,6 +117,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// 32 bytes, a whole sector (each lane of a warp has its own row: 16-byte halves go out one by one)
+__device__ __forceinline__ void store8(float *p, const float *x)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
 // x[at] += y without indexing the registers
 __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
 {
@@ -125,7 +136,8 @@ __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
 // ---------------------------------------------------------------------------
 template <int D, bool SH>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
-    attn_tc_kernel(const typename Kind<SH>::Args p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+    attn_tc_kernel(const __grid_constant__ typename Kind<SH>::Args p, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap)
 {
     typedef Geo<D> G;
     typedef typename std::conditional<SH, Shared, Plain>::type View;
@@ -137,7 +149,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     const uint32_t sbase = sm_addr(smem);
     const AttentionArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int mt = p.tq * G::NO, hkv = a.pages.hkv, ps = a.pages.page_size;
+    const int mt = item_tokens(p, G::NO), hkv = a.pages.hkv, ps = a.pages.page_size;
     auto bar = [&](unsigned long long &b) { return sm_addr(&b); };
 
     if (sbase & 1023) { // the swizzled tiles need it; the whole CTA leaves
@@ -325,6 +337,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     break;
                 const int ntok = __shfl_sync(0xffffffffu, ctl.item[slot].ntok, 0);
                 const int n = __shfl_sync(0xffffffffu, ctl.item[slot].jb - ctl.item[slot].ja, 0);
+                // keys from the run's first tile to the last that a token sees (see `used` below)
+                const int left = !SH ? 0 : __shfl_sync(0xffffffffu, ctl.item[slot].see + (ntok - 1) * see_step(ctl.item[slot]) - ctl.item[slot].ja * KT, 0);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(ctl.iempty[slot]));
@@ -367,16 +381,25 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     }
                     const uint64_t vd = desc_mn(stage_addr(vst), KT * 128);
                     const bool more = i >= G::NO;
+                    const int last = left - (pair ? i >> 1 : i) * KT; // keys of the tile that are seen, where they are few
 #pragma unroll
                     for (int half = 0; half < G::HALVES; ++half) {
                         if (!wait(ctl.pready[b][half], pparity[b]))
                             return;
                         after_sync();
                         if (leader) {
+                            auto product = [&](int k) {
+                                mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, vd + k * (2048 >> 4), idesc(D, true), k > 0 || more);
+                            };
+                            if (!SH || last > KT - 16) {
 #pragma unroll
-                            for (int k = 4 * half; k < 4 * half + 4; ++k)
-                                mma_ts(tmem + G::O0 + o * D, tmem + G::S0 + b * KT + 8 * k, vd + k * (2048 >> 4),
-                                       idesc(D, true), k > 0 || more);
+                                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                    product(k);
+                            } else { // 16 keys a product: those past the last key are left out, and V's rows there not looked at
+#pragma unroll 1
+                                for (int k = 4 * half; k < 4 * half + 4 && 16 * k < last; ++k)
+                                    product(k);
+                            }
                             if (half == G::HALVES - 1) {
                                 // O is waited for at an item's end and, with one group, before it is rescaled
                                 if (G::NO == 1 || i + 2 >= steps)
@@ -429,6 +452,18 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     if (!wait(ctl.qempty[s], (qc / G::NQ + 1) & 1))
                         break;
                     const int rows = (min(it.ntok - i * p.tq, p.tq)) * p.g;
+                    if constexpr (SH) {
+                        if (rows > kCopyRows) { // a tile at once, with the rows of other tokens behind the item's
+                            if (lane == 0) {
+                                mbar_arrive_tx(bar(ctl.qfull[s]), (uint32_t)(p.tq * p.g * D * 2));
+                                for (int c = 0; c < G::CH; ++c)
+                                    tma3(sbase + s * G::QBYTES + c * 128 * 128, &p.qmap, 64 * c, it.head * p.g, it.tok + i * p.tq,
+                                         bar(ctl.qfull[s]));
+                            }
+                            __syncwarp();
+                            continue;
+                        }
+                    }
                     constexpr int VR = D / 8; // 16-byte vectors a row
                     const bf16 *const src = static_cast<const bf16 *>(a.q) + (size_t)(it.tok + i * p.tq) * a.q_stride +
                                             (size_t)it.head * p.g * D;
@@ -504,21 +539,25 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                 if (valid < min(KT, end - key))
                     broken = min(broken, key + valid);
                 const int later = max(0, it.see - key); // keys of the tile from here on are hidden from some tokens
+                // and those that the product with V takes (with shared prefixes, whose rows' own keys are few: else the choice
+                // takes 2 % of a prompt's chunk)
+                const int used = SH ? min(KT, (end - key + 15) & ~15) : KT;
                 // A weight of zero does not hide a NaN or an infinity.  Rows of V past the good ones may hold anything:
                 // they become zeros.  Elements that only some tokens see become zeros too where they are not finite,
                 // and the item's end adds them to the rows that do see them.
                 auto clean = [&] {
-                    if (later >= KT)
+                    if (later >= used)
                         return true;
                     const unsigned pl = place0 + v_place(pair, j, n);
                     const int st = pl % G::STAGES;
                     if (!wait(ctl.full[st], (pl / G::STAGES) & 1))
                         return false;
                     unsigned char *const v = smem + G::RING + st * G::SBYTES;
-                    for (int x = row; x < (KT - later) * 8 * G::CH; x += 128) {
-                        const int ch = x / ((KT - later) * 8), y = x - ch * (KT - later) * 8;
-                        uint4 *const at = reinterpret_cast<uint4 *>(v + ch * KT * 128 + later * 128 + y * 16);
-                        if (later + (y >> 3) >= valid) {
+                    constexpr int VR = 8 * G::CH; // 16-byte vectors a key; a thread keeps its place in it (a division a vector took
+                                                  // 3 us of a tile)
+                    for (int r = later + row / VR; r < used; r += 128 / VR) {
+                        uint4 *const at = reinterpret_cast<uint4 *>(v + (row % VR >> 3) * KT * 128 + r * 128 + (row & 7) * 16);
+                        if (r >= valid) {
                             *at = make_uint4(0, 0, 0, 0);
                         } else {
                             uint4 z = *at;
@@ -697,8 +736,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     }
                     if (mine && partial) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(po + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        for (int e = 0; e < 32; e += SH ? 8 : 4) {
+                            if constexpr (SH)
+                                store8(po + k + e, &x[e]);
+                            else
+                                *reinterpret_cast<float4 *>(po + k + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        }
                     } else if (mine) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
@@ -743,10 +786,28 @@ bool encode_pages(CUtensorMap *m, void *base, const kv_page_pool &v, int box)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int slot_rows(int d, int g, int total_tokens)
+// q as [tokens][heads][d], boxes of 64 d x the heads of a group x the tokens of a tile: its rows, in order
+bool encode_q(CUtensorMap *m, const AttentionArgs &a, int g, int tq)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.pages.d, (cuuint64_t)a.hq, (cuuint64_t)a.c.total_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.pages.d * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t boxes[3] = {64u, (cuuint32_t)g, (cuuint32_t)tq}, step[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// With shared prefixes an item is a single tile where pairs would be few: a group's item over long shared keys is cut into
+// many parts, and each costs its rows' partial sums.  Of 64 samples of a prompt of 16,000 (two tiles a key head) pairs take
+// 59.8 us, single tiles XX; prompts' chunks, whose tiles are many, are better off with pairs.
+bool single_tiles(int d, int g, int total_tokens, bool shared) { return d == 256 || (shared && total_tokens < kPairTokens / g); }
+
+int slot_rows(int d, int g, int total_tokens, bool shared)
 {
     const int tq = 128 / g, one = tq * g;
-    if (d == 256 || total_tokens <= tq)
+    if (single_tiles(d, g, total_tokens, shared) || total_tokens <= tq)
         return total_tokens < tq ? total_tokens * g : one;
     return 128 + one; // a pair of tiles, the second's rows from 128 on
 }
@@ -782,8 +843,8 @@ template <int D> cudaError_t go(const AttentionArgs &a, const SharedPrefix *f, k
     p.groups = a.hq / a.pages.hkv / p.g;
     p.tq = 128 / p.g;
     p.runs = kSms; // one CTA an SM: its tensor memory is taken whole
-    p.rows_max = slot_rows(D, p.g, a.c.total_tokens);
-    p.second = G::NO == 2 ? 128 : 0;
+    p.rows_max = slot_rows(D, p.g, a.c.total_tokens, f != nullptr);
+    p.second = single_tiles(D, p.g, a.c.total_tokens, f != nullptr) ? 0 : 128;
     {
         const std::lock_guard<std::mutex> lk(pool.map_mutex);
         const int box = pool.page_size < G::KT ? pool.page_size : G::KT;
@@ -796,6 +857,8 @@ template <int D> cudaError_t go(const AttentionArgs &a, const SharedPrefix *f, k
     const dim3 grid(p.runs), block(G::THREADS);
     if (f) {
         shared_layout(p, *f);
+        if (!encode_q(&p.qmap, a, p.g, p.tq))
+            return cudaErrorInvalidValue;
         e = launch_pdl(attn_tc_kernel<D, true>, grid, block, (size_t)G::TOTAL, s, p, pool.kmap, pool.vmap);
         return e == cudaSuccess ? launch_join<bf16, D>(p, s) : e;
     }
@@ -808,7 +871,7 @@ template <int D> cudaError_t go(const AttentionArgs &a, const SharedPrefix *f, k
 
 size_t attention_tc_workspace_bytes(int d, int hq, int hkv, int total_tokens, bool shared)
 {
-    const int g = group_heads(hq, hkv, 128), rows = slot_rows(d, g, total_tokens);
+    const int g = group_heads(hq, hkv, 128), rows = slot_rows(d, g, total_tokens, shared);
     return shared ? shared_bytes(d, hq, hq / g, total_tokens, kSms, rows) : work_bytes(d, kSms, rows);
 }
 
