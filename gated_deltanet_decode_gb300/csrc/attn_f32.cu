@@ -65,11 +65,16 @@ template <int D> struct Geo32 {
 // Units of a tile, by its time.  (Measured, us of a CTA: up to 16, 32, 64 and 128 rows 1.13, 2.0, 3.1 and 5.3 at d = 64
 // and 1.19, 2.0, 3.0 and 5.3 at d = 128; up to 32 and 64 rows 2.0 and 3.7 at d = 256.)
 template <int D> struct Cost32 {
-    static constexpr int least = 4, most = D == 256 ? 7 : 18;
+    static constexpr int least = 4, most = D == 256 ? 7 : 18, item = 0;
     static __device__ __forceinline__ int of(int rows)
     {
         return rows <= 16 * Geo32<D>::WRS ? least : D == 256 ? most : rows <= 32 ? 7 : rows <= 64 ? 11 : most;
     }
+};
+
+// With shared prefixes items are many and short: their begins and ends count (2 to 3 us).
+template <int D> struct SharedCost32 : Cost32<D> {
+    static constexpr int item = 10;
 };
 
 template <typename V> struct Ctrl32 {
@@ -252,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(co
     typedef Geo32<D> G;
     typedef typename std::conditional<SH, Shared, Plain>::type View;
     typedef typename Kind<SH>::ItemT ItemT;
-    typedef Walk<Cost32<D>, View, typename Kind<SH>::Args> WalkT;
+    typedef typename std::conditional<SH, SharedCost32<D>, Cost32<D>>::type Cost;
+    typedef Walk<Cost, View, typename Kind<SH>::Args> WalkT;
     constexpr int KT = G::KT, LD = G::LD;
     extern __shared__ __align__(16) float sm[];
     __shared__ Ctrl32<View> ctl;
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(co
     const float c2 = a.scale * 1.44269504088896341f;
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const RunOf<View> run = plan_run<kThreads, KT, Cost32<D>, View>(p, p.tq, ctl.scan, ctl.found);
+    const RunOf<View> run = plan_run<kThreads, KT, Cost, View>(p, p.tq, ctl.scan, ctl.found);
     zero_dead<float, D, kThreads, View>(p, tid);
     WalkT walk(p, run, p.tq, KT); // warp 0's is followed (another warp's writes the same zero)
     for (;;) {
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(co
                 o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
             m0 = m8 = -INFINITY, l0 = l8 = 0.f;
             if (few) { // two tiles at a time, 8 keys a warp; SF - 2 tiles ahead
-                constexpr int SH = KT / 8, SF = G::STAGES_FEW, A = SF - 2; // shares of a tile
+                constexpr int NS = KT / 8, SF = G::STAGES_FEW, A = SF - 2; // shares of a tile
                 Pages pages[A];
 #pragma unroll
                 for (int i = 0; i < A; ++i)
@@ -378,9 +384,9 @@ __global__ void __launch_bounds__(kThreads, Geo32<D>::PER_SM) attn_f32_kernel(co
                     load(pages[0], j + A, (j + A) % SF);
                     load(pages[1], j + A + 1, (j + A + 1) % SF);
                     look(pages[0], j + A + 2), look(pages[1], j + A + 3);
-                    const int mine = j + wk / SH;
+                    const int mine = j + wk / NS;
                     if (16 * wr < rows && mine < n)
-                        work(mine, mine % SF, wk % SH * 8, Width<1>(), second);
+                        work(mine, mine % SF, wk % NS * 8, Width<1>(), second);
                 }
             } else {
                 constexpr int S = G::STAGES, A = S - 1;

@@ -42,9 +42,10 @@ struct Cut {
 };
 
 // Units of a key tile of an item with `rows` rows: kernels whose tiles cost the
-// same whatever the rows, and others.
+// same whatever the rows, and others.  `item` units more are for an item to
+// begin and end, where items of few tiles are many; its first tile counts them.
 struct EvenCost {
-    static constexpr int least = 1, most = 1;
+    static constexpr int least = 1, most = 1, item = 0;
     static __device__ __forceinline__ int of(int) { return 1; }
 };
 
@@ -243,6 +244,7 @@ template <typename V> struct RunOf {
     long long share, u0, u1, base;
     long long per;           // units a head of the row it begins in
     int row;
+    int item;                // units of an item besides its tiles'
     typename V::RowT first;  // that row
 };
 template <typename V> struct FoundOf { // shared memory
@@ -255,40 +257,60 @@ __device__ RunOf<V> plan_run(const Args &p, int mt, long long *part, FoundOf<V> 
 {
     const int count = V::count(p), heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
     typename V::RowT x = {};
-    long long per = 0;
-    auto cost_of = [&](int r) -> long long {
+    long long per = 0, items = 0; // units of the tiles of a key head of this thread's row, and its items
+    auto look = [&](int r) {
+        per = items = 0;
         if (r >= count)
-            return 0;
+            return;
         x = V::get(p, r);
-        per = x.live ? head_units<Cost, V>(x, mt, KT, p.g) : 0;
-        return per * heads;
+        if (x.live) {
+            per = head_units<Cost, V>(x, mt, KT, p.g);
+            if (Cost::item)
+                items = items_of(x, mt);
+        }
     };
     int dearest = 1; // tile of this thread's rows
     RunOf<V> run;
-    long long total = 0, cost = 0, before = 0, sum;
+    long long total = 0, begun = 0, cost = 0, before = 0, sum, n0 = 0, n;
     for (int b = 0; b < count; b += THREADS) {
-        cost = cost_of(b + tid);
+        look(b + tid);
+        cost = per * heads;
         if (cost > 0)
             dearest = max(dearest, Cost::of(min(x.n, mt) * p.g));
         if (x.bad && blockIdx.x == 0)
             report(p.a.err, GDN_DEVERR_BAD_PAGE);
         before = scan64(cost, part, THREADS / 32, sum);
         total += sum;
+        if (Cost::item) {
+            n0 = scan64(items * heads, part, THREADS / 32, n);
+            begun += n;
+        }
     }
-    run.share = (total + gridDim.x - 1) / gridDim.x;
     // (Cost's values are few, and one barrier tells whether a thread has seen more than the least)
     const int least = Cost::least, tile = Cost::most == least ? least : __syncthreads_or(dearest > least) ? Cost::most : least;
-    if (run.share < tile)
-        run.share = tile;
+    // A run is no shorter than an item's first tile, with what the item takes besides.  Where there is less work than that
+    // for every run, it is better spread than weighed.
+    run.item = Cost::item && total + Cost::item * begun >= (long long)(tile + Cost::item) * gridDim.x ? Cost::item : 0;
+    total += run.item * begun;
+    run.share = (total + gridDim.x - 1) / gridDim.x;
+    if (run.share < tile + run.item)
+        run.share = tile + run.item;
     run.u0 = run.share * blockIdx.x;
     run.u1 = min(total, run.u0 + run.share);
+    auto weigh = [&] {
+        per += run.item * items;
+        cost = per * heads;
+    };
     if (count <= THREADS) { // the one pass has it
+        weigh();
+        before += run.item * n0;
         if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
             found = {before, per, tid, x};
     } else {
         long long seen = 0;
         for (int b = 0; b < count && seen <= run.u0 && run.u0 < total; b += THREADS) {
-            cost = cost_of(b + tid);
+            look(b + tid);
+            weigh();
             before = seen + scan64(cost, part, THREADS / 32, sum);
             if (cost > 0 && before <= run.u0 && run.u0 < before + cost)
                 found = {before, per, b + tid, x};
@@ -365,18 +387,26 @@ template <typename Cost, typename V, typename Args> struct Walk {
             for (; rem >= run.per; ++h)
                 rem -= run.per;
             for (;; ++t) {
-                const long long units = item_tiles<V>(x, t, mt, kt) * (long long)unit();
+                const long long units = extra() + item_tiles<V>(x, t, mt, kt) * (long long)unit();
                 if (rem < units)
                     break;
                 rem -= units;
             }
-            ja = (int)((rem + unit() - 1) / unit());
-            u += (long long)ja * unit() - rem; // a tile that began before u0 is the run's before
+            ja = tile_from(rem, unit());
+            u += tile_begin(ja, unit()) - rem; // a tile that began before u0 is the run's before
             if (ja == item_tiles<V>(x, t, mt, kt))
                 done();
         }
     }
     static constexpr bool SH = sizeof(Args) != sizeof(WorkArgs);
+    __device__ int extra() const { return Cost::item ? run.item : 0; }
+    // Where tile j of an item begins, in units from the item's begin, and the first tile to begin at `at` or later.
+    __device__ long long tile_begin(int j, int w) const { return j == 0 ? 0 : extra() + (long long)j * w; }
+    __device__ int tile_from(long long at, int w) const
+    {
+        const int j = (int)((at - extra() + w - 1) / w);
+        return Cost::item == 0 ? j : at <= 0 ? 0 : max(1, j);
+    }
     __device__ int unit() const { return Cost::of(min(mt, x.n - t * mt) * p.g); }
     __device__ void done() // with item t
     {
@@ -427,16 +457,17 @@ template <typename Cost, typename V, typename Args> struct Walk {
             enter(x);
         }
         const int J = item_tiles<V>(x, t, mt, kt);
-        const int w = unit(), jb = (int)min((long long)J, ja + (run.u1 - u + w - 1) / w);
+        const int w = unit();
+        const long long start = u - tile_begin(ja, w);
+        const int jb = Cost::item == 0 ? (int)min((long long)J, ja + (run.u1 - u + w - 1) / w) : min(J, tile_from(run.u1 - start, w));
         const int t0 = t * mt, ntok = min(mt, x.n - t0);
         const bool cut = ja > 0 || jb < J;
-        const long long start = u - (long long)ja * w;
         if constexpr (SH) {
             static_cast<Item &>(it) = {x.b + t0, ntok, h, x.row, x.len - (x.n - t0 - 1) * x.step, ja, jb,
                                        ja > 0 ? (int)blockIdx.x : cut || x.kind || x.skip > 0 ? kDense : -1};
             it.skip = x.skip, it.step = x.step, it.kind = x.kind;
             if (ja == 0) { // the item's first part says where the others are
-                const int more = (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x;
+                const int more = (int)((start + tile_begin(J - 1, w)) / run.share) - (int)blockIdx.x;
                 for (int i = lane; i < ntok; i += 32)
                     p.rec[((size_t)x.kind * p.a.c.total_tokens + x.b + t0 + i) * heads + h] =
                         make_int4(x.b + t0, (int)blockIdx.x, more, x.skip > 0);
@@ -447,7 +478,7 @@ template <typename Cost, typename V, typename Args> struct Walk {
             if (lane == 0 && ja > 0 && start >= run.u0 - run.share)
                 p.cuts[blockIdx.x] = {2 + (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x, x.b + t0, ntok, h};
         }
-        u += (long long)(jb - ja) * w;
+        u = start + tile_begin(jb, w);
         done();
         return true;
     }

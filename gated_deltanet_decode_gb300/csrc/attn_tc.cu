@@ -70,6 +70,12 @@ constexpr int kCopyRows = 16;
 constexpr int kPairTokens = 1024; // and rows of new tokens of a key head from which items are pairs of tiles
 constexpr int kTmemCols = 512;
 
+// Rows' own keys behind shared prefixes make items of a few tiles, of which each takes about as long as three tiles to begin
+// and to end (its copies' latency, and sums that are not ready before their products).
+struct SharedCost : EvenCost {
+    static constexpr int item = 3;
+};
+
 template <int D> struct Geo {
     static constexpr int KT = D == 256 ? 64 : 128;       // keys a tile
     static constexpr int NO = D == 256 ? 1 : 2;          // O accumulators, softmax groups, tiles of an item at most
@@ -143,6 +149,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     typedef typename std::conditional<SH, Shared, Plain>::type View;
     typedef CtrlOf<View> Ctrl;
     typedef typename Kind<SH>::ItemT ItemT;
+    typedef typename std::conditional<SH, SharedCost, EvenCost>::type Cost;
     constexpr int KT = G::KT;
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctrl &ctl = *reinterpret_cast<Ctrl *>(smem + G::CTRL);
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const RunOf<View> run = plan_run<G::THREADS, KT, EvenCost, View>(p, mt, ctl.scan, ctl.found);
+    const RunOf<View> run = plan_run<G::THREADS, KT, Cost, View>(p, mt, ctl.scan, ctl.found);
     bool alive = true; // false once a bounded wait ran out
     auto wait_at = [&](uint32_t b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
         if (!__all_sync(0xffffffffu, mbar_try(b, parity)) && alive && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 3) {
             // ---- the walk: this run's items, in order
-            Walk<EvenCost, View, typename Kind<SH>::Args> walk(p, run, mt, KT);
+            Walk<Cost, View, typename Kind<SH>::Args> walk(p, run, mt, KT);
             ItemT it;
             for (int q = 0; alive; ++q) {
                 const bool more = walk.next(it);
