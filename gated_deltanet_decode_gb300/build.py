@@ -23,6 +23,7 @@ SOURCES = ["gdn_api.cu", "gdn_stream.cu", "gdn_conv.cu", "gdn_prefill.cu", "gdn_
 HEADERS = [os.path.join(CSRC, "gdn_device.cuh"), os.path.join(CSRC, "gdn_ptx.cuh"),
            os.path.join(CSRC, "gdn_chunk_common.cuh"), os.path.join(CSRC, "attn_plan.cuh"),
            os.path.join(CSRC, "tc_ops.cuh"), os.path.join(CSRC, "linear_plan.cuh"),
+           os.path.join(CSRC, "tf32_ops.cuh"),
            os.path.join(CSRC, "gdn_internal.h"),
            os.path.join(ROOT, "include", "gdn_decode.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

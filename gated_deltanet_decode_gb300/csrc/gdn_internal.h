@@ -217,7 +217,7 @@ size_t prefill_chunked_workspace_bytes(int nseq, int total_tokens, int hv);
 cudaError_t launch_linear_decode(const LinearArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_linear_serial(const LinearArgs &a, int dtype, cudaStream_t s);
 // Packed sequences: the short ones by the serial kernel, the others in chunks, bf16 with dk and dv 64 or 128 on the
-// tensor cores (launch_linear_chunked), the rest in fp32 FMAs.
+// tensor cores (launch_linear_chunked), the rest to fp32's precision.
 size_t linear_prefill_workspace_bytes(const LinearArgs &a, int dtype);
 cudaError_t launch_linear_prefill(LinearArgs a, int dtype, cudaStream_t s);
 size_t linear_chunked_workspace_bytes(const LinearArgs &a);

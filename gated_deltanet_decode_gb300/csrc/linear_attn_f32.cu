@@ -1,26 +1,28 @@
 // Linear attention with a decay for each head over packed sequences in chunks
-// of C = 64 tokens in fp32 (sm_103a): fp32 activations, and bf16 ones whose head
+// of C = 64 tokens to fp32's precision (sm_103a): fp32 activations, and bf16 ones whose head
 // sizes the tensor core kernel (linear_attn_tc.cu, with the formula) is not made
 // for.  Work is divided as linear_plan.cuh says; a CTA takes a block of VB value
 // rows of a head through a segment, with its state in shared memory.
 //
 // All four products are sums over the last dimension of two tiles in shared
-// memory, rows DK + 4 or C + 4 floats apart:
+// memory, rows DK + 4 or C + 4 floats apart, so that a fragment's loads fall in
+// 32 banks:
 //   P = Q K^T,   O = e^G Q S^T + (P e^{G_i - G_j}) V,   S += (e^{G_C - G} V)^T K
-// with V kept transposed, and K transposed into Q's place for the last.  A thread
-// has 4 x 4 of a result, rows 4 and 8 apart, so that a warp's loads of 16 bytes
-// are of rows in different banks.  Multiplications are packed fp32 FMAs of pairs
-// along the sum: three tf32 products of split operands (attn_f32.cu) would be as
-// fast, and cut their sums short.
+// with V kept transposed, and K transposed into Q's place for the last.  They run
+// on the tensor cores in tf32 with split operands (tf32_ops.cuh), eight warps as
+// 2 x 4 blocks of a result of 64 x 64.  In packed FMAs of 4 x 4 results a thread,
+// whose operands' loads took all of shared memory's bandwidth, the batch below
+// took XX us.
 //
-// Bound: the FMAs, two wide, a chunk's 3/4 + 5/8 + 1 + 1 products of 64 x 64 x
-// DK each.
+// Bound: latency.  A segment is mostly a single chunk; its loads, five barriers
+// and the products' chains follow each other, with one to two CTAs an SM.
 #include <atomic>
 
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
 #include "gdn_ptx.cuh"
 #include "linear_plan.cuh"
+#include "tf32_ops.cuh"
 
 namespace gdn {
 namespace {
@@ -33,7 +35,7 @@ template <int DK> struct FGeo {
     static constexpr int VB = DK == 256 ? 32 : 64; // value rows a CTA: shared memory
     static constexpr int LD = DK + 4;
     // floats: K; Q, later K transposed; the state; V transposed; the weights
-    static constexpr int K = 0, Q = K + kC * LD, QN = kC * LD > DK * kLd ? kC * LD : DK * kLd;
+    static constexpr int K = 0, Q = K + kC * LD, KT = (DK > 32 ? DK : 32) * kLd, QN = kC * LD > KT ? kC * LD : KT;
     static constexpr int S = Q + QN, V = S + VB * LD, P = V + VB * kLd, END = P + kC * kLd;
 };
 
@@ -44,34 +46,50 @@ struct FCtrl {
     int badfrom[64], dirty;           // first token with a value that is not finite, by value row
 };
 
-// acc += sum over k0 <= k < k1 of rows of a (r0 + 4 i) and of b (c0 + 8 j), pairs of k
-template <int N> __device__ __forceinline__ void dots(const float *a, int lda, const float *b, int ldb, int k0, int k1, float2 (&acc)[4][N])
+// A warp's 32 x 8 N of a result: sums over k < k1 (a multiple of 16) of rows of a and of b.  Result fragments: rows
+// 16 m + g and + 8, columns 8 n + 2 c and + 1, with g = lane / 4, c = lane % 4.
+template <int N> __device__ __forceinline__ void products(const float *a, int lda, const float *b, int ldb, int k1, float (&sum)[2][N][4])
 {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[m][n][e] = 0.f;
+    a += g * lda + c, b += g * ldb + c;
 #pragma unroll 2
-    for (int k = k0; k < k1; k += 4) {
-        float4 x[4], y[N];
+    for (int k0 = 0; k0 < k1; k0 += 16) { // the tensor cores sum two steps of eight
+        float t[2][N][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const float4 *>(a + 4 * i * lda + k);
+        for (int k = k0; k < k0 + 16; k += 8) {
+            uint32_t ah[2][4], al[2][4];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            y[j] = *reinterpret_cast<const float4 *>(b + 8 * j * ldb + k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                acc[i][j] = fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), acc[i][j]);
-                acc[i][j] = fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), acc[i][j]);
+            for (int m = 0; m < 2; ++m) {
+                split2(a[16 * m * lda + k], a[(16 * m + 8) * lda + k], ah[m][0], al[m][0], ah[m][1], al[m][1]);
+                split2(a[16 * m * lda + k + 4], a[(16 * m + 8) * lda + k + 4], ah[m][2], al[m][2], ah[m][3], al[m][3]);
             }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                uint32_t h0, l0, h1, l1;
+                split2(b[8 * n * ldb + k], b[8 * n * ldb + k + 4], h0, l0, h1, l1);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    mma8(t[m][n], al[m], h0, h1);
+                    mma8(t[m][n], ah[m], l0, l1);
+                    mma8(t[m][n], ah[m], h0, h1);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sum[m][n][e] += t[m][n][e];
     }
-}
-template <int N> __device__ __forceinline__ void clear(float2 (&acc)[4][N])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            acc[i][j] = make_float2(0.f, 0.f);
 }
 
 // four elements in fp32
@@ -81,6 +99,12 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
     const uint2 w = *reinterpret_cast<const uint2 *>(p);
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xffff0000u));
+}
+
+__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
 }
 
 // The decays of a chunk, by one warp, two tokens a lane.
@@ -118,16 +142,16 @@ __device__ __forceinline__ void chunk_decays(const LinearArgs &a, int tok, int n
 }
 
 // SUM: the segments' own sums; else the outputs, and the states at the sequences' ends.
-template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThreads) linear_ffma_kernel(const ChunkArgs p)
+template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const ChunkArgs p)
 {
     typedef FGeo<DK> G;
-    constexpr int VB = G::VB, LD = G::LD, N = VB / 16;
+    constexpr int VB = G::VB, LD = G::LD, N = VB / 32, VQ = VB * kC / 4 / kThreads;
     extern __shared__ __align__(16) float sm[];
     __shared__ FCtrl ctl;
     const LinearArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // this thread's rows r0 + 4 i of a result, and columns c0 + 8 j of VB, k0 + 8 j of 64
-    const int r0 = 16 * (warp >> 1) + (lane >> 3), c0 = VB / 2 * (warp & 1) + (lane & 7), k0 = 32 * (warp & 1) + (lane & 7);
+    // this warp's rows r0 .. + 32 of a result, and columns c0 .. + 8 N of VB, k0 .. + 16 of 64; this thread's place in them
+    const int r0 = 32 * (warp >> 2), c0 = VB / 4 * (warp & 3), k0 = 16 * (warp & 3), g = lane >> 2, c = lane & 3;
     const int blocks = (a.dv + VB - 1) / VB;
     wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -159,14 +183,22 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
         for (int t = 0; t < it.n; t += kC) {
             const int n = min(kC, it.n - t);
             const long long tok = it.tok + t;
+            // V, on its way: eight tokens x 16 values a warp
+            float4 ahead[VQ];
+#pragma unroll
+            for (int i = 0; i < VQ; ++i) {
+                const int x = tid + i * kThreads, j = (x & 7) + 8 * (x / (2 * VB)), v = 4 * ((x >> 3) % (VB / 4));
+                ahead[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < n && v < rows)
+                    ahead[i] = load4(static_cast<const T *>(a.v) + (tok + j) * a.v_stride + head * a.dv + v0 + v);
+            }
             __syncthreads(); // the chunk before is done with the tiles
             if (tid < VB)
                 ctl.badfrom[tid] = kC;
             if (tid == 0)
                 ctl.dirty = 0;
-            if (warp == 0)
-                chunk_decays(a, (int)tok, n, head, ctl);
             // K and Q as they are, V transposed; zeros past the end
+#pragma unroll 4
             for (int x = tid; x < kC * (DK / 4); x += kThreads) {
                 const int j = x / (DK / 4), k = 4 * (x - j * (DK / 4));
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
@@ -179,13 +211,13 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                 if (!SUM)
                     *reinterpret_cast<float4 *>(sm + G::Q + j * LD + k) = z;
             }
+            if (warp == 0)
+                chunk_decays(a, (int)tok, n, head, ctl);
             __syncthreads(); // (the marks are clear)
-            for (int x = tid; x < kC * (VB / 4); x += kThreads) { // eight tokens x 16 values a warp
-                const int j = (x & 7) + 8 * (x / (2 * VB)), v = 4 * ((x >> 3) % (VB / 4));
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j < n && v < rows)
-                    y = load4(static_cast<const T *>(a.v) + (tok + j) * a.v_stride + head * a.dv + v0 + v);
-                float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < VQ; ++i) {
+                const int x = tid + i * kThreads, j = (x & 7) + 8 * (x / (2 * VB)), v = 4 * ((x >> 3) % (VB / 4));
+                float z[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     // a weight of zero does not hide a value that is not finite: it is left out, and its row marked
@@ -199,46 +231,44 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
             }
             __syncthreads();
             if constexpr (!SUM) {
-                // the weights: the rows' tokens r0 + 4 i, keys k0 + 8 j
-                {
-                    float2 acc[4][4];
-                    clear(acc);
-                    const bool hidden = (warp & 1) && warp < 4; // all keys behind all tokens
-                    if (!hidden)
-                        dots<4>(sm + G::Q + r0 * LD, LD, sm + G::K + k0 * LD, LD, 0, DK, acc);
+                { // the weights: tokens r0 .., keys k0 ..
+                    float p2[2][2][4] = {};
+                    if (k0 < r0 + 32) // (else all keys are behind all tokens)
+                        products<2>(sm + G::Q + r0 * LD, LD, sm + G::K + k0 * LD, LD, DK, p2);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int r = r0 + 4 * i, c = k0 + 8 * j;
-                            sm[G::P + r * kLd + c] =
-                                c <= r ? (acc[i][j].x + acc[i][j].y) * exp2f((ctl.hi[r] - ctl.hi[c]) + (ctl.lo[r] - ctl.lo[c])) : 0.f;
-                        }
+                        for (int n2 = 0; n2 < 2; ++n2)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int r = r0 + 16 * m + g + 8 * (e >> 1), k = k0 + 8 * n2 + 2 * c + (e & 1);
+                                sm[G::P + r * kLd + k] =
+                                    k <= r ? p2[m][n2][e] * exp2f((ctl.hi[r] - ctl.hi[k]) + (ctl.lo[r] - ctl.lo[k])) : 0.f;
+                            }
                 }
-                float2 acc[4][N];
-                clear(acc);
-                dots<N>(sm + G::Q + r0 * LD, LD, sm + G::S + c0 * LD, LD, 0, DK, acc);
-                float o[4][N];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f = exp2f(ctl.hi[r0 + 4 * i] + ctl.lo[r0 + 4 * i]);
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        o[i][j] = (acc[i][j].x + acc[i][j].y) * f;
-                }
+                float o[2][N][4], own[2][N][4];
+                products<N>(sm + G::Q + r0 * LD, LD, sm + G::S + c0 * LD, LD, DK, o);
                 __syncthreads(); // the weights are there
-                clear(acc);
-                dots<N>(sm + G::P + r0 * kLd, kLd, sm + G::V + c0 * kLd, kLd, 0, 16 * (warp >> 1) + 16, acc);
+                products<N>(sm + G::P + r0 * kLd, kLd, sm + G::V + c0 * kLd, kLd, r0 + 32, own);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const int r = r0 + 4 * i, c = c0 + 8 * j;
-                        float x = (o[i][j] + (acc[i][j].x + acc[i][j].y)) * a.scale;
-                        if (ctl.dirty && ctl.badfrom[c] <= r)
-                            x = __int_as_float(0x7fc00000);
-                        if (r < n && c < rows)
-                            static_cast<T *>(a.out)[((tok + r) * a.hv + head) * a.dv + v0 + c] = from_f<T>(x);
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = r0 + 16 * m + g + 8 * h;
+                        const float f = exp2f(ctl.hi[r] + ctl.lo[r]);
+#pragma unroll
+                        for (int n2 = 0; n2 < N; ++n2) {
+                            const int v = c0 + 8 * n2 + 2 * c;
+                            float x[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                x[e] = fmaf(o[m][n2][2 * h + e], f, own[m][n2][2 * h + e]) * a.scale;
+                                if (ctl.dirty && ctl.badfrom[v + e] <= r)
+                                    x[e] = __int_as_float(0x7fc00000);
+                            }
+                            if (r < n && v < rows)
+                                store2(static_cast<T *>(a.out) + ((tok + r) * a.hv + head) * a.dv + v0 + v, x[0], x[1]);
+                        }
                     }
                 if (t + kC >= it.n && !it.last)
                     continue; // the next segment's state comes from the scan
@@ -258,20 +288,21 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
             __syncthreads();
             const float all = ctl.all;
             total *= all;
-            for (int m = 0; m < DK; m += 64) { // rows m .. of the state's dk
-                if (m + 16 * (warp >> 1) >= DK)
-                    continue;
-                float2 acc[4][N];
-                clear(acc);
-                dots<N>(sm + G::Q + (m + r0) * kLd, kLd, sm + G::V + c0 * kLd, kLd, 0, kC, acc);
+            for (int x0 = r0; x0 < DK; x0 += 64) { // rows x0 .. + 32 of the state's dk
+                float y[2][N][4];
+                products<N>(sm + G::Q + x0 * kLd, kLd, sm + G::V + c0 * kLd, kLd, kC, y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const int c = c0 + 8 * j;
-                        float *const s = sm + G::S + c * LD + m + r0 + 4 * i;
-                        *s = fmaf(*s, all, acc[i][j].x + acc[i][j].y) + (ctl.dirty && ctl.badfrom[c] < kC ? __int_as_float(0x7fc00000) : 0.f);
-                    }
+                    for (int n2 = 0; n2 < N; ++n2)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = x0 + 16 * m + g + 8 * (e >> 1), v = c0 + 8 * n2 + 2 * c + (e & 1);
+                            if (DK >= 32 || k < DK) {
+                                float *const s = sm + G::S + v * LD + k;
+                                *s = fmaf(*s, all, y[m][n2][e]) + (ctl.dirty && ctl.badfrom[v] < kC ? __int_as_float(0x7fc00000) : 0.f);
+                            }
+                        }
             }
         }
         if (SUM || it.last) {
@@ -307,9 +338,9 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
         return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(linear_ffma_kernel<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+        e = cudaFuncSetAttribute(linear_f32_kernel<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(linear_ffma_kernel<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+            e = cudaFuncSetAttribute(linear_f32_kernel<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
         if (e != cudaSuccess)
             return e;
         configured.fetch_or(bit, std::memory_order_release);
@@ -323,13 +354,13 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
     const long long most = places(a.rows, a.total_tokens, p.span) * p.heads; // items
     const dim3 grid((unsigned)(most < 8 * kSms ? most : 8 * kSms));
     if (a.total_tokens > p.span) { // a sequence can have several segments
-        e = launch_pdl(linear_ffma_kernel<T, DK, true>, grid, dim3(kThreads), (size_t)BYTES, s, p);
+        e = launch_pdl(linear_f32_kernel<T, DK, true>, grid, dim3(kThreads), (size_t)BYTES, s, p);
         if (e == cudaSuccess)
             e = launch_scan(p, s);
         if (e != cudaSuccess)
             return e;
     }
-    return launch_pdl(linear_ffma_kernel<T, DK, false>, grid, dim3(kThreads), (size_t)BYTES, s, p);
+    return launch_pdl(linear_f32_kernel<T, DK, false>, grid, dim3(kThreads), (size_t)BYTES, s, p);
 }
 template <typename T> cudaError_t by_dk(const LinearArgs &a, cudaStream_t s)
 {
