@@ -254,7 +254,7 @@ template <typename T, int DK> cudaError_t serial(const LinearArgs &a, cudaStream
     typedef SGeo<T, DK, R> G;
     static_assert(G::BYTES <= 48 * 1024, "shared memory");
     const long long items = (long long)a.rows * a.hv * ((a.dv + G::ROWS - 1) / G::ROWS);
-    const unsigned grid = (unsigned)(items < 152 * 8 ? items : 152 * 8);
+    const unsigned grid = (unsigned)(items < 152 * 64 ? items : 152 * 64);
     return launch_pdl(linear_serial_kernel<T, DK, R>, dim3(grid), dim3(kThreads), (size_t)G::BYTES, s, a);
 }
 template <typename T> cudaError_t by_dk(const LinearArgs &a, bool prefill, cudaStream_t s)
