@@ -123,13 +123,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// 32 bytes, a whole sector (each lane of a warp has its own row: 16-byte halves go out one by one)
-__device__ __forceinline__ void store8(float *p, const float *x)
-{
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
-                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
 // x[at] += y without indexing the registers
 __device__ __forceinline__ void poison(float (&x)[32], int at, float y)
 {

@@ -192,8 +192,8 @@ template <int DK, int DV> struct ChunkCtrl {
     unsigned long long qk, qs, pready, odone, ofree, dsdone, sready, vseen;
     LItem item[kQueue];
     Decays tab[2];
-    int badfrom[3][kC]; // by chunk: first token with a value that is not finite, by column
-    int dirty[3];       // whether there is one
+    int badfrom[4][kC]; // by chunk: first token with a value that is not finite, by column
+    int dirty[4];       // whether there is one
     uint32_t tmem;
 };
 
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(ctl.qk), 1), mbar_init(bar(ctl.qs), 1), mbar_init(bar(ctl.pready), kComp / 2);
         mbar_init(bar(ctl.odone), 1), mbar_init(bar(ctl.ofree), kComp / 2), mbar_init(bar(ctl.vseen), kComp / 2);
         mbar_init(bar(ctl.dsdone), 1), mbar_init(bar(ctl.sready), kComp), mbar_init(bar(ctl.b.drain), 1);
-        ctl.dirty[0] = ctl.dirty[1] = ctl.dirty[2] = 0;
+        ctl.dirty[0] = ctl.dirty[1] = ctl.dirty[2] = ctl.dirty[3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int i = tid; i < 3 * kC; i += kThreads)
+    for (int i = tid; i < 4 * kC; i += kThreads)
         (&ctl.badfrom[0][0])[i] = kC;
     before_sync();
     __syncthreads();
@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int w4 = warp & 3, quarter = (warp - 4) >> 2, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)w4 << 21;
         const bool has = row < DV; // whether this thread keeps a part of the state: row `row`, columns quarter WK ..
-        float s[WK];
+        const bool whole = (reinterpret_cast<uintptr_t>(a.pool) & 31) == 0; // (a pool's memory is aligned to 16 bytes)
+        alignas(16) float s[WK];
         auto write_state = [&] { // in bf16, for the products
             if (has) {
 #pragma unroll
@@ -477,17 +478,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t slot = (size_t)a.hv * DV * DK, mine = (size_t)it.head * DV * DK + (size_t)row * DK + quarter * WK;
             const float *const from = it.from < 0 ? a.pool + slot * it.rs + mine : p.state + slot * it.from + mine;
 #pragma unroll
-            for (int k = 0; k < WK; k += 4) {
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (has)
-                    x = *reinterpret_cast<const float4 *>(from + k);
-                s[k] = x.x, s[k + 1] = x.y, s[k + 2] = x.z, s[k + 3] = x.w;
+            for (int k = 0; k < WK; k += 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s[k + e] = 0.f;
+                if (has && (whole || it.from >= 0)) {
+                    load8(from + k, &s[k]);
+                } else if (has) {
+                    *reinterpret_cast<float4 *>(&s[k]) = *reinterpret_cast<const float4 *>(from + k);
+                    *reinterpret_cast<float4 *>(&s[k + 4]) = *reinterpret_cast<const float4 *>(from + k + 4);
+                }
             }
             write_state();
         };
-        auto update = [&](int t) { // the state, with the sum of the chunk at token t of the item
-            const float all = ctl.tab[ch & 1].all;
-            if (!wait(ctl.dsdone, ch & 1))
+        auto update = [&](unsigned c, float all, bool more) { // the state, with the sum of chunk c, and whether the item has more
+            if (!wait(ctl.dsdone, c & 1))
                 return false;
             after_sync();
             {
@@ -497,14 +502,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < WK; ++e)
                     s[e] = fmaf(s[e], all, __uint_as_float(r[e]));
             }
-            if (t + kC < it.n) {
+            if (more) {
                 write_state();
             } else {
                 if (it.last && has) {
                     float *const to = a.pool + (size_t)a.hv * DV * DK * it.ws + (size_t)it.head * DV * DK + (size_t)row * DK + quarter * WK;
 #pragma unroll
-                    for (int k = 0; k < WK; k += 4)
-                        *reinterpret_cast<float4 *>(to + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
+                    for (int k = 0; k < WK; k += 8)
+                        if (whole) {
+                            store8(to + k, &s[k]);
+                        } else {
+                            *reinterpret_cast<float4 *>(to + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
+                            *reinterpret_cast<float4 *>(to + k + 4) = make_float4(s[k + 4], s[k + 5], s[k + 6], s[k + 7]);
+                        }
                 }
                 before_sync();
             }
@@ -517,8 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = (warp - 4) >> 2, ct = tid - 128;
             for (int q = 0; take(q, it); ++q) {
                 begin();
+                float all = 0.f;
                 for (int t = 0; t < it.n && alive; t += kC, ++ch) {
-                    const int n = min(kC, it.n - t), buf = ch % 3;
+                    const int n = min(kC, it.n - t), buf = ch & 3;
                     const Decays &tab = ctl.tab[ch & 1];
                     if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait(ctl.b.full[ch & 1], (ch >> 1) & 1))
                         break;
@@ -571,19 +582,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tst_wait();
                         before_sync();
                         arrive(ctl.b.wready[run & 1]);
+                        if (run == 1 && t > 0 && !update(ch - 1, all, true)) // the chunk before's sum, when it is there
+                            break;
                     }
                     arrive(ctl.vseen);
-                    if (!alive || !update(t))
+                    if (!alive)
                         break;
-                    // nobody looks at the marks of the chunk before any more: the products of this one waited for its outputs
-                    const int old = (ch + 2) % 3;
+                    // nobody looks at the marks of two chunks before any more: the products of the last waited for its outputs
+                    const int old = (ch + 2) & 3;
                     if (half == 0)
                         ctl.badfrom[old][ct] = kC;
                     if (ct == 0)
                         ctl.dirty[old] = 0;
+                    all = tab.all;
                     arrive(ctl.b.gempty[ch & 1]);
                 }
-                if (!alive)
+                if (!alive || !update(ch - 1, all, false))
                     break;
             }
         } else {
@@ -593,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 begin();
                 for (int t = 0; t < it.n && alive; t += kC, ++ch) {
                     const uint32_t par = ch & 1;
-                    const int n = min(kC, it.n - t), buf = ch % 3;
+                    const int n = min(kC, it.n - t), buf = ch & 3;
                     const Decays &tab = ctl.tab[ch & 1];
                     if (!wait(ctl.b.gfull[ch & 1], (ch >> 1) & 1) || !wait(ctl.qk, par))
                         break;
@@ -651,9 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tst_wait();
                     before_sync();
                     arrive(ctl.pready);
-                    if (!update(t))
-                        break;
-                    if (!wait(ctl.vseen, par) || !wait(ctl.odone, par)) // all of V was looked at, and read
+                    // all of V was looked at (waited for before the update, without which nobody goes on to the next chunk's)
+                    if (!wait(ctl.vseen, par) || !update(ch, tab.all, t + kC < it.n) || !wait(ctl.odone, par))
                         break;
                     after_sync();
                     const bool dirty = *reinterpret_cast<volatile int *>(&ctl.dirty[buf]) != 0;
@@ -945,8 +958,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (has) {
                 float *const to = p.state + ((size_t)it.at * a.hv + it.head) * DV * DK + (size_t)row * DK + quarter * WK;
 #pragma unroll
-                for (int k = 0; k < WK; k += 4)
-                    *reinterpret_cast<float4 *>(to + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
+                for (int k = 0; k < WK; k += 8)
+                    store8(to + k, &s[k]);
             }
             if (tid == 128)
                 p.decay[(size_t)it.at * a.hv + it.head] = total;

@@ -83,6 +83,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
     return *reinterpret_cast<float2 *>(&d);
 }
+// 32 bytes, a whole sector, at an address that is a multiple of it.  Where each lane of a warp has its own row, as with
+// tensor memory's, 16-byte halves of sectors go out, and come in, one by one.
+__device__ __forceinline__ void store8(float *p, const float *x)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+__device__ __forceinline__ void load8(const float *p, float *x)
+{
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+}
 // Two bf16: whether both are finite; with zeros in the place of those that are not.
 __device__ __forceinline__ bool finite2(uint32_t w)
 {

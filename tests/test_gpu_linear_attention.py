@@ -120,6 +120,21 @@ def test_tokens_behind_the_last_sequence_are_left_alone(gdn, dtype):
     assert (out[134:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pool_aligned_to_sixteen_bytes(gdn, dtype):
+    """A wrapped pool's memory need not be aligned to more."""
+    c = Case([1000, 40, 1], dtype, 1, 1, 64, 64, seed=13)
+    room = torch.empty(c.state.numel() + 4, device=DEV)
+    c.sd = room[4:].view(c.state.shape)
+    assert c.sd.data_ptr() % 32 == 16
+    c.sd.copy_(c.state)
+    c.check(prefill(gdn, c, gdn.GDNStatePool(c.sd.shape[0], 1, 1, 64, 64, tensor=c.sd)))
+    d = Case([1] * 3, dtype, 1, 1, 64, 64, seed=14)
+    d.sd = room[4:4 + d.state.numel()].view(d.state.shape)
+    d.sd.copy_(d.state)
+    d.check(decode(gdn, d, gdn.GDNStatePool(d.sd.shape[0], 1, 1, 64, 64, tensor=d.sd)))
+
+
 def test_prefill_is_decode_token_after_token(gdn):
     """fp32, and tokens of a sequence fed in two calls."""
     c = Case([37], "f32", 2, 2, 64, 64, seed=7)
