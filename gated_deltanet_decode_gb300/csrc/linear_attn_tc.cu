@@ -170,6 +170,9 @@ template <int DK, int DV> struct CGeo {
     static constexpr int WK = DK / 4;                 // a thread's columns of the state
 };
 
+// The waits go on in one place: where they did in line, the computing warps' loops left the instruction cache.
+__device__ __noinline__ bool wait_on(uint32_t b, uint32_t parity) { return mbar_wait(b, parity); }
+
 // What both kernels wait for each other with.
 struct Bars {
     unsigned long long ifull[kQueue], iempty[kQueue];
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool alive = true; // false once a bounded wait ran out
     auto wait_at = [&](uint32_t b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
-        if (!__all_sync(0xffffffffu, mbar_try(b, parity)) && alive && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
+        if (!__all_sync(0xffffffffu, mbar_try(b, parity)) && alive && !__all_sync(0xffffffffu, wait_on(b, parity))) {
             alive = false;
             report(a.err, GDN_DEVERR_TIMEOUT);
         }
@@ -678,12 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < HV; k += 32) {
                         uint32_t x[32];
                         tld(tmem + lanes + CO + hb * HV + k, x);
-                        if (dirty) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (ctl.badfrom[buf][hb * HV + k + e] <= row)
-                                    x[e] = 0x7fffffffu;
-                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t w[4];
@@ -692,6 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 w[z] = bf16_pair(__uint_as_float(x[8 * i + 2 * z]) * a.scale, __uint_as_float(x[8 * i + 2 * z + 1]) * a.scale);
                             *piece(row, k / 8 + i) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
+                    }
+                    if (dirty) {
+#pragma unroll 1
+                        for (int v = 0; v < HV; ++v)
+                            if (ctl.badfrom[buf][hb * HV + v] <= row)
+                                reinterpret_cast<unsigned short *>(piece(row, v >> 3))[v & 7] = 0x7fff;
                     }
                     before_sync();
                     arrive(ctl.ofree);                    if (n < kC) { // the last tokens of a sequence: the rows that there are, by this warp itself
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool alive = true; // false once a bounded wait ran out
     auto wait = [&](unsigned long long &b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
-        if (!__all_sync(0xffffffffu, mbar_try(bar(b), parity)) && alive && !__all_sync(0xffffffffu, mbar_wait(bar(b), parity))) {
+        if (!__all_sync(0xffffffffu, mbar_try(bar(b), parity)) && alive && !__all_sync(0xffffffffu, wait_on(bar(b), parity))) {
             alive = false;
             report(a.err, GDN_DEVERR_TIMEOUT);
         }
