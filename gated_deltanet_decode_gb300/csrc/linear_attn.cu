@@ -149,8 +149,8 @@ template <typename T, int DK, int R> __global__ void __launch_bounds__(kThreads)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % G::LPR;
     const int blocks = (p.dv + G::ROWS - 1) / G::ROWS;
     const int row_in = warp * G::RPW + lane / G::LPR;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     wait_prior_grid();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); // (the chunks' kernel goes on beside this one)
     const long long items = (long long)p.rows * p.hv * blocks;
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
         const int block = (int)(it % blocks), h = (int)(it / blocks % p.hv), r = (int)(it / blocks / p.hv);

@@ -11,8 +11,9 @@
 // with V kept transposed, and K transposed into Q's place for the last.  They run
 // on the tensor cores in tf32 with split operands (tf32_ops.cuh), eight warps as
 // 2 x 4 blocks of a result of 64 x 64.  In packed FMAs of 4 x 4 results a thread,
-// whose operands' loads took all of shared memory's bandwidth, the batch below
-// took XX us.
+// whose operands' loads took all of shared memory's bandwidth, five sequences of 200
+// to 900 tokens (8 heads of 64 x 64, fp32) took 71 us instead of 41, of which
+// the sums took 10, the scan 5 and the outputs 18; beside the serial kernel 31.
 //
 // Bound: latency.  A segment is mostly a single chunk; its loads, five barriers
 // and the products' chains follow each other, with one to two CTAs an SM.
@@ -153,7 +154,8 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
     // this warp's rows r0 .. + 32 of a result, and columns c0 .. + 8 N of VB, k0 .. + 16 of 64; this thread's place in them
     const int r0 = 32 * (warp >> 2), c0 = VB / 4 * (warp & 3), k0 = 16 * (warp & 3), g = lane >> 2, c = lane & 3;
     const int blocks = (a.dv + VB - 1) / VB;
-    wait_prior_grid();
+    if (!p.beside)
+        wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     ItemWalk<SUM> walk(p); // warp 0's is followed
     for (;;) {
@@ -316,6 +318,8 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                 p.decay[(size_t)it.at * a.hv + head] = total;
         }
     }
+    if (p.beside)
+        wait_prior_grid();
 }
 
 // Chunks a segment: one, unless that gives more CTAs than would stand on the GPU eight times over, and their states more
@@ -323,7 +327,8 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
 int segment_chunks(const LinearArgs &a, int vb)
 {
     const long long chunks = ((long long)a.total_tokens / kC + a.rows) * a.hv * ((a.dv + vb - 1) / vb);
-    return (int)((chunks + 8 * kSms - 1) / (8 * kSms));
+    const long long each = (chunks + 8 * kSms - 1) / (8 * kSms);
+    return (int)(each < kMostChunks ? each : kMostChunks);
 }
 
 template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s)
@@ -349,6 +354,7 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
     p.a = a;
     p.span = kC * segment_chunks(a, G::VB);
     p.least = kSerial;
+    p.beside = 1;
     p.heads = a.hv * ((a.dv + G::VB - 1) / G::VB);
     chunk_layout(p);
     const long long most = places(a.rows, a.total_tokens, p.span) * p.heads; // items
@@ -359,6 +365,7 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
             e = launch_scan(p, s);
         if (e != cudaSuccess)
             return e;
+        p.beside = 0;
     }
     return launch_pdl(linear_f32_kernel<T, DK, false>, grid, dim3(kThreads), (size_t)BYTES, s, p);
 }

@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    wait_prior_grid();
+    if (!p.beside)
+        wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true; // false once a bounded wait ran out
@@ -719,6 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     after_sync();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (p.beside)
+        wait_prior_grid();
 }
 
 // ---- the segments' own sums ----
@@ -778,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    wait_prior_grid();
+    if (!p.beside)
+        wait_prior_grid();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true; // false once a bounded wait ran out
@@ -973,6 +977,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     after_sync();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (p.beside)
+        wait_prior_grid();
 }
 
 // ---- host ----
@@ -991,7 +997,7 @@ int segment_chunks(int nseq, int tokens, int hv)
         if (cost < least)
             least = cost, best = segs > 1 ? len : 2 * m;
     }
-    return best < 4 ? 4 : best;
+    return best < 4 ? 4 : best < kMostChunks ? best : kMostChunks;
 }
 // [tokens][heads][d] bf16, boxes of 64 d of one head x kC tokens
 bool encode_tokens(CUtensorMap *m, const void *base, int d, int heads, int tokens, long long stride)
@@ -1034,6 +1040,7 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
     p.a = a;
     p.span = kC * segment_chunks(a.rows, a.total_tokens, a.hv);
     p.least = kSerial;
+    p.beside = 1;
     p.heads = a.hv;
     chunk_layout(p);
     const long long most = places(a.rows, a.total_tokens, p.span) * a.hv; // items
@@ -1044,6 +1051,7 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
             e = launch_scan(p, s);
         if (e != cudaSuccess)
             return e;
+        p.beside = 0;
     }
     return launch_pdl(linear_chunk_kernel<DK, DV>, grid, dim3(kThreads), (size_t)CHUNK, s, p, qmap, kmap, vmap, omap);
 }

@@ -17,12 +17,20 @@ namespace gdn {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kSerial = 32; // tokens up to which a sequence is the serial kernel's: a chunk takes the time of some tens of its steps
+constexpr int kMostChunks = 1 << 20; // of a segment: its tokens stay within an int
+// Tokens up to which a sequence is the serial kernel's: a chunk takes the time of some tens of its steps.  37 sequences of 12
+// (bf16, 16 heads of 128) take 33.9 us there and 44.3 in chunks, of 20 61.0 and 60.3, of 32 83.7 and 60.0; 4 sequences of 12
+// 11.3 and 13.6, of 24 17.4 and 13.6; in fp32 (8 heads of 64) 37 of 12 15.6 and 23.7, of 24 22.5 and 24.4, of 32 26.6 and 24.7.
+constexpr int kSerial = 20;
 
 struct ChunkArgs {
     LinearArgs a;
     int span;     // tokens a segment, whole chunks
     int least;    // sequences of more tokens than this are divided into segments; the others are the serial kernel's
+    // Whether the kernel runs beside the serial one before it, which shares no sequence with it and let it start when its own
+    // wait for the grid before was over; the kernel then waits at its end, so that who comes next has both behind it.  One after
+    // the other, five sequences of 200 to 900 tokens in fp32 take 39.1 us instead of 31.0, 37 of 1 to 9 in bf16 22.9 and 21.9.
+    int beside;
     int heads;    // value heads, or blocks of their rows where a CTA takes less than a head
     float *state; // [segments][hv][dv][dk]: a segment's sum, then the state after it (a sequence's last: the state before all)
     float *decay; // [segments][hv]: the segment's decay
@@ -168,8 +176,10 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkArgs p)
 
 inline cudaError_t launch_scan(const ChunkArgs &p, cudaStream_t s)
 {
-    const unsigned parts = ((unsigned)p.a.dv * p.a.dk + 1023) / 1024;
-    return launch_pdl(linear_scan_kernel, dim3((unsigned)p.a.rows * p.a.hv * parts), dim3(256), 0, s, p);
+    const long long blocks = (long long)p.a.rows * p.a.hv * ((p.a.dv * p.a.dk + 1023) / 1024);
+    if (blocks > 0x7fffffffll)
+        return cudaErrorInvalidConfiguration;
+    return launch_pdl(linear_scan_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p);
 }
 
 // The workspace: states, then decays.

@@ -406,7 +406,18 @@ int gdn_commit(int32_t *read_slot, int32_t *write_slot, int rows, void *stream);
  * write_slot[r] (twin) or read_slot[r] (in place).  An empty twin sequence
  * moves its state unchanged.  Tokens of no sequence are left alone; a sequence
  * whose range is outside [0, total_tokens] is a bad row.  Bad and padding
- * sequences' outputs are zero.  Slots of one call must not overlap. */
+ * sequences' outputs are zero.  Slots of one call must not overlap, and out
+ * shares no memory with the inputs.
+ *   workspace: device memory, 128-byte aligned, at least
+ *   linear_attention_prefill_workspace_bytes(...) bytes (which may be none),
+ *   its contents without meaning before and after; calls that overlap on the
+ *   GPU need their own
+ * Sequences of up to 20 tokens run token after token; longer ones in chunks,
+ * which group the same sums otherwise: the state is right to fp32 in either
+ * form; in bf16, with dk and dv 64 or 128, the weights of a chunk's own tokens
+ * and the state, as factors of the outputs, are rounded to bf16 once.  A value
+ * that is not finite makes what it reaches NaN: outputs of its own sequence
+ * (and value column, in v) from its token on, and the state. */
 int linear_attention_decode(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const float *log_decay, int decay_per_token, gdn_pool *pool,
                             const int32_t *read_slot, const int32_t *write_slot, float scale, void *out, int rows,
