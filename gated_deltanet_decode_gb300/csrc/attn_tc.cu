@@ -64,9 +64,6 @@ namespace {
 constexpr int kQueue = 4;   // items in flight between the walking warp and the others
 constexpr int kMeta = 16;   // key tiles whose valid-row count is kept; over a ring's tiles
 constexpr float kLazy = 8.f;
-// With shared prefixes, rows of a Q tile from which it comes by a tensor copy, whole: one warp's 16-byte copies take 4 us
-// for 128 rows, and a group's item, cut into many parts, has its Q in each of them.  A row of its own few rows copies those.
-constexpr int kCopyRows = 16;
 constexpr int kPairTokens = 1024; // and rows of new tokens of a key head from which items are pairs of tiles
 constexpr int kTmemCols = 512;
 
@@ -434,7 +431,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
             __syncwarp();
             mbar_wait(bar(ctl.drain), 0);
         } else {
-            // ---- Q tiles, by 16-byte asynchronous copies
+            // ---- Q tiles.  By 16-byte asynchronous copies; with shared prefixes by a tensor copy, as one warp's copies take 4 us
+            // for 128 rows, and a group's item, cut into many parts, has its Q in each of them (8 chunks of 64 tokens behind
+            // 4,000 shared ones: 57.1 us by copies, 40.8; 64 samples of 16,000: 44.5 and 43.7; 16 of 512: 16.4 and 15.6)
             unsigned qc = 0;
             for (int q = 0;; ++q) {
                 const int slot = q % kQueue;
@@ -451,45 +450,46 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1)
                     const int s = qc % G::NQ;
                     if (!wait(ctl.qempty[s], (qc / G::NQ + 1) & 1))
                         break;
-                    const int rows = (min(it.ntok - i * p.tq, p.tq)) * p.g;
-                    if constexpr (SH) {
-                        if (rows > kCopyRows) { // a tile at once, with the rows of other tokens behind the item's
-                            if (lane == 0) {
-                                mbar_arrive_tx(bar(ctl.qfull[s]), (uint32_t)(p.tq * p.g * D * 2));
-                                for (int c = 0; c < G::CH; ++c)
-                                    tma3(sbase + s * G::QBYTES + c * 128 * 128, &p.qmap, 64 * c, it.head * p.g, it.tok + i * p.tq,
-                                         bar(ctl.qfull[s]));
-                            }
-                            __syncwarp();
-                            continue;
+                    if constexpr (SH) { // a tile at once, with the rows of other tokens behind the item's
+                        if (lane == 0) {
+                            mbar_arrive_tx(bar(ctl.qfull[s]), (uint32_t)(p.tq * p.g * D * 2));
+                            for (int c = 0; c < G::CH; ++c)
+                                tma3(sbase + s * G::QBYTES + c * 128 * 128, &p.qmap, 64 * c, it.head * p.g, it.tok + i * p.tq,
+                                     bar(ctl.qfull[s]));
                         }
-                    }
-                    constexpr int VR = D / 8; // 16-byte vectors a row
-                    const bf16 *const src = static_cast<const bf16 *>(a.q) + (size_t)(it.tok + i * p.tq) * a.q_stride +
-                                            (size_t)it.head * p.g * D;
-                    const uint32_t dst = sbase + s * G::QBYTES;
-                    constexpr int RP = 32 / VR;                                // rows a pass
-                    const int vec = lane % VR;
-                    int row = lane / VR, tok = row / p.g, head = row - tok * p.g;
-                    const uint32_t at = dst + (vec >> 3) * 128 * 128;
+                        __syncwarp();
+                    } else {
+                        const int rows = (min(it.ntok - i * p.tq, p.tq)) * p.g;
+                        constexpr int VR = D / 8; // 16-byte vectors a row
+                        const bf16 *const src = static_cast<const bf16 *>(a.q) + (size_t)(it.tok + i * p.tq) * a.q_stride +
+                                                (size_t)it.head * p.g * D;
+                        const uint32_t dst = sbase + s * G::QBYTES;
+                        constexpr int RP = 32 / VR;                                // rows a pass
+                        const int vec = lane % VR;
+                        int row = lane / VR, tok = row / p.g, head = row - tok * p.g;
+                        const uint32_t at = dst + (vec >> 3) * 128 * 128;
 #pragma unroll 4
-                    for (; row < rows; row += RP) {
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         at + row * 128 + (((vec & 7) ^ (row & 7)) << 4)),
-                                     "l"(src + (size_t)tok * a.q_stride + head * D + vec * 8)
-                                     : "memory");
-                        for (head += RP; head >= p.g; head -= p.g)
-                            ++tok;
+                        for (; row < rows; row += RP) {
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             at + row * 128 + (((vec & 7) ^ (row & 7)) << 4)),
+                                         "l"(src + (size_t)tok * a.q_stride + head * D + vec * 8)
+                                         : "memory");
+                            for (head += RP; head >= p.g; head -= p.g)
+                                ++tok;
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        smem_to_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(ctl.qfull[s]));
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    smem_to_async();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar(ctl.qfull[s]));
                 }
                 if (!alive)
                     break;
             }
+            if constexpr (SH) // the last copies land before the CTA leaves, whoever still waits for them
+                for (unsigned i = qc > (unsigned)G::NQ ? qc - G::NQ : 0; i < qc; ++i)
+                    mbar_wait(bar(ctl.qfull[i % G::NQ]), (i / G::NQ) & 1);
         }
     } else {
         if constexpr (G::NO == 2)
@@ -800,8 +800,8 @@ bool encode_q(CUtensorMap *m, const AttentionArgs &a, int g, int tq)
 }
 
 // With shared prefixes an item is a single tile where pairs would be few: a group's item over long shared keys is cut into
-// many parts, and each costs its rows' partial sums.  Of 64 samples of a prompt of 16,000 (two tiles a key head) pairs take
-// 59.8 us, single tiles XX; prompts' chunks, whose tiles are many, are better off with pairs.
+// many parts, and each costs its rows' partial sums.  Of 64 samples of a prompt of 16,000 (288 rows a key head) pairs take
+// 44.8 us and single tiles 44.4; of 8 chunks of 64 tokens (2,048 rows) 41.0 and 45.5, of 512 tokens 205 and 279.
 bool single_tiles(int d, int g, int total_tokens, bool shared) { return d == 256 || (shared && total_tokens < kPairTokens / g); }
 
 int slot_rows(int d, int g, int total_tokens, bool shared)
