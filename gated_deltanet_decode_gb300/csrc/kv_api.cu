@@ -301,8 +301,8 @@ int paged_attention_shared(const void *q, int64_t q_stride, kv_page_pool *pool, 
                            int groups, const int32_t *prefix, float scale, void *out, int hq, int rows,
                            int total_tokens, void *workspace, size_t workspace_bytes, int dtype, void *stream)
 {
-    if (groups < 0 || groups > rows)
-        return api_fail(GDN_EINVAL, "groups=%d outside [0, rows=%d]", groups, rows);
+    if (groups < (rows > 0) || groups > rows)
+        return api_fail(GDN_EINVAL, "groups=%d for rows=%d: every row is in a group", groups, rows);
     if (total_tokens > 0 && (!bounds || !prefix))
         return api_fail(GDN_EINVAL, "bounds and prefix must be non-NULL");
     if (reinterpret_cast<uintptr_t>(prefix) & 7u)

@@ -31,7 +31,7 @@ def attention(L, h, **k):
 
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(pool=None), dict(table=None), dict(sl=None), dict(cu=None), dict(bounds=None),
-                                 dict(prefix=None), dict(prefix=FAKE + 4), dict(groups=-1), dict(groups=3), dict(out=None), dict(hq=3),
+                                 dict(prefix=None), dict(prefix=FAKE + 4), dict(groups=-1), dict(groups=0), dict(groups=3), dict(out=None), dict(hq=3),
                                  dict(layer=2), dict(rows=-1), dict(T=-1), dict(mp=0), dict(dtype=F32), dict(scale=0.0),
                                  dict(scale=float("nan")), dict(qs=500), dict(ws=None), dict(wb=100), dict(ws=FAKE + 8)])
 def test_attention_refusals(L, pool, bad):
