@@ -154,8 +154,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
     // this warp's rows r0 .. + 32 of a result, and columns c0 .. + 8 N of VB, k0 .. + 16 of 64; this thread's place in them
     const int r0 = 32 * (warp >> 2), c0 = VB / 4 * (warp & 3), k0 = 16 * (warp & 3), g = lane >> 2, c = lane & 3;
     const int blocks = (a.dv + VB - 1) / VB;
-    if (!p.beside)
-        wait_prior_grid();
+    begin_chunks(p);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     ItemWalk<SUM> walk(p); // warp 0's is followed
     for (;;) {

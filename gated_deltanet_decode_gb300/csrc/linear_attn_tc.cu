@@ -254,8 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    if (!p.beside)
-        wait_prior_grid();
+    begin_chunks(p);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true; // false once a bounded wait ran out
@@ -781,8 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    if (!p.beside)
-        wait_prior_grid();
+    begin_chunks(p);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true; // false once a bounded wait ran out

@@ -36,6 +36,14 @@ struct ChunkArgs {
     float *decay; // [segments][hv]: the segment's decay
 };
 
+__device__ __forceinline__ void begin_chunks(const ChunkArgs &p)
+{
+    if (!p.beside)
+        wait_prior_grid();
+    else // what came before the serial kernel is complete; this SM's L1 may hold lines of an older grid
+        __threadfence();
+}
+
 // A segment of a sequence and head.
 struct LItem {
     int tok, n, head; // first token, tokens (0: no more items), value head (or block)

@@ -215,6 +215,33 @@ def test_captured_and_on_another_stream(gdn):
         assert torch.equal(other, again)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[700], [5, 300, 1, 90]], ids=str)
+def test_calls_behind_one_another(gdn, dtype, lens):
+    """The kernels of a call run beside each other and are launched before those ahead of them end: calls that each read what
+    the one before wrote (states in place, values) give the same bits with and without a pause between them."""
+    c = Case(lens, dtype, 2, 2, 64, 64)
+    q, k, v, g = c.device_inputs()
+    cu, slots, one = i32(c.cu), i32(c.read), i32(c.read[:1])
+    k = k * 0.1
+
+    def run(pause):
+        pool, x, outs = c.pool(gdn), v.clone(), []
+        for _ in range(12):
+            x = gdn.linear_attention_prefill(q, k, x, g, pool, cu, slots, keep_in_place=True)
+            pause()
+            outs.append(gdn.linear_attention_decode(q[:1], k[:1], x[:1], g[:1], pool, one, keep_in_place=True))
+            pause()
+        torch.cuda.synchronize()
+        return torch.cat([o.flatten() for o in outs] + [x.flatten()]), c.sd
+
+    a, s = run(torch.cuda.synchronize)
+    assert torch.isfinite(a).all()
+    for _ in range(3):
+        b, t = run(lambda: None)
+        assert torch.equal(a, b) and torch.equal(s, t)
+
+
 def test_python_refusals(gdn):
     c = Case([3, 2], "bf16", 1, 2, 64, 64)
     pool = c.pool(gdn)
