@@ -13,7 +13,7 @@
 // 2 x 4 blocks of a result of 64 x 64.  In packed FMAs of 4 x 4 results a thread,
 // whose operands' loads took all of shared memory's bandwidth, five sequences of 200
 // to 900 tokens (8 heads of 64 x 64, fp32) took 71 us instead of 41, of which
-// the sums took 10, the scan 5 and the outputs 18; beside the serial kernel 31.
+// the sums took 10, the scan 5 and the outputs 18; with the kernels beside each other 30.
 //
 // Bound: latency.  A segment is mostly a single chunk; its loads, five barriers
 // and the products' chains follow each other, with one to two CTAs an SM.
@@ -154,8 +154,12 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
     // this warp's rows r0 .. + 32 of a result, and columns c0 .. + 8 N of VB, k0 .. + 16 of 64; this thread's place in them
     const int r0 = 32 * (warp >> 2), c0 = VB / 4 * (warp & 3), k0 = 16 * (warp & 3), g = lane >> 2, c = lane & 3;
     const int blocks = (a.dv + VB - 1) / VB;
-    begin_chunks(p);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_chunks();
+    if (SUM && p.rare && !any_cut(p)) {
+        wait_prior_grid();
+        return;
+    }
     ItemWalk<SUM> walk(p); // warp 0's is followed
     for (;;) {
         __syncthreads();
@@ -174,6 +178,8 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
         // the state
         {
             const float *const from = SUM ? nullptr : it.from < 0 ? a.pool + slot * it.rs + mine : p.state + slot * it.from + mine;
+            if (!SUM && it.from >= 0)
+                wait_prior_grid(); // the scan
             for (int x = tid; x < VB * (DK / 4); x += kThreads) {
                 const int v = x / (DK / 4), k = 4 * (x - v * (DK / 4));
                 *reinterpret_cast<float4 *>(sm + G::S + v * LD + k) =
@@ -317,17 +323,28 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                 p.decay[(size_t)it.at * a.hv + head] = total;
         }
     }
-    if (p.beside)
-        wait_prior_grid();
+    wait_prior_grid();
 }
 
-// Chunks a segment: one, unless that gives more CTAs than would stand on the GPU eight times over, and their states more
-// room than they save time.
-int segment_chunks(const LinearArgs &a, int vb)
+// Chunks a segment, as in linear_attn_tc.cu: the fewest rounds of CTAs, in chunks, where a segment costs half a chunk's time to
+// begin and a chunk a quarter of its time in the sums.  Against a chunk a segment (several only where that gave 8 x 152 CTAs): a
+// sequence of 16,000 (8 heads of 64) takes 157 us instead of 177, of 4,000 47 instead of 57, 64 of 200 125 instead of 146, 8 of
+// 2,000 with 32 heads of 128 2.1 ms instead of 2.6; 32 of 100 to 900 153 instead of 143.
+int segment_chunks(const LinearArgs &a, bool &cut)
 {
-    const long long chunks = ((long long)a.total_tokens / kC + a.rows) * a.hv * ((a.dv + vb - 1) / vb);
-    const long long each = (chunks + 8 * kSms - 1) / (8 * kSms);
-    return (int)(each < kMostChunks ? each : kMostChunks);
+    const int vb = a.dk == 256 ? FGeo<256>::VB : FGeo<128>::VB, at_once = kSms * (a.dk > 64 ? 1 : 2);
+    const long long m = ((long long)a.total_tokens + (long long)a.rows * kC - 1) / ((long long)a.rows * kC); // chunks a sequence
+    const long long blocks = (long long)a.rows * a.hv * ((a.dv + vb - 1) / vb);
+    long long best = m;
+    double least = 1e30;
+    for (int cuts = 1; cuts <= m && cuts <= 2 * at_once; ++cuts) {
+        const long long len = (m + cuts - 1) / cuts, segs = (m + len - 1) / len;
+        auto rounds = [&](long long n) { return (double)((n * blocks + at_once - 1) / at_once); };
+        const double cost = rounds(segs) * (len + 0.5) + (segs > 1 ? rounds(segs - 1) * (0.25 * len + 0.5) + 1 : 0);
+        if (cost < least)
+            least = cost, cut = segs > 1, best = len;
+    }
+    return (int)(best < kMostChunks ? best : kMostChunks);
 }
 
 template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s)
@@ -351,9 +368,10 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
     }
     ChunkArgs p;
     p.a = a;
-    p.span = kC * segment_chunks(a, G::VB);
+    bool cut = false;
+    p.span = kC * segment_chunks(a, cut);
+    p.rare = !cut;
     p.least = kSerial;
-    p.beside = 1;
     p.heads = a.hv * ((a.dv + G::VB - 1) / G::VB);
     chunk_layout(p);
     const long long most = places(a.rows, a.total_tokens, p.span) * p.heads; // items
@@ -364,7 +382,6 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
             e = launch_scan(p, s);
         if (e != cudaSuccess)
             return e;
-        p.beside = 0;
     }
     return launch_pdl(linear_f32_kernel<T, DK, false>, grid, dim3(kThreads), (size_t)BYTES, s, p);
 }
@@ -397,7 +414,8 @@ size_t linear_prefill_workspace_bytes(const LinearArgs &a, int dtype)
         return 0;
     if (on_tensor_cores(a, dtype))
         return linear_chunked_workspace_bytes(a);
-    const long long span = (long long)kC * segment_chunks(a, a.dk == 256 ? FGeo<256>::VB : FGeo<128>::VB);
+    bool cut;
+    const long long span = (long long)kC * segment_chunks(a, cut);
     return a.total_tokens > span ? chunk_bytes(a, span) : 0;
 }
 

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             report(a.err, GDN_DEVERR_TIMEOUT);
         return;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -254,8 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    begin_chunks(p);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_chunks();
 
     bool alive = true; // false once a bounded wait ran out
     auto wait_at = [&](uint32_t b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
@@ -480,6 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto begin = [&] { // an item: its state
             const size_t slot = (size_t)a.hv * DV * DK, mine = (size_t)it.head * DV * DK + (size_t)row * DK + quarter * WK;
             const float *const from = it.from < 0 ? a.pool + slot * it.rs + mine : p.state + slot * it.from + mine;
+            if (it.from >= 0)
+                wait_prior_grid(); // the scan
 #pragma unroll
             for (int k = 0; k < WK; k += 8) {
 #pragma unroll
@@ -719,8 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     after_sync();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    if (p.beside)
-        wait_prior_grid();
+    wait_prior_grid();
 }
 
 // ---- the segments' own sums ----
@@ -759,6 +760,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             report(a.err, GDN_DEVERR_TIMEOUT);
         return;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.rare && !any_cut(p)) {
+        wait_prior_grid();
+        return;
+    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -780,8 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    begin_chunks(p);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_chunks();
 
     bool alive = true; // false once a bounded wait ran out
     auto wait = [&](unsigned long long &b, uint32_t parity) { // by a whole warp, which goes on or leaves as one
@@ -975,15 +980,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     after_sync();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    if (p.beside)
-        wait_prior_grid();
+    wait_prior_grid();
 }
 
 // ---- host ----
 // Chunks a segment, from what the host knows (the lengths are on the device; sequences are taken as equal): the fewest
 // rounds of CTAs, in chunks, where a segment costs one more to begin, and forming the sums half a chunk's time.  Uncut,
 // sequences of up to twice their mean length and of four chunks stay whole: a short piece too many is a round too many.
-int segment_chunks(int nseq, int tokens, int hv)
+// One of 16,000 tokens (16 heads of 128) takes 95 us, whole 410; 2 of 4,000 64 and 115; one of 1,000 27 and 35; 8 of 1,500 to
+// 2,600, whole, 92, and 174 where those over the mean are cut.
+int segment_chunks(int nseq, int tokens, int hv, bool &cut)
 {
     const int m = (int)(((long long)tokens + (long long)nseq * kC - 1) / ((long long)nseq * kC)); // chunks a sequence
     int best = m;
@@ -993,9 +999,9 @@ int segment_chunks(int nseq, int tokens, int hv)
         auto rounds = [&](long long n) { return (double)((n * nseq * hv + kSms - 1) / kSms); };
         const double cost = rounds(segs) * (len + 1) + (segs > 1 ? rounds(segs - 1) * (0.5 * len + 1) + 3 : 0);
         if (cost < least)
-            least = cost, best = segs > 1 ? len : 2 * m;
+            least = cost, cut = segs > 1, best = cut ? len : 2 * m > 4 ? 2 * m : 4;
     }
-    return best < 4 ? 4 : best < kMostChunks ? best : kMostChunks;
+    return best < kMostChunks ? best : kMostChunks;
 }
 // [tokens][heads][d] bf16, boxes of 64 d of one head x kC tokens
 bool encode_tokens(CUtensorMap *m, const void *base, int d, int heads, int tokens, long long stride)
@@ -1036,9 +1042,10 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     ChunkArgs p;
     p.a = a;
-    p.span = kC * segment_chunks(a.rows, a.total_tokens, a.hv);
+    bool cut = false;
+    p.span = kC * segment_chunks(a.rows, a.total_tokens, a.hv, cut);
+    p.rare = !cut;
     p.least = kSerial;
-    p.beside = 1;
     p.heads = a.hv;
     chunk_layout(p);
     const long long most = places(a.rows, a.total_tokens, p.span) * a.hv; // items
@@ -1049,7 +1056,6 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
             e = launch_scan(p, s);
         if (e != cudaSuccess)
             return e;
-        p.beside = 0;
     }
     return launch_pdl(linear_chunk_kernel<DK, DV>, grid, dim3(kThreads), (size_t)CHUNK, s, p, qmap, kmap, vmap, omap);
 }
@@ -1058,7 +1064,8 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
 
 size_t linear_chunked_workspace_bytes(const LinearArgs &a)
 {
-    const int span = kC * segment_chunks(a.rows, a.total_tokens, a.hv);
+    bool cut;
+    const int span = kC * segment_chunks(a.rows, a.total_tokens, a.hv, cut);
     return a.total_tokens > span ? chunk_bytes(a, span) : 0;
 }
 

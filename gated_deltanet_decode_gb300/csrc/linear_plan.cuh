@@ -27,21 +27,24 @@ struct ChunkArgs {
     LinearArgs a;
     int span;     // tokens a segment, whole chunks
     int least;    // sequences of more tokens than this are divided into segments; the others are the serial kernel's
-    // Whether the kernel runs beside the serial one before it, which shares no sequence with it and let it start when its own
-    // wait for the grid before was over; the kernel then waits at its end, so that who comes next has both behind it.  One after
-    // the other, five sequences of 200 to 900 tokens in fp32 take 39.1 us instead of 31.0, 37 of 1 to 9 in bf16 22.9 and 21.9.
-    int beside;
+    // Whether the host expects no sequence of several segments.  The sums' kernel and the scan, there for a long sequence among
+    // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 91.6 us, without the look 94.5, and 87.4
+    // without the two kernels; 8 of 300 26.9, 30.6 and 23.7.
+    int rare;
     int heads;    // value heads, or blocks of their rows where a CTA takes less than a head
     float *state; // [segments][hv][dv][dk]: a segment's sum, then the state after it (a sequence's last: the state before all)
     float *decay; // [segments][hv]: the segment's decay
 };
 
-__device__ __forceinline__ void begin_chunks(const ChunkArgs &p)
+// The kernels of a call run beside each other as far as they can: each lets the next one start at once, but for the serial one,
+// which does so when its own wait for the grid before is over.  What came before the call is complete then, and of the call's
+// own kernels only the scan reads what another one wrote (the sums), and then the segments that begin with the scan's states:
+// those wait, a sequence of a single segment does not.  Every kernel waits at its end at the latest, so that who comes next
+// has all of them behind it.  One after the other, a sequence of 16,000 tokens (bf16, 16 heads of 128) takes 99.6 us instead of
+// 95.0, five of 200 to 900 in fp32 (8 heads of 64) 39.1 instead of 30.0, 37 of 1 to 9 in bf16 22.9 instead of 21.9.
+__device__ __forceinline__ void begin_chunks()
 {
-    if (!p.beside)
-        wait_prior_grid();
-    else // what came before the serial kernel is complete; this SM's L1 may hold lines of an older grid
-        __threadfence();
+    __threadfence(); // this SM's L1 may hold lines of a grid before the call
 }
 
 // A segment of a sequence and head.
@@ -67,6 +70,16 @@ __device__ __forceinline__ int segments(const ChunkArgs &p, int r, int &b, int &
 // The workspace's places of a sequence's segments begin at its first token's
 // place over a segment's length and one a sequence before it, so no two meet.
 __device__ __forceinline__ int first_place(const ChunkArgs &p, int b, int r) { return b / p.span + r; }
+// Whether a sequence has several segments.  By all threads of a CTA.
+__device__ __forceinline__ bool any_cut(const ChunkArgs &p)
+{
+    int any = 0;
+    for (int r = threadIdx.x; r < p.a.rows; r += blockDim.x) {
+        int b, n, rs, ws;
+        any |= segments(p, r, b, n, rs, ws) > 1;
+    }
+    return __syncthreads_or(any);
+}
 inline long long places(int nseq, int tokens, long long span) { return tokens / span + nseq + 1; }
 
 // The items of a CTA: number blockIdx.x and every gridDim.x-th on, heads of a
@@ -150,44 +163,48 @@ __device__ __forceinline__ float ex2(float x)
 // in their places: a thread four floats of a (sequence, head).
 __global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkArgs p)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     wait_prior_grid();
-    const int floats = p.a.dv * p.a.dk, parts = (floats + 1023) / 1024;
-    const int part = blockIdx.x % parts, x = blockIdx.x / parts, h = x % p.a.hv, r = x / p.a.hv;
-    int b, n, rs, ws;
-    const int segs = segments(p, r, b, n, rs, ws);
-    if (segs < 2 || part * 1024 + 4 * (int)threadIdx.x >= floats)
+    if (p.rare && !any_cut(p))
         return;
-    const size_t slot = (size_t)p.a.hv * floats, mine = (size_t)h * floats + part * 1024 + 4 * threadIdx.x;
-    const size_t place = first_place(p, b, r);
-    float4 s = *reinterpret_cast<const float4 *>(p.a.pool + slot * rs + mine);
-    // (the first segment takes its state from the last one's place: in place, the slot is written by the last segment)
-    *reinterpret_cast<float4 *>(p.state + slot * (place + segs - 1) + mine) = s;
-    constexpr int U = 4; // segments under way
-    for (int i0 = 0; i0 < segs - 1; i0 += U) {
-        float4 y[U];
-        float f[U];
+    const int floats = p.a.dv * p.a.dk, parts = (floats + 1023) / 1024;
+    for (long long at = blockIdx.x; at < (long long)p.a.rows * p.a.hv * parts; at += gridDim.x) {
+        const int part = (int)(at % parts), x = (int)(at / parts), h = x % p.a.hv, r = x / p.a.hv;
+        int b, n, rs, ws;
+        const int segs = segments(p, r, b, n, rs, ws);
+        if (segs < 2 || part * 1024 + 4 * (int)threadIdx.x >= floats)
+            continue;
+        const size_t slot = (size_t)p.a.hv * floats, mine = (size_t)h * floats + part * 1024 + 4 * threadIdx.x;
+        const size_t place = first_place(p, b, r);
+        float4 s = *reinterpret_cast<const float4 *>(p.a.pool + slot * rs + mine);
+        // (the first segment takes its state from the last one's place: in place, the slot is written by the last segment)
+        *reinterpret_cast<float4 *>(p.state + slot * (place + segs - 1) + mine) = s;
+        constexpr int U = 4; // segments under way
+        for (int i0 = 0; i0 < segs - 1; i0 += U) {
+            float4 y[U];
+            float f[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < segs - 1) {
-                y[u] = *reinterpret_cast<const float4 *>(p.state + slot * (place + i0 + u) + mine);
-                f[u] = p.decay[(place + i0 + u) * p.a.hv + h];
-            }
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < segs - 1) {
+                    y[u] = *reinterpret_cast<const float4 *>(p.state + slot * (place + i0 + u) + mine);
+                    f[u] = p.decay[(place + i0 + u) * p.a.hv + h];
+                }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < segs - 1) {
-                s.x = fmaf(s.x, f[u], y[u].x), s.y = fmaf(s.y, f[u], y[u].y);
-                s.z = fmaf(s.z, f[u], y[u].z), s.w = fmaf(s.w, f[u], y[u].w);
-                *reinterpret_cast<float4 *>(p.state + slot * (place + i0 + u) + mine) = s;
-            }
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < segs - 1) {
+                    s.x = fmaf(s.x, f[u], y[u].x), s.y = fmaf(s.y, f[u], y[u].y);
+                    s.z = fmaf(s.z, f[u], y[u].z), s.w = fmaf(s.w, f[u], y[u].w);
+                    *reinterpret_cast<float4 *>(p.state + slot * (place + i0 + u) + mine) = s;
+                }
+        }
     }
 }
 
 inline cudaError_t launch_scan(const ChunkArgs &p, cudaStream_t s)
 {
     const long long blocks = (long long)p.a.rows * p.a.hv * ((p.a.dv * p.a.dk + 1023) / 1024);
-    if (blocks > 0x7fffffffll)
-        return cudaErrorInvalidConfiguration;
-    return launch_pdl(linear_scan_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p);
+    const long long most = (p.rare ? 1 : 4) * kSms;
+    return launch_pdl(linear_scan_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s, p);
 }
 
 // The workspace: states, then decays.
