@@ -1019,6 +1019,8 @@ def _linear_args(q, k, v, log_decay, pool: GDNStatePool, out):
     dev, dt = pool.tensor.device, q.dtype
     _dtype_code(dt)
     T = q.shape[0]
+    if T > 0x7FFFFFFF:
+        raise ValueError(f"{T} tokens are more than a call takes")
 
     def rows(x, heads, d, what):
         shape, st = x.shape, x.stride()

@@ -258,23 +258,24 @@ __device__ RunOf<V> plan_run(const Args &p, int mt, long long *part, FoundOf<V> 
     const int count = V::count(p), heads = p.a.pages.hkv * p.groups, tid = threadIdx.x;
     typename V::RowT x = {};
     long long per = 0, items = 0; // units of the tiles of a key head of this thread's row, and its items
+    long long cost = 0;
     auto look = [&](int r) {
-        per = items = 0;
+        per = items = cost = 0;
         if (r >= count)
             return;
         x = V::get(p, r);
         if (x.live) {
             per = head_units<Cost, V>(x, mt, KT, p.g);
+            cost = per * heads;
             if (Cost::item)
                 items = items_of(x, mt);
         }
     };
     int dearest = 1; // tile of this thread's rows
     RunOf<V> run;
-    long long total = 0, begun = 0, cost = 0, before = 0, sum, n0 = 0, n;
+    long long total = 0, begun = 0, before = 0, sum, n0 = 0, n;
     for (int b = 0; b < count; b += THREADS) {
         look(b + tid);
-        cost = per * heads;
         if (cost > 0)
             dearest = max(dearest, Cost::of(min(x.n, mt) * p.g));
         if (x.bad && blockIdx.x == 0)
@@ -298,8 +299,10 @@ __device__ RunOf<V> plan_run(const Args &p, int mt, long long *part, FoundOf<V> 
     run.u0 = run.share * blockIdx.x;
     run.u1 = min(total, run.u0 + run.share);
     auto weigh = [&] {
-        per += run.item * items;
-        cost = per * heads;
+        if constexpr (Cost::item != 0) {
+            per += run.item * items;
+            cost = per * heads;
+        }
     };
     if (count <= THREADS) { // the one pass has it
         weigh();
@@ -392,8 +395,14 @@ template <typename Cost, typename V, typename Args> struct Walk {
                     break;
                 rem -= units;
             }
-            ja = tile_from(rem, unit());
-            u += tile_begin(ja, unit()) - rem; // a tile that began before u0 is the run's before
+            // a tile that began before u0 is the run's before
+            if constexpr (Cost::item == 0) {
+                ja = (int)((rem + unit() - 1) / unit());
+                u += (long long)ja * unit() - rem;
+            } else {
+                ja = tile_from(rem, unit());
+                u += tile_begin(ja, unit()) - rem;
+            }
             if (ja == item_tiles<V>(x, t, mt, kt))
                 done();
         }
@@ -405,7 +414,7 @@ template <typename Cost, typename V, typename Args> struct Walk {
     __device__ int tile_from(long long at, int w) const
     {
         const int j = (int)((at - extra() + w - 1) / w);
-        return Cost::item == 0 ? j : at <= 0 ? 0 : max(1, j);
+        return at <= 0 ? 0 : max(1, j);
     }
     __device__ int unit() const { return Cost::of(min(mt, x.n - t * mt) * p.g); }
     __device__ void done() // with item t
@@ -478,7 +487,10 @@ template <typename Cost, typename V, typename Args> struct Walk {
             if (lane == 0 && ja > 0 && start >= run.u0 - run.share)
                 p.cuts[blockIdx.x] = {2 + (int)((start + (J - 1ll) * w) / run.share) - (int)blockIdx.x, x.b + t0, ntok, h};
         }
-        u = start + tile_begin(jb, w);
+        if constexpr (Cost::item == 0)
+            u += (long long)(jb - ja) * w;
+        else
+            u = start + tile_begin(jb, w);
         done();
         return true;
     }
@@ -488,7 +500,7 @@ template <typename Cost, typename V, typename Args> struct Walk {
 // `row` of the item's tiles) of a partial item writes.
 __device__ __forceinline__ size_t part_row(const WorkArgs &p, const Item &it, int, int, int row)
 {
-    return (size_t)max(it.part, 0) * p.rows_max + row;
+    return (size_t)it.part * p.rows_max + row;
 }
 __device__ __forceinline__ size_t part_row(const SharedArgs &p, const SharedItem &it, int tok, int head, int row)
 {

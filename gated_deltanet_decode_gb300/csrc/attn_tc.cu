@@ -68,7 +68,8 @@ constexpr int kPairTokens = 1024; // and rows of new tokens of a key head from w
 constexpr int kTmemCols = 512;
 
 // Rows' own keys behind shared prefixes make items of a few tiles, of which each takes about as long as three tiles to begin
-// and to end (its copies' latency, and sums that are not ready before their products).
+// and to end (its copies' latency, and sums that are not ready before their products): 64 samples of 16,000 tokens took 43.2 us,
+// with two tiles 45.2, with five 51.0.
 struct SharedCost : EvenCost {
     static constexpr int item = 3;
 };

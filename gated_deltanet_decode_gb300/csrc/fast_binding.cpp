@@ -335,7 +335,7 @@ struct Linear {
           k(tensor(a[1]), s.dk, type, s.device), v(tensor(a[2]), s.dv, type, s.device)
     {
         if ((type != at::kFloat && type != at::kBFloat16) || !current(s.device) || !q.ok || !k.ok || !v.ok || q.heads != s.hk ||
-            k.heads != s.hk || v.heads != s.hv || k.tokens != q.tokens || v.tokens != q.tokens)
+            k.heads != s.hk || v.heads != s.hv || k.tokens != q.tokens || v.tokens != q.tokens || q.tokens > 0x7fffffff)
             return;
         code = type == at::kBFloat16 ? GDN_BF16 : GDN_F32;
         const at::Tensor *g = tensor(a[3]);

@@ -597,6 +597,8 @@ cudaError_t launch_pages_shared(const CacheRows &c, const int32_t *bounds, int g
     // CTAs a group: 32 groups of 32 rows over 1,000 to 16,000 tokens (pages of 16) take 15.2 us with one, 10.0 with two, 6.8
     // with four, 5.1 with eight; one group of 16 rows over 512 3.9 with one, 3.3 with eight.
     constexpr unsigned kCluster = 8;
+    if (groups > (int)(0x7fffffff / kCluster))
+        return cudaErrorInvalidConfiguration;
     int shift = 0;
     while ((1 << shift) < page_size)
         ++shift;

@@ -225,21 +225,30 @@ def test_calls_behind_one_another(gdn, dtype, lens):
     cu, slots, one = i32(c.cu), i32(c.read), i32(c.read[:1])
     k = k * 0.1
 
-    def run(pause):
-        pool, x, outs = c.pool(gdn), v.clone(), []
+    def run(pool, pause):
+        x, outs = v.clone(), []
         for _ in range(12):
             x = gdn.linear_attention_prefill(q, k, x, g, pool, cu, slots, keep_in_place=True)
             pause()
             outs.append(gdn.linear_attention_decode(q[:1], k[:1], x[:1], g[:1], pool, one, keep_in_place=True))
             pause()
-        torch.cuda.synchronize()
-        return torch.cat([o.flatten() for o in outs] + [x.flatten()]), c.sd
+        return torch.cat([o.flatten() for o in outs] + [x.flatten()])
 
-    a, s = run(torch.cuda.synchronize)
+    a = run(c.pool(gdn), torch.cuda.synchronize)
+    s = c.sd
     assert torch.isfinite(a).all()
     for _ in range(3):
-        b, t = run(lambda: None)
-        assert torch.equal(a, b) and torch.equal(s, t)
+        b = run(c.pool(gdn), lambda: None)
+        assert torch.equal(a, b) and torch.equal(s, c.sd)
+    pool = c.pool(gdn)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b = run(pool, lambda: None)
+    for _ in range(3):
+        c.sd.copy_(c.state)
+        graph.replay()
+        assert torch.equal(a, b) and torch.equal(s, c.sd)
 
 
 def test_python_refusals(gdn):
@@ -254,6 +263,8 @@ def test_python_refusals(gdn):
         gdn.linear_attention_prefill(**a)
 
     call()
+    with pytest.raises(ValueError, match="more than a call takes"):
+        call(q=q[:1].expand(2 ** 31, -1, -1))
     for wrong in (dict(q=q[:, :, :32]), dict(k=k[:4]), dict(v=v.transpose(1, 2)), dict(log_decay=g[:, :1]), dict(log_decay=g[None]),
                   dict(read_slot=read[:1]), dict(q=q.cpu()), dict(out=torch.empty(4, 2, 64, dtype=torch.bfloat16, device=DEV))):
         with pytest.raises((ValueError, gdn.GDNError)):
