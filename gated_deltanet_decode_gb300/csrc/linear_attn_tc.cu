@@ -795,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
+    // (now, with tensor memory taken: a CTA of the last kernel may hold an SM's while it waits for the scan, and so for this grid)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true; // false once a bounded wait ran out
@@ -997,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rounds of CTAs, in chunks, where a segment costs one more to begin, and forming the sums half a chunk's time.  Uncut,
 // sequences of up to twice their mean length and of four chunks stay whole: a short piece too many is a round too many.
 // One of 16,000 tokens (16 heads of 128) takes 95 us, whole 410; 2 of 4,000 64 and 115; one of 1,000 27 and 35; 8 of 1,500 to
-// 2,600, whole, 92, and 174 where those over the mean are cut.
+// 2,600, whole, 93, and 174 where those over the mean are cut.
 int segment_chunks(int nseq, int tokens, int hv, bool &cut)
 {
     const int m = (int)(((long long)tokens + (long long)nseq * kC - 1) / ((long long)nseq * kC)); // chunks a sequence

@@ -28,8 +28,8 @@ struct ChunkArgs {
     int span;     // tokens a segment, whole chunks
     int least;    // sequences of more tokens than this are divided into segments; the others are the serial kernel's
     // Whether the host expects no sequence of several segments.  The sums' kernel and the scan, there for a long sequence among
-    // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 91.6 us, without the look 94.5, and 87.4
-    // without the two kernels; 8 of 300 26.9, 30.6 and 23.7.
+    // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 92.7 us, without the look 94.5, and 87.4
+    // without the two kernels; 8 of 300 27.4, 30.6 and 23.7.
     int rare;
     int heads;    // value heads, or blocks of their rows where a CTA takes less than a head
     float *state; // [segments][hv][dv][dk]: a segment's sum, then the state after it (a sequence's last: the state before all)
