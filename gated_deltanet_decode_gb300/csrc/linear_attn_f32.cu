@@ -156,7 +156,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
     const int blocks = (a.dv + VB - 1) / VB;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     begin_chunks();
-    if (SUM && p.rare && !any_cut(p)) {
+    if (SUM ? p.rare && !any_with(p, 2) : p.none && !any_with(p, 1)) {
         wait_prior_grid();
         return;
     }
@@ -371,6 +371,7 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
     bool cut = false;
     p.span = kC * segment_chunks(a, cut);
     p.rare = !cut;
+    p.none = a.total_tokens <= (long long)kSerial * a.rows;
     p.least = kSerial;
     p.heads = a.hv * ((a.dv + G::VB - 1) / G::VB);
     chunk_layout(p);

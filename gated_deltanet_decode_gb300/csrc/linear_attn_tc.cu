@@ -231,6 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             report(a.err, GDN_DEVERR_TIMEOUT);
         return;
     }
+    begin_chunks();
+    if (p.none && !any_with(p, 1)) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        wait_prior_grid();
+        return;
+    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -262,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     after_sync();
     const uint32_t tmem = ctl.tmem;
-    begin_chunks();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     bool alive = true; // false once a bounded wait ran out
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     begin_chunks();
-    if (p.rare && !any_cut(p)) {
+    if (p.rare && !any_with(p, 2)) {
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         wait_prior_grid();
         return;
@@ -1055,6 +1060,7 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
     bool cut = false;
     p.span = kC * segment_chunks(a.rows, a.total_tokens, a.hv, cut);
     p.rare = !cut;
+    p.none = a.total_tokens <= (long long)kSerial * a.rows;
     p.least = kSerial;
     p.heads = a.hv;
     chunk_layout(p);

@@ -19,8 +19,8 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kMostChunks = 1 << 20; // of a segment: its tokens stay within an int
 // Tokens up to which a sequence is the serial kernel's: a chunk takes the time of some tens of its steps.  37 sequences of 12
-// (bf16, 16 heads of 128) take 33.9 us there and 44.3 in chunks, of 20 61.0 and 60.3, of 32 83.7 and 60.0; 4 sequences of 12
-// 11.3 and 13.6, of 24 17.4 and 13.6; in fp32 (8 heads of 64) 37 of 12 15.6 and 23.7, of 24 22.5 and 24.4, of 32 26.6 and 24.7.
+// (bf16, 16 heads of 128) take 31.8 us there and 44.3 in chunks, of 20 49.6 and 60.3, of 32 83.7 and 60.0; 4 sequences of 12
+// 7.7 and 13.6, of 24 17.4 and 13.6; in fp32 (8 heads of 64) 37 of 12 15.6 and 23.7, of 24 22.5 and 24.4, of 32 26.6 and 24.7.
 constexpr int kSerial = 20;
 
 struct ChunkArgs {
@@ -31,6 +31,9 @@ struct ChunkArgs {
     // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 92.7 us, without the look 94.5, and 87.4
     // without the two kernels; 8 of 300 27.4, 30.6 and 23.7.
     int rare;
+    // Whether it expects no sequence for the chunks at all, by the mean: their kernel then looks before it sets up.  37
+    // sequences of 1 to 9 tokens take 20.4 us, without the look 22.2, 4 of 12 7.7 and 10.1; with chunks to do it costs 0.5.
+    int none;
     int heads;    // value heads, or blocks of their rows where a CTA takes less than a head
     float *state; // [segments][hv][dv][dk]: a segment's sum, then the state after it (a sequence's last: the state before all)
     float *decay; // [segments][hv]: the segment's decay
@@ -70,13 +73,13 @@ __device__ __forceinline__ int segments(const ChunkArgs &p, int r, int &b, int &
 // The workspace's places of a sequence's segments begin at its first token's
 // place over a segment's length and one a sequence before it, so no two meet.
 __device__ __forceinline__ int first_place(const ChunkArgs &p, int b, int r) { return b / p.span + r; }
-// Whether a sequence has several segments.  By all threads of a CTA.
-__device__ __forceinline__ bool any_cut(const ChunkArgs &p)
+// Whether a sequence has `most` segments or more.  By all threads of a CTA.
+__device__ __forceinline__ bool any_with(const ChunkArgs &p, int most)
 {
     int any = 0;
     for (int r = threadIdx.x; r < p.a.rows; r += blockDim.x) {
         int b, n, rs, ws;
-        any |= segments(p, r, b, n, rs, ws) > 1;
+        any |= segments(p, r, b, n, rs, ws) >= most;
     }
     return __syncthreads_or(any);
 }
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkArgs p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     wait_prior_grid();
-    if (p.rare && !any_cut(p))
+    if (p.rare && !any_with(p, 2))
         return;
     const int floats = p.a.dv * p.a.dk, parts = (floats + 1023) / 1024;
     for (long long at = blockIdx.x; at < (long long)p.a.rows * p.a.hv * parts; at += gridDim.x) {
