@@ -44,7 +44,7 @@ struct ChunkArgs {
 // own kernels only the scan reads what another one wrote (the sums), and then the segments that begin with the scan's states:
 // those wait, a sequence of a single segment does not.  Every kernel waits at its end at the latest, so that who comes next
 // has all of them behind it.  One after the other, a sequence of 16,000 tokens (bf16, 16 heads of 128) takes 99.6 us instead of
-// 95.0, five of 200 to 900 in fp32 (8 heads of 64) 39.1 instead of 30.0, 37 of 1 to 9 in bf16 22.9 instead of 21.9.
+// 95.0, five of 200 to 900 in fp32 (8 heads of 64) 39.1 instead of 30.0, 37 of 1 to 9 in bf16 1.0 less.
 __device__ __forceinline__ void begin_chunks()
 {
     __threadfence(); // this SM's L1 may hold lines of a grid before the call
