@@ -65,6 +65,17 @@ def test_one_long_sequence(gdn, dtype):
     c.check(prefill(gdn, c, c.pool(gdn)))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dims", [(1, 2, 64, 64), (1, 1, 128, 128)], ids=str)
+@pytest.mark.parametrize("lens", [[1] * 24 + [300], [30] * 12 + [1700], [3] * 150 + [25, 2000, 0, 21]], ids=["300", "1700", "2000"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_long_sequence_among_short_ones(gdn, dtype, dims, lens, in_place):
+    """The mean, which is all that the host knows, says there are no chunks, or that no sequence is cut."""
+    c = Case(lens, dtype, *dims, pad=[0, 3], seed=5)
+    c.check(prefill(gdn, c, c.pool(gdn), in_place), in_place)
+    assert gdn.get_device_error() == 0
+
+
 def test_decays_at_their_ends(gdn):
     """-inf forgets what came before, 0 and what is above keep all of it."""
     for dtype in ("bf16", "f32"):
