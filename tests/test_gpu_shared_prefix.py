@@ -82,6 +82,17 @@ def test_verification_and_chunks(gdn, dtype, hq, hkv, d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 2, 64), (16, 2, 128), (16, 1, 256)])
+def test_many_tokens_over_a_long_prefix(gdn, dtype, hq, hkv, d):
+    """More tokens and heads than there are places for warps, and items of several parts, own and shared."""
+    c = Forked([(60, [(9, 4), (320, 300), (0, 2), (12, 12)]), (0, [(40, 3)])], dtype, hkv, d, 32, seed=d, poison=float("nan"))
+    q, out = run(gdn, c, hq)
+    assert len(q) * hq > 32 * 152
+    check_attention(out, *attention_ref(c, q, c.new, d ** -0.5), dtype)
+    assert gdn.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_long_prefix_is_divided(gdn, dtype):
     """A shared prefix that every CTA has a part of, and the same with a layer, a scale and given buffers."""
     c = Forked([(1500, [(1, 1), (33, 1), (0, 1), (700, 1)]), (2, [(3, 1)])], dtype, 2, 128, 16, seed=3, layers=2, poison=float("nan"))
