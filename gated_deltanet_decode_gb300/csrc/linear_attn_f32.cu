@@ -15,6 +15,10 @@
 // to 900 tokens (8 heads of 64 x 64, fp32) took 71 us instead of 41, of which
 // the sums took 10, the scan 5 and the outputs 18; with the kernels beside each other 30.
 //
+// Every operand lies in shared memory at half its value: a head is rounded, and rounding would take finite values from 3.402e38
+// on out of the range (their products with the mask's zeros are NaN).  Halves, and the factors of four that make up for them,
+// are exact, but for the last bit of denormal numbers; they cost 1 % (a bound on each operand at its splitting 3 to 9).
+//
 // Bound: latency.  A segment is mostly a single chunk; its loads, five barriers
 // and the products' chains follow each other, with one to two CTAs an SM.
 #include <atomic>
@@ -92,6 +96,8 @@ template <int N> __device__ __forceinline__ void products(const float *a, int ld
                     sum[m][n][e] += t[m][n][e];
     }
 }
+
+__device__ __forceinline__ float4 times(float f, float4 x) { return make_float4(f * x.x, f * x.y, f * x.z, f * x.w); }
 
 // four elements in fp32
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -183,7 +189,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
             for (int x = tid; x < VB * (DK / 4); x += kThreads) {
                 const int v = x / (DK / 4), k = 4 * (x - v * (DK / 4));
                 *reinterpret_cast<float4 *>(sm + G::S + v * LD + k) =
-                    !SUM && v < rows ? load4(from + (size_t)v * DK + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    !SUM && v < rows ? times(0.5f, load4(from + (size_t)v * DK + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
         float total = 1.f;
@@ -204,7 +210,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                 ctl.badfrom[tid] = kC;
             if (tid == 0)
                 ctl.dirty = 0;
-            // K and Q as they are, V transposed; zeros past the end
+            // K and Q in their order, V transposed; zeros past the end
 #pragma unroll 4
             for (int x = tid; x < kC * (DK / 4); x += kThreads) {
                 const int j = x / (DK / 4), k = 4 * (x - j * (DK / 4));
@@ -214,9 +220,9 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                     if (!SUM)
                         z = load4(static_cast<const T *>(a.q) + (tok + j) * a.q_stride + hk * DK + k);
                 }
-                *reinterpret_cast<float4 *>(sm + G::K + j * LD + k) = y;
+                *reinterpret_cast<float4 *>(sm + G::K + j * LD + k) = times(0.5f, y);
                 if (!SUM)
-                    *reinterpret_cast<float4 *>(sm + G::Q + j * LD + k) = z;
+                    *reinterpret_cast<float4 *>(sm + G::Q + j * LD + k) = times(0.5f, z);
             }
             if (warp == 0)
                 chunk_decays(a, (int)tok, n, head, ctl);
@@ -233,7 +239,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                         atomicMin(&ctl.badfrom[v + e], j);
                         ctl.dirty = 1;
                     }
-                    sm[G::V + (v + e) * kLd + j] = z[e];
+                    sm[G::V + (v + e) * kLd + j] = 0.5f * z[e];
                 }
             }
             __syncthreads();
@@ -250,7 +256,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                             for (int e = 0; e < 4; ++e) {
                                 const int r = r0 + 16 * m + g + 8 * (e >> 1), k = k0 + 8 * n2 + 2 * c + (e & 1);
                                 sm[G::P + r * kLd + k] =
-                                    k <= r ? p2[m][n2][e] * exp2f((ctl.hi[r] - ctl.hi[k]) + (ctl.lo[r] - ctl.lo[k])) : 0.f;
+                                    k <= r ? 2.f * p2[m][n2][e] * exp2f((ctl.hi[r] - ctl.hi[k]) + (ctl.lo[r] - ctl.lo[k])) : 0.f;
                             }
                 }
                 float o[2][N][4], own[2][N][4];
@@ -269,7 +275,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                             float x[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                x[e] = fmaf(o[m][n2][2 * h + e], f, own[m][n2][2 * h + e]) * a.scale;
+                                x[e] = 4.f * fmaf(o[m][n2][2 * h + e], f, own[m][n2][2 * h + e]) * a.scale;
                                 if (ctl.dirty && ctl.badfrom[v + e] <= r)
                                     x[e] = __int_as_float(0x7fc00000);
                             }
@@ -307,7 +313,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
                             const int k = x0 + 16 * m + g + 8 * (e >> 1), v = c0 + 8 * n2 + 2 * c + (e & 1);
                             if (DK >= 32 || k < DK) {
                                 float *const s = sm + G::S + v * LD + k;
-                                *s = fmaf(*s, all, y[m][n2][e]) + (ctl.dirty && ctl.badfrom[v] < kC ? __int_as_float(0x7fc00000) : 0.f);
+                                *s = fmaf(*s, all, 2.f * y[m][n2][e]) + (ctl.dirty && ctl.badfrom[v] < kC ? __int_as_float(0x7fc00000) : 0.f);
                             }
                         }
             }
@@ -317,7 +323,7 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
             float *const to = SUM ? p.state + slot * it.at + mine : a.pool + slot * it.ws + mine;
             for (int x = tid; x < rows * (DK / 4); x += kThreads) {
                 const int v = x / (DK / 4), k = 4 * (x - v * (DK / 4));
-                *reinterpret_cast<float4 *>(to + (size_t)v * DK + k) = load4(sm + G::S + v * LD + k);
+                *reinterpret_cast<float4 *>(to + (size_t)v * DK + k) = times(2.f, load4(sm + G::S + v * LD + k));
             }
             if (SUM && v0 == 0 && tid == 0)
                 p.decay[(size_t)it.at * a.hv + head] = total;
