@@ -98,3 +98,33 @@ class Case:
             assert off.max() <= 0, f"state of sequence {r} off by {off.max()} over the bound"
             want[slot] = pool[slot]
         assert torch.equal(pool, want), "a slot that nobody writes changed"
+
+    def check_norm(self, out, scale=None):
+        """Of every sequence of more than 20 tokens and head, the difference's norm over the output's.
+
+        bf16: the weights, the state as a factor, and the output are rounded, each value by at most half a step, which is spread
+        evenly over +- 2^-8 of it at worst, 2^-8 / sqrt(3) = 0.00226 in the mean square.  The terms of an output have random
+        signs, so what the first two give has at most the output's own norm times that: sqrt(2) 0.00226 = 0.0032 in all.  The
+        rest of the limit of 0.004 is for the spread of a norm over some thousands of values.
+        fp32: a product leaves out 2^-22 of a term and a sum of sixteen is cut short by up to 2^-21 of it, an exponential is off by
+        2^-22 and a state's step by 2^-24: 2^-19 with the same random signs."""
+        ref = self.reference(scale)[0]
+        limit = 0.004 if self.dtype == "bf16" else 2.0 ** -19
+        o = out.double().cpu()
+        for r, n in enumerate(self.lens):
+            if n > 20 and r not in self.pad:
+                at = slice(int(self.cu[r]), int(self.cu[r + 1]))
+                off = (o[at] - ref[at]).pow(2).sum((0, 2)).sqrt() / ref[at].pow(2).sum((0, 2)).sqrt()
+                assert off.max() <= limit, f"sequence {r}: off by {off.tolist()} of the outputs' norm"
+
+
+class SlowCase(Case):
+    """A memory of 1,000 to 10,000 tokens, another one a head, and a head that keeps all (every third): the state from before a
+    segment of some hundreds of tokens is most of the one after it."""
+
+    def __init__(self, lens, dtype, hk, hv, dk, dv, fixed=False, seed=0, **k):
+        super().__init__(lens, dtype, hk, hv, dk, dv, fixed=fixed, seed=seed, **k)
+        rate = 10.0 ** (-4 + torch.arange(hv).float() / max(hv - 1, 1))
+        rate[2::3] = 0.0
+        step = torch.ones(hv) if fixed else 0.5 + torch.rand(self.T, hv, generator=torch.Generator().manual_seed(seed + 1))
+        self.decay = -rate * step
