@@ -166,17 +166,20 @@ struct Shared {
         SharedRow x = {};
         if (i < p.ngroups) {
             const int r0 = p.bounds[i], r1 = p.bounds[i + 1];
-            x.bad = r0 < 0 || r1 < r0 || r1 > c.rows;
-            if (x.bad || r0 == r1)
-                return x;
-            const int2 f = p.prefix[r0];
-            const int b = c.cu_seqlens[r0], e = c.cu_seqlens[r1];
-            if (f.y == 0)
-                return x;
-            x.bad = f.x < 0 || f.x >= c.rows || f.y < 0 || f.y > c.max_pages || b < 0 || e < b || e > c.total_tokens;
-            x.live = !x.bad && e > b;
-            if (x.live)
-                x.b = b, x.n = e - b, x.len = f.y * ps, x.row = f.x, x.kind = 1;
+            x.bad = (i == 0 && r0 != 0) || (i == p.ngroups - 1 && r1 != c.rows); // (rows of no group, which does not concern this one)
+            if (r0 < 0 || r1 < r0 || r1 > c.rows)
+                x.bad = true;
+            else if (r0 < r1) {
+                const int2 f = p.prefix[r0];
+                const int b = c.cu_seqlens[r0], e = c.cu_seqlens[r1];
+                if (f.y != 0) {
+                    const bool wrong = f.x < 0 || f.x >= c.rows || f.y < 0 || f.y > c.max_pages || b < 0 || e < b || e > c.total_tokens;
+                    x.bad |= wrong;
+                    x.live = !wrong && e > b;
+                    if (x.live)
+                        x.b = b, x.n = e - b, x.len = f.y * ps, x.row = f.x, x.kind = 1;
+                }
+            }
             return x;
         }
         const int r = i - p.ngroups, pages = p.prefix[r].y;

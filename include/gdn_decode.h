@@ -531,8 +531,11 @@ int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int lay
  * bounds (another is fine that names, alike for every row of a group, a row
  * and a number of its pages that all of the group's live rows begin with).  A
  * row whose pages before its new tokens are fewer than prefix[r][1] gives
- * zeros, with GDN_DEVERR_BAD_PAGE; the outputs of a group whose bounds or
- * prefix are wrong mean nothing, with the same code.  The workspace is
+ * zeros, with GDN_DEVERR_BAD_PAGE.  The outputs of a group mean nothing whose
+ * bounds are wrong, or whose prefix is out of the tables' range or not alike
+ * for its rows: with the same code, but for a prefix that is in range, whose
+ * rows are not compared again.  Bounds that leave rows out have the code too;
+ * such a row's outputs are right where its prefix is (r, 0).  The workspace is
  * paged_attention_shared_workspace_bytes. */
 int kv_pages_shared(const int32_t *table, int rows, int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens,
                     const int32_t *bounds, int groups, int page_size, int32_t *prefix, void *stream);
