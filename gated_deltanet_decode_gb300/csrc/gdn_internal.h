@@ -141,6 +141,8 @@ struct LinearArgs {
     void *out;
     int rows, total_tokens, hk, hv, dk, dv; // rows: of the batch, or sequences
     int most;                               // tokens of the longest sequence that the serial kernel takes
+    int span;                               // the chunked kernels': tokens a segment, whole chunks (linear_divide)
+    bool cut;                               // whether sequences of the mean length have several segments
     int *err;
     void *work;                             // the chunked kernels'
 };
@@ -218,9 +220,11 @@ cudaError_t launch_linear_decode(const LinearArgs &a, int dtype, cudaStream_t s)
 cudaError_t launch_linear_serial(const LinearArgs &a, int dtype, cudaStream_t s);
 // Packed sequences: the short ones by the serial kernel, the others in chunks, bf16 with dk and dv 64 or 128 on the
 // tensor cores (launch_linear_chunked), the rest to fp32's precision.
-size_t linear_prefill_workspace_bytes(const LinearArgs &a, int dtype);
+// linear_divide comes before the others and sets a.span and a.cut from the counts and sizes (of one sequence and token at least).
+void linear_divide(LinearArgs &a, int dtype);
+size_t linear_prefill_workspace_bytes(const LinearArgs &a);
 cudaError_t launch_linear_prefill(LinearArgs a, int dtype, cudaStream_t s);
-size_t linear_chunked_workspace_bytes(const LinearArgs &a);
+int linear_chunked_segment(const LinearArgs &a, bool &cut);
 cudaError_t launch_linear_chunked(const LinearArgs &a, cudaStream_t s);
 
 // Attention layers over a page pool.

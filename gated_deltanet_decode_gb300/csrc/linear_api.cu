@@ -94,7 +94,8 @@ size_t linear_attention_prefill_workspace_bytes(const gdn_pool *pool, int nseq, 
     gdn::LinearArgs a = {};
     a.rows = nseq, a.total_tokens = total_tokens;
     a.hk = pool->dims.hk, a.hv = pool->dims.hv, a.dk = pool->dims.dk, a.dv = pool->dims.dv;
-    return gdn::linear_prefill_workspace_bytes(a, dtype);
+    gdn::linear_divide(a, dtype);
+    return gdn::linear_prefill_workspace_bytes(a);
 }
 
 int linear_attention_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -114,7 +115,9 @@ int linear_attention_prefill(const void *q, int64_t q_stride, const void *k, int
         return api_ok();
     if (!cu_seqlens)
         return api_fail(GDN_EINVAL, "cu_seqlens must be non-NULL");
-    const size_t need = linear_attention_prefill_workspace_bytes(pool, nseq, total_tokens, dtype);
+    if (total_tokens > 0)
+        gdn::linear_divide(a, dtype);
+    const size_t need = total_tokens > 0 ? gdn::linear_prefill_workspace_bytes(a) : 0;
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 127u)))
         return api_fail(GDN_EINVAL, "workspace must be 128-byte aligned and hold %zu bytes (given %zu)", need,
                         workspace ? workspace_bytes : (size_t)0);

@@ -341,15 +341,11 @@ int segment_chunks(const LinearArgs &a, bool &cut)
     const int vb = a.dk == 256 ? FGeo<256>::VB : FGeo<128>::VB, at_once = kSms * (a.dk > 64 ? 1 : 2);
     const long long m = ((long long)a.total_tokens + (long long)a.rows * kC - 1) / ((long long)a.rows * kC); // chunks a sequence
     const long long blocks = (long long)a.rows * a.hv * ((a.dv + vb - 1) / vb);
-    long long best = m;
-    double least = 1e30;
-    for (int cuts = 1; cuts <= m && cuts <= 2 * at_once; ++cuts) {
-        const long long len = (m + cuts - 1) / cuts, segs = (m + len - 1) / len;
-        auto rounds = [&](long long n) { return (double)((n * blocks + at_once - 1) / at_once); };
-        const double cost = rounds(segs) * (len + 0.5) + (segs > 1 ? rounds(segs - 1) * (0.25 * len + 0.5) + 1 : 0);
-        if (cost < least)
-            least = cost, cut = segs > 1, best = len;
-    }
+    auto rounds = [&](long long n) { return (double)((n * blocks + at_once - 1) / at_once); };
+    const long long best = cheapest_length(m, 2 * at_once, [&](long long segs, long long len) {
+        return rounds(segs) * (len + 0.5) + (segs > 1 ? rounds(segs - 1) * (0.25 * len + 0.5) + 1 : 0);
+    });
+    cut = best < m;
     return (int)(best < kMostChunks ? best : kMostChunks);
 }
 
@@ -374,16 +370,14 @@ template <typename T, int DK> cudaError_t go(const LinearArgs &a, cudaStream_t s
     }
     ChunkArgs p;
     p.a = a;
-    bool cut = false;
-    p.span = kC * segment_chunks(a, cut);
-    p.rare = !cut;
+    p.rare = !a.cut;
     p.none = a.total_tokens <= (long long)kSerial * a.rows;
     p.least = kSerial;
     p.heads = a.hv * ((a.dv + G::VB - 1) / G::VB);
     chunk_layout(p);
-    const long long most = places(a.rows, a.total_tokens, p.span) * p.heads; // items
+    const long long most = places(a.rows, a.total_tokens, a.span) * p.heads; // items
     const dim3 grid((unsigned)(most < 8 * kSms ? most : 8 * kSms));
-    if (a.total_tokens > p.span) { // a sequence can have several segments
+    if (a.total_tokens > a.span) { // a sequence can have several segments
         e = launch_pdl(linear_f32_kernel<T, DK, true>, grid, dim3(kThreads), (size_t)BYTES, s, p);
         if (e == cudaSuccess)
             e = launch_scan(p, s);
@@ -415,15 +409,14 @@ bool on_tensor_cores(const LinearArgs &a, int dtype)
 
 } // namespace
 
-size_t linear_prefill_workspace_bytes(const LinearArgs &a, int dtype)
+void linear_divide(LinearArgs &a, int dtype)
 {
-    if (a.total_tokens <= kSerial)
-        return 0;
-    if (on_tensor_cores(a, dtype))
-        return linear_chunked_workspace_bytes(a);
-    bool cut;
-    const long long span = (long long)kC * segment_chunks(a, cut);
-    return a.total_tokens > span ? chunk_bytes(a, span) : 0;
+    a.span = on_tensor_cores(a, dtype) ? linear_chunked_segment(a, a.cut) : kC * segment_chunks(a, a.cut);
+}
+
+size_t linear_prefill_workspace_bytes(const LinearArgs &a)
+{
+    return a.total_tokens > kSerial && a.total_tokens > a.span ? chunk_bytes(a) : 0;
 }
 
 cudaError_t launch_linear_prefill(LinearArgs a, int dtype, cudaStream_t s)

@@ -1007,15 +1007,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 int segment_chunks(int nseq, int tokens, int hv, bool &cut)
 {
     const int m = (int)(((long long)tokens + (long long)nseq * kC - 1) / ((long long)nseq * kC)); // chunks a sequence
-    int best = m;
-    double least = 1e30;
-    for (int cuts = 1; cuts <= m && cuts <= kSms; ++cuts) {
-        const int len = (m + cuts - 1) / cuts, segs = (m + len - 1) / len;
-        auto rounds = [&](long long n) { return (double)((n * nseq * hv + kSms - 1) / kSms); };
-        const double cost = rounds(segs) * (len + 1) + (segs > 1 ? rounds(segs - 1) * (0.5 * len + 1) + 3 : 0);
-        if (cost < least)
-            least = cost, cut = segs > 1, best = cut ? len : 2 * m > 4 ? 2 * m : 4;
-    }
+    auto rounds = [&](long long n) { return (double)((n * nseq * hv + kSms - 1) / kSms); };
+    const int len = (int)cheapest_length(m, kSms, [&](long long segs, long long chunks) {
+        return rounds(segs) * (chunks + 1) + (segs > 1 ? rounds(segs - 1) * (0.5 * chunks + 1) + 3 : 0);
+    });
+    cut = len < m;
+    const int best = cut ? len : 2 * m > 4 ? 2 * m : 4;
     return best < kMostChunks ? best : kMostChunks;
 }
 // [tokens][heads][d] bf16, boxes of 64 d of one head x kC tokens
@@ -1057,16 +1054,14 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     ChunkArgs p;
     p.a = a;
-    bool cut = false;
-    p.span = kC * segment_chunks(a.rows, a.total_tokens, a.hv, cut);
-    p.rare = !cut;
+    p.rare = !a.cut;
     p.none = a.total_tokens <= (long long)kSerial * a.rows;
     p.least = kSerial;
     p.heads = a.hv;
     chunk_layout(p);
-    const long long most = places(a.rows, a.total_tokens, p.span) * a.hv; // items
+    const long long most = places(a.rows, a.total_tokens, a.span) * a.hv; // items
     const dim3 grid((unsigned)(most < kSms ? most : kSms));
-    if (a.total_tokens > p.span) { // a sequence can have several segments
+    if (a.total_tokens > a.span) { // a sequence can have several segments
         e = launch_pdl(linear_sum_kernel<DK, DV>, grid, dim3(kThreads), (size_t)SUM, s, p, kmap, vmap);
         if (e == cudaSuccess)
             e = launch_scan(p, s);
@@ -1078,12 +1073,7 @@ template <int DK, int DV> cudaError_t go(const LinearArgs &a, cudaStream_t s)
 
 } // namespace
 
-size_t linear_chunked_workspace_bytes(const LinearArgs &a)
-{
-    bool cut;
-    const int span = kC * segment_chunks(a.rows, a.total_tokens, a.hv, cut);
-    return a.total_tokens > span ? chunk_bytes(a, span) : 0;
-}
+int linear_chunked_segment(const LinearArgs &a, bool &cut) { return kC * segment_chunks(a.rows, a.total_tokens, a.hv, cut); }
 
 cudaError_t launch_linear_chunked(const LinearArgs &a, cudaStream_t s)
 {

@@ -25,7 +25,6 @@ constexpr int kSerial = 20;
 
 struct ChunkArgs {
     LinearArgs a;
-    int span;     // tokens a segment, whole chunks
     int least;    // sequences of more tokens than this are divided into segments; the others are the serial kernel's
     // Whether the host expects no sequence of several segments.  The sums' kernel and the scan, there for a long sequence among
     // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 92.7 us, without the look 94.5, and 87.4
@@ -68,11 +67,11 @@ __device__ __forceinline__ int segments(const ChunkArgs &p, int r, int &b, int &
     if (classify_seq(rs, ws, p.a.write_slot == nullptr, nullptr, b, e, p.a.total_tokens, p.a.num_slots) != 1)
         return 0;
     n = e - b;
-    return n > p.least ? n / p.span + (n % p.span != 0) : 0;
+    return n > p.least ? n / p.a.span + (n % p.a.span != 0) : 0;
 }
 // The workspace's places of a sequence's segments begin at its first token's
 // place over a segment's length and one a sequence before it, so no two meet.
-__device__ __forceinline__ int first_place(const ChunkArgs &p, int b, int r) { return b / p.span + r; }
+__device__ __forceinline__ int first_place(const ChunkArgs &p, int b, int r) { return b / p.a.span + r; }
 // Whether a sequence has `most` segments or more.  By all threads of a CTA.
 __device__ __forceinline__ bool any_with(const ChunkArgs &p, int most)
 {
@@ -120,7 +119,7 @@ template <bool SUM> struct ItemWalk {
             }
             const int s = (int)((i - done) / p.heads), h = (int)((i - done) - (long long)s * p.heads);
             const int who = __ffs(__ballot_sync(0xffffffffu, upto > s)) - 1;
-            const int seg = s - __shfl_sync(0xffffffffu, upto - segs, who), span = p.span;
+            const int seg = s - __shfl_sync(0xffffffffu, upto - segs, who), span = p.a.span;
             const int wb = __shfl_sync(0xffffffffu, b, who), wn = __shfl_sync(0xffffffffu, n, who);
             const int count = __shfl_sync(0xffffffffu, segs, who) + (SUM ? 1 : 0);
             it.tok = wb + seg * span, it.n = min(span, wn - seg * span), it.head = h;
@@ -210,15 +209,33 @@ inline cudaError_t launch_scan(const ChunkArgs &p, cudaStream_t s)
     return launch_pdl(linear_scan_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s, p);
 }
 
-// The workspace: states, then decays.
-inline size_t chunk_bytes(const LinearArgs &a, long long span)
+// The cheapest of the lengths that m chunks have when cut evenly in up to `most` pieces, each looked at once (about 2 sqrt(m);
+// looking at every number of pieces took 9 us of host time for 40,000 tokens).  cost(segments, length)
+template <typename Cost> long long cheapest_length(long long m, long long most, const Cost &cost)
 {
-    return sizeof(float) * (size_t)places(a.rows, a.total_tokens, span) * a.hv * ((size_t)a.dv * a.dk + 1);
+    long long best = m;
+    double least = 1e30;
+    for (long long cuts = 1; cuts <= m && cuts <= most;) {
+        const long long len = (m + cuts - 1) / cuts;
+        const double c = cost((m + len - 1) / len, len);
+        if (c < least)
+            least = c, best = len;
+        if (len == 1)
+            break;
+        cuts = (m + len - 2) / (len - 1); // the fewest that give a shorter one
+    }
+    return best;
+}
+
+// The workspace: states, then decays.
+inline size_t chunk_bytes(const LinearArgs &a)
+{
+    return sizeof(float) * (size_t)places(a.rows, a.total_tokens, a.span) * a.hv * ((size_t)a.dv * a.dk + 1);
 }
 inline void chunk_layout(ChunkArgs &p)
 {
     p.state = static_cast<float *>(p.a.work);
-    p.decay = p.state + (size_t)places(p.a.rows, p.a.total_tokens, p.span) * p.a.hv * p.a.dv * p.a.dk;
+    p.decay = p.state + (size_t)places(p.a.rows, p.a.total_tokens, p.a.span) * p.a.hv * p.a.dv * p.a.dk;
 }
 
 } // namespace
