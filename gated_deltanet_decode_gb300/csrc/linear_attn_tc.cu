@@ -197,6 +197,50 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
         tma3(dst + c * kC * 128, map, 64 * c, head, tok, bar);
 }
 
+// What both kernels do with a wait of theirs, `wait(barrier, parity)`, by a whole warp that goes on or leaves as one.
+__device__ __forceinline__ void arrive_warp(unsigned long long &b)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(sm_addr(&b));
+    __syncwarp();
+}
+// The queue's items: one warp walks them, and the readers take turn q's.
+template <bool SUM, typename Ctrl, typename Wait> __device__ __forceinline__ void walk_items(const ChunkArgs &p, Ctrl &ctl, const Wait &wait)
+{
+    ItemWalk<SUM> walk(p);
+    bool more = true;
+    for (int q = 0; more; ++q) {
+        LItem x;
+        more = walk.next(x);
+        const int slot = q % kQueue;
+        if (!wait(ctl.b.iempty[slot], (q / kQueue + 1) & 1))
+            break;
+        if (!more)
+            x.n = 0;
+        if (walk.lane == 0) {
+            ctl.item[slot] = x;
+            mbar_arrive(sm_addr(&ctl.b.ifull[slot]));
+        }
+        __syncwarp();
+    }
+}
+template <typename Ctrl, typename Wait> __device__ __forceinline__ bool take_item(Ctrl &ctl, const Wait &wait, int q, LItem &it) // false: no more
+{
+    const int slot = q % kQueue;
+    if (!wait(ctl.b.ifull[slot], (q / kQueue) & 1))
+        return false;
+    it = ctl.item[slot];
+    arrive_warp(ctl.b.iempty[slot]);
+    return it.n > 0;
+}
+// Tensor memory, all of it, by one warp.
+__device__ __forceinline__ void take_tmem(uint32_t &at)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&at)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
 // ---- the outputs, and the states at the sequences' ends ----
 template <int DK, int DV> struct ChunkCtrl {
     Bars b;
@@ -237,10 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_prior_grid();
         return;
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(512) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 0)
+        take_tmem(ctl.tmem);
     if (tid == 64) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
@@ -279,21 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return alive;
     };
     auto wait = [&](unsigned long long &b, uint32_t parity) { return wait_at(bar(b), parity); };
-    auto arrive = [&](unsigned long long &b) { // a warp
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(bar(b));
-        __syncwarp();
-    };
-    // the item of the queue's turn q
-    auto take = [&](int q, LItem &it) {
-        const int slot = q % kQueue;
-        if (!wait(ctl.b.ifull[slot], (q / kQueue) & 1))
-            return false;
-        it = ctl.item[slot];
-        arrive(ctl.b.iempty[slot]);
-        return it.n > 0;
-    };
+    auto arrive = [](unsigned long long &b) { arrive_warp(b); };
+    auto take = [&](int q, LItem &it) { return take_item(ctl, wait, q, it); };
     // tiles: V of even and odd chunks, K of even and odd chunks, Q
     constexpr int TQ = 4;
     auto tile = [&](int t) { return sbase + t * G::TILE; };
@@ -301,23 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     LItem it;
 
     if (warp == 3) {
-        ItemWalk<false> walk(p);
-        for (int q = 0; alive; ++q) {
-            LItem x;
-            const bool more = walk.next(x);
-            const int slot = q % kQueue;
-            if (!wait(ctl.b.iempty[slot], (q / kQueue + 1) & 1))
-                break;
-            if (!more)
-                x.n = 0;
-            if (lane == 0) {
-                ctl.item[slot] = x;
-                mbar_arrive(bar(ctl.b.ifull[slot]));
-            }
-            __syncwarp();
-            if (!more)
-                break;
-        }
+        walk_items<false>(p, ctl, wait);
     } else if (warp == 0) {
         // ---- Q, K and V
         auto load = [&](int t, uint32_t use, const CUtensorMap *map, int blocks, int head, int tok, int bytes) {
@@ -712,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 reinterpret_cast<unsigned short *>(piece(row, v >> 3))[v & 7] = 0x7fff;
                     }
                     before_sync();
-                    arrive(ctl.ofree);                    if (n < kC) { // the last tokens of a sequence: the rows that there are, by this warp itself
+                    arrive(ctl.ofree);
+                    if (n < kC) { // the last tokens of a sequence: the rows that there are, by this warp itself
                         constexpr int P = HV / 8; // pieces of a row
                         bf16 *const out = static_cast<bf16 *>(a.out) + ((size_t)(it.tok + t) * a.hv + it.head) * DV + hb * HV;
                         for (int i = lane; i < 32 * P; i += 32) {
@@ -779,10 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_prior_grid();
         return;
     }
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&ctl.tmem)), "r"(512) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 0)
+        take_tmem(ctl.tmem);
     if (tid == 32) {
         for (int i = 0; i < kQueue; ++i)
             mbar_init(bar(ctl.b.ifull[i]), 1), mbar_init(bar(ctl.b.iempty[i]), kReaders);
@@ -811,20 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return alive;
     };
-    auto arrive = [&](unsigned long long &b) { // a warp
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(bar(b));
-        __syncwarp();
-    };
-    auto take = [&](int q, LItem &it) {
-        const int slot = q % kQueue;
-        if (!wait(ctl.b.ifull[slot], (q / kQueue) & 1))
-            return false;
-        it = ctl.item[slot];
-        arrive(ctl.b.iempty[slot]);
-        return it.n > 0;
-    };
+    auto arrive = [](unsigned long long &b) { arrive_warp(b); };
+    auto take = [&](int q, LItem &it) { return take_item(ctl, wait, q, it); };
     auto tile = [&](int t) { return sbase + t * G::TILE; };
     unsigned ch = 0; // chunks done
     int st = 0;      // the chunk's tiles: V in st, K in STAGES + st, with the phase `turn` of their barriers
@@ -837,23 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     LItem it;
 
     if (warp == 3) {
-        ItemWalk<true> walk(p);
-        for (int q = 0; alive; ++q) {
-            LItem x;
-            const bool more = walk.next(x);
-            const int slot = q % kQueue;
-            if (!wait(ctl.b.iempty[slot], (q / kQueue + 1) & 1))
-                break;
-            if (!more)
-                x.n = 0;
-            if (lane == 0) {
-                ctl.item[slot] = x;
-                mbar_arrive(bar(ctl.b.ifull[slot]));
-            }
-            __syncwarp();
-            if (!more)
-                break;
-        }
+        walk_items<true>(p, ctl, wait);
     } else if (warp == 0) {
         unsigned asked = 0; // chunks whose copies were asked for
         for (int q = 0; take(q, it); ++q) {
