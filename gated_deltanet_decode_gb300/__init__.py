@@ -897,6 +897,9 @@ def paged_attention_shared(q, pool: KVPagePool, table, seq_len, cu_seqlens, boun
                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """paged_attention with the pages that a group's rows share read once for all of them, for rows that were forked.
 
+    It pays from about 512 shared tokens on in bf16 and 2,000 in fp32, with eight rows a group or more; elsewhere
+    paged_attention takes up to 4 us less a call (fp32: up to 10).
+
     bounds [groups + 1] and prefix [rows][2] are kv_pages_shared's (which a step calls once, for all of its layers)."""
     if scale is None:
         scale = pool.d ** -0.5

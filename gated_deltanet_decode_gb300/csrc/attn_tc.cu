@@ -60,7 +60,6 @@
 namespace gdn {
 namespace {
 
-
 constexpr int kQueue = 4;   // items in flight between the walking warp and the others
 constexpr int kMeta = 16;   // key tiles whose valid-row count is kept; over a ring's tiles
 constexpr float kLazy = 8.f;

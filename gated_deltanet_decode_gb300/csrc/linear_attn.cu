@@ -18,9 +18,9 @@
 // Measured: decode of 64 rows (16 heads of 128 x 128, bf16; 118 MB) 20.2 us, 5.9
 // TB/s, 86 % of a plain copy's rate, of 203 (2 and 32 heads, 128 x 64, fp32; 429
 // MB) 66.3 us, 95 %; one row 4.2, a launch's latency.  37 sequences of 1 to 9
-// tokens (8 and 16 heads of 128 x 128, bf16; 80 MB) 20.4 us: the states' loads
-// and stores, 12 at a copy's rate, have the tokens' arithmetic between them
-// (issue slots 58 % busy).
+// tokens (8 and 16 heads of 128 x 128, bf16; 80 MB) 20.5 us in a graph and 21.7
+// called back to back: the states' loads and stores, 12 at a copy's rate, have
+// the tokens' arithmetic between them (issue slots 58 % busy).
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
 #include "gdn_ptx.cuh"

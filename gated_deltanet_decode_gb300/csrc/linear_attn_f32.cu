@@ -13,7 +13,8 @@
 // 2 x 4 blocks of a result of 64 x 64.  In packed FMAs of 4 x 4 results a thread,
 // whose operands' loads took all of shared memory's bandwidth, five sequences of 200
 // to 900 tokens (8 heads of 64 x 64, fp32) took 71 us instead of 41, of which
-// the sums took 10, the scan 5 and the outputs 18; with the kernels beside each other 30.
+// the sums took 10, the scan 5 and the outputs 18; with the kernels beside each other 30.3
+// in a graph, 31.2 called back to back.
 //
 // Every operand lies in shared memory at half its value: a head is rounded, and rounding would take finite values from 3.402e38
 // on out of the range (their products with the mask's zeros are NaN).  Halves, and the factors of four that make up for them,
@@ -334,8 +335,8 @@ template <typename T, int DK, bool SUM> __global__ void __launch_bounds__(kThrea
 
 // Chunks a segment, as in linear_attn_tc.cu: the fewest rounds of CTAs, in chunks, where a segment costs half a chunk's time to
 // begin and a chunk a quarter of its time in the sums.  Against a chunk a segment (several only where that gave 8 x 152 CTAs): a
-// sequence of 16,000 (8 heads of 64) takes 157 us instead of 177, of 4,000 47 instead of 57, 64 of 200 125 instead of 146, 8 of
-// 2,000 with 32 heads of 128 2.1 ms instead of 2.6; 32 of 100 to 900 153 instead of 143.
+// sequence of 16,000 (8 heads of 64) takes 160 us instead of 177, of 4,000 47 instead of 57, 64 of 200 125 instead of 146, 8 of
+// 2,000 with 32 heads of 128 2.2 ms instead of 2.6; 32 of 100 to 900 154 instead of 143.
 int segment_chunks(const LinearArgs &a, bool &cut)
 {
     const int vb = a.dk == 256 ? FGeo<256>::VB : FGeo<128>::VB, at_once = kSms * (a.dk > 64 ? 1 : 2);

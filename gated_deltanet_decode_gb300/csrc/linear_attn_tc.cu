@@ -34,7 +34,7 @@
 // 0.0023 of their norm instead of the 0.0017 of their own rounding, and three
 // products of each would take as long again as all of them.
 //
-// Measured (16 heads of 128 x 128): 8 sequences of 1,500 to 2,600 tokens 92 us,
+// Measured (16 heads of 128 x 128, in a graph): 8 sequences of 1,500 to 2,600 tokens 92.6 us,
 // half of the rate of their bytes; 128 chains of up to 21 chunks on 152 SMs, a
 // chunk 6,700 clocks.  One of 16,000 tokens 95 us: sums 34, scan 5, the segments
 // 62, less what lies beside each other.  Bound: the chain of a chunk, scores,

@@ -27,11 +27,11 @@ struct ChunkArgs {
     LinearArgs a;
     int least;    // sequences of more tokens than this are divided into segments; the others are the serial kernel's
     // Whether the host expects no sequence of several segments.  The sums' kernel and the scan, there for a long sequence among
-    // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 92.7 us, without the look 94.5, and 87.4
-    // without the two kernels; 8 of 300 27.4, 30.6 and 23.7.
+    // short ones, then look for one first: 8 sequences of 1,500 to 2,600 tokens take 92.6 us, without the look 94.5, and 87.4
+    // without the two kernels; 8 of 300 27.7, 30.6 and 23.7.  (Here and below in a graph; called back to back 1 more.)
     int rare;
     // Whether it expects no sequence for the chunks at all, by the mean: their kernel then looks before it sets up.  37
-    // sequences of 1 to 9 tokens take 20.4 us, without the look 22.2, 4 of 12 7.7 and 10.1; with chunks to do it costs 0.5.
+    // sequences of 1 to 9 tokens take 20.5 us, without the look 22.2, 4 of 12 7.7 and 10.1; with chunks to do it costs 0.5.
     int none;
     int heads;    // value heads, or blocks of their rows where a CTA takes less than a head
     float *state; // [segments][hv][dv][dk]: a segment's sum, then the state after it (a sequence's last: the state before all)

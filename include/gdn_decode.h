@@ -415,9 +415,11 @@ int gdn_commit(int32_t *read_slot, int32_t *write_slot, int rows, void *stream);
  * Sequences of up to 20 tokens run token after token; longer ones in chunks,
  * which group the same sums otherwise: the state is right to fp32 in either
  * form; in bf16, with dk and dv 64 or 128, the weights of a chunk's own tokens
- * and the state, as factors of the outputs, are rounded to bf16 once.  A value
- * that is not finite makes what it reaches NaN: outputs of its own sequence
- * (and value column, in v) from its token on, and the state. */
+ * and the state, as factors of the outputs, are rounded to bf16 once (so that
+ * from 3.396e38 on they count as infinite there).  A value that is not finite
+ * makes what it reaches infinite or NaN, in chunks NaN where the rule may have
+ * an infinity: outputs of its own sequence (and value column, in v) from its
+ * token on, and the state. */
 int linear_attention_decode(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const float *log_decay, int decay_per_token, gdn_pool *pool,
                             const int32_t *read_slot, const int32_t *write_slot, float scale, void *out, int rows,
@@ -535,7 +537,10 @@ int paged_attention(const void *q, int64_t q_stride, kv_page_pool *pool, int lay
  * bounds are wrong, or whose prefix is out of the tables' range or not alike
  * for its rows: with the same code, but for a prefix that is in range, whose
  * rows are not compared again.  Bounds that leave rows out have the code too;
- * such a row's outputs are right where its prefix is (r, 0).  The workspace is
+ * such a row's outputs are right where its prefix is (r, 0).  Sharing pays
+ * from about 512 shared tokens on in bf16 and 2,000 in fp32, with eight rows a
+ * group or more; elsewhere paged_attention takes up to 4 us less a call (fp32:
+ * up to 10).  The workspace is
  * paged_attention_shared_workspace_bytes. */
 int kv_pages_shared(const int32_t *table, int rows, int max_pages, const int32_t *seq_len, const int32_t *cu_seqlens,
                     const int32_t *bounds, int groups, int page_size, int32_t *prefix, void *stream);
